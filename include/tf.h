@@ -497,6 +497,94 @@ TF_API tf_status tf_attention_verify(const tf_kv_cache *c, int32_t group, const 
                                      size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
+ * A batch of sequences that continue one prompt.
+ *
+ * The project's own measurements decode several seeded replies of one prompt
+ * (README, the decode tables: 64-token replies, seeds 1234-1238).  These calls
+ * serve such a batch: the prompt's cache entries are shared, and each sequence
+ * keeps a cache of its own for what follows.  Rows are sequence-major: row
+ * b * R + r is row r of sequence b, at position pos[b] + r of that sequence's
+ * own cache.  pos: dev int64 [n_seq], read on the device; pos[b] = -1 marks an
+ * idle sequence (a finished reply), any other value outside [0, max_len - R]
+ * records TF_DEV_BAD_POSITION in ws and is treated as idle: nothing is written
+ * to an idle sequence's cache, and its output rows are zeros.  No output bit of
+ * a row depends on R, on the other rows of the call or on other sequences.
+ * ------------------------------------------------------------------------
+ * tf_kv_batch: n_seq caches of n_kv heads and max_len entries (a positive
+ *   multiple of 256), caller-owned, 16-B aligned.
+ *   TF_KV_BF16: k and v are bf16 [n_seq][n_kv][max_len][128], each sequence in
+ *     tf_kv_cache's layout (a tf_kv_cache is a batch of one); scales unused.
+ *   TF_KV_E4M3: k and v hold one E4M3 code per element, [n_seq][n_kv][max_len][128]
+ *     bytes; k_scale and v_scale one byte s per entry, [n_seq][n_kv][max_len];
+ *     value = code * 2^(s - 127), exact in bf16.  s - 127 is the smallest
+ *     exponent e in [-120, 7] with max|x| <= 448 * 2^e over the entry's 128
+ *     elements; code = x * 2^-e rounded to nearest even, saturating at 448.  s =
+ *     255 marks an entry that held an infinity or NaN: all its elements read
+ *     as NaN.  Element d of an entry is byte
+ *       16 * ((d % 64) / 8) + 8 * (d / 64) + d % 8,
+ *     with the bytes of elements 4i + 1 and 4i + 2 exchanged.
+ * tf_kv_store: entries pos[b] + r of sequence b from rows b * R + r of k_new,
+ *   v_new (dev bf16 [n_seq*R][ld], head j at columns j*128; ld a multiple of 8;
+ *   rows 16-B aligned), R in 1..max_len.  ws: >= 256 B.
+ * tf_kv_load: the reverse: those entries' values as bf16 rows (zeros for idle
+ *   sequences).
+ * tf_qk_norm_rope: one pass over the rows of a fused projection.  x: dev [n_seq*R][ldx],
+ *   fp32 (x_fp32 != 0; ldx a multiple of 4) or bf16 (ldx a multiple of 8), 16-B
+ *   aligned, n_q query heads, then n_k key heads, then n_v value heads of 128
+ *   columns each; y: dev bf16 [n_seq*R][ldy] in the same order (ldy a multiple
+ *   of 8; y may be x itself when x is bf16 and ldx = ldy).  Query and key heads:
+ *     n = x / sqrt(mean(x^2) + eps) * w   (w = q_weight or k_weight, dev bf16
+ *                                          [128], 16-B aligned; both NULL: n = x),
+ *     then elements (d, d + rot_dim/2), d < rot_dim/2, or (2d, 2d + 1) when
+ *     adjacent != 0, turn by the angle of frequency d: (a, b) -> (a cos - b sin,
+ *     b cos + a sin); elements past rot_dim keep n.  rot_dim: a multiple of 8 in
+ *     0..128 (0: no rotation).  Value heads are only rounded.  turns: dev uint64
+ *     [rot_dim/2], 16-B aligned: frequency d in units of 2^-64 turn per position, i.e.
+ *     round(2^64 * f_d / (2 pi)); the angle is (pos[b] + pos_offset + r) *
+ *     turns[d] modulo 2^64, so it is as exact at far positions as at near ones.
+ *     Any int64 position is valid here; there are no idle sequences.
+ * tf_attention_batch: out[row][h*128 + d] (dev bf16 [n_seq*R][ldo], rounded once;
+ *   ldo a multiple of 8, 16-B aligned), R in 1..16 with R * group <= 128, group
+ *   in 1..16 query heads per KV head, q: dev bf16 [n_seq*R][ldq] (query head h
+ *   at columns h*128, ldq a multiple of 8, 16-B aligned).  Row r of sequence b
+ *   attends over entries 0..prefix_len-1 of `prefix` (n_seq = 1, own's n_kv and
+ *   format; may be NULL when prefix_len = 0) and entries 0..pos[b]+r of its own
+ *   cache, the pass's own rows already stored:
+ *     s_t = q . k_t / sqrt(128),  out = sum_t exp(s_t - max s) v_t / sum_t exp(s_t - max s).
+ *   The prefix is read once for the whole batch.  Entries no row attends over
+ *   may hold anything, infinities and NaN included.  n_seq in 1..1024.  ws:
+ *   tf_attention_batch_workspace_bytes of scratch (0: unsupported arguments).
+ */
+#define TF_KV_BF16 0
+#define TF_KV_E4M3 1
+#define TF_MAX_SEQS 1024
+
+typedef struct tf_kv_batch {
+    void *k;
+    void *v;
+    uint8_t *k_scale;
+    uint8_t *v_scale;
+    int32_t n_seq;
+    int32_t n_kv;
+    int32_t max_len;
+    int32_t format;
+} tf_kv_batch;
+
+TF_API tf_status tf_qk_norm_rope(const void *x, int32_t x_fp32, int32_t ldx, int32_t n_seq, int32_t R, int32_t n_q,
+                                 int32_t n_k, int32_t n_v, const uint16_t *q_weight, const uint16_t *k_weight,
+                                 float eps, const uint64_t *turns, int32_t rot_dim, int32_t adjacent,
+                                 const int64_t *pos, int64_t pos_offset, uint16_t *y, int32_t ldy, void *stream);
+TF_API tf_status tf_kv_store(const tf_kv_batch *c, const uint16_t *k_new, const uint16_t *v_new, int32_t ld,
+                             int32_t R, const int64_t *pos, void *ws, size_t ws_bytes, void *stream);
+TF_API tf_status tf_kv_load(const tf_kv_batch *c, const int64_t *pos, int32_t R, uint16_t *k_out, uint16_t *v_out,
+                            int32_t ld, void *ws, size_t ws_bytes, void *stream);
+TF_API size_t tf_attention_batch_workspace_bytes(const tf_kv_batch *own, int32_t group, int32_t R,
+                                                 int32_t prefix_len);
+TF_API tf_status tf_attention_batch(const tf_kv_batch *own, const tf_kv_batch *prefix, int32_t prefix_len,
+                                    int32_t group, const uint16_t *q, int32_t ldq, int32_t R, const int64_t *pos,
+                                    uint16_t *out, int32_t ldo, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
  * Pieces of the synthetic decoder (the steps tf_verify_step chains), public so
  * a caller can compose or check them one layer at a time.
  * ------------------------------------------------------------------------

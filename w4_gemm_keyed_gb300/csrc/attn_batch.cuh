@@ -1,0 +1,23 @@
+// Attention of a batch of sequences over a shared prefix and their own caches:
+// declarations.
+#pragma once
+#include "kv_batch.cuh"
+
+namespace tfk {
+
+struct AttnBatchArgs {
+    KvBatch own, prefix;    // prefix: n_seq = 1; not read when prefix_len == 0
+    int prefix_len;
+    int group, R;
+    const uint16_t *q;      // bf16 [n_seq * R][ldq]
+    int ldq;
+    const int64_t *pos;     // [n_seq]
+    uint16_t *out;          // bf16 [n_seq * R][ldo]
+    int ldo;
+    int *err;
+};
+
+size_t attn_batch_bytes(const KvBatch &own, int prefix_len, int group, int R);
+cudaError_t launch_attn_batch(const AttnBatchArgs &a, cudaStream_t s);
+
+}  // namespace tfk

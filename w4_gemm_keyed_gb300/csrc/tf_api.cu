@@ -1,6 +1,7 @@
 // extern "C" entry points of libtf: argument validation, workspace layout and
 // launch sequencing.  Every step of the verify pass runs in this library's own
-// kernels (w4_gemm.cu, sampler.cu, glue.cu, attention.cu); nothing here computes
+// kernels (w4_gemm.cu, sampler.cu, glue.cu, attention.cu, kv_batch.cu,
+// attn_batch.cu); nothing here computes
 // on the host.
 #include <cmath>
 #include <cstdarg>
@@ -9,6 +10,7 @@
 
 #include "../../include/tf.h"
 #include "attention.cuh"
+#include "attn_batch.cuh"
 #include "glue.cuh"
 #include "sampler.cuh"
 #include "w4_gemm.cuh"
@@ -818,6 +820,170 @@ tf_status tf_attention_verify(const tf_kv_cache *c, int32_t group, const uint16_
     a.ldo = ldo;
     cudaError_t e = launch_attention(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "tf_attention_verify");
+    return ok();
+}
+
+namespace {
+
+KvBatch kv_batch(const tf_kv_batch &c) {
+    return KvBatch{c.k, c.v, c.k_scale, c.v_scale, c.n_seq, c.n_kv, c.max_len, c.format};
+}
+
+tf_status check_batch(const tf_kv_batch *c, const char *name) {
+    if (!c) return fail(TF_ERR_INVALID_ARG, "%s: null KV batch", name);
+    if (c->format != TF_KV_BF16 && c->format != TF_KV_E4M3)
+        return fail(TF_ERR_UNSUPPORTED, "%s: format=%d is neither TF_KV_BF16 nor TF_KV_E4M3", name, c->format);
+    if (c->n_seq < 1 || c->n_seq > TF_MAX_SEQS)
+        return fail(TF_ERR_UNSUPPORTED, "%s: n_seq=%d outside [1, %d]", name, c->n_seq, TF_MAX_SEQS);
+    if (c->n_kv < 1 || c->n_kv > 128) return fail(TF_ERR_UNSUPPORTED, "%s: n_kv=%d outside [1, 128]", name, c->n_kv);
+    if (c->max_len <= 0 || c->max_len % kKvPart)
+        return fail(TF_ERR_UNSUPPORTED, "%s: max_len=%d is not a positive multiple of %d", name, c->max_len, kKvPart);
+    if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16))
+        return fail(TF_ERR_INVALID_ARG, "%s: k, v must be non-null and 16-B aligned", name);
+    if (c->format == TF_KV_E4M3 &&
+        (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16)))
+        return fail(TF_ERR_INVALID_ARG, "%s: E4M3 scales must be non-null and 16-B aligned", name);
+    return TF_OK;
+}
+
+// rows of one tf_kv_store / tf_kv_load call
+tf_status check_kv_rows(const tf_kv_batch *c, int32_t R, const void *k, const void *v, int32_t ld,
+                        const int64_t *pos) {
+    tf_status st = check_batch(c, "KV batch");
+    if (st != TF_OK) return st;
+    if (R < 1 || R > c->max_len) return fail(TF_ERR_INVALID_ARG, "R=%d outside [1, max_len=%d]", R, c->max_len);
+    if ((2LL * c->n_seq * R * c->n_kv + 15) / 16 > 0x7FFFFFFFLL)
+        return fail(TF_ERR_UNSUPPORTED, "n_seq=%d x R=%d x n_kv=%d entries exceed one launch", c->n_seq, R, c->n_kv);
+    if (!k || !v || !pos || !aligned(pos, 8)) return fail(TF_ERR_INVALID_ARG, "null or misaligned k, v or pos");
+    if (!aligned(k, 16) || !aligned(v, 16)) return fail(TF_ERR_INVALID_ARG, "k, v rows not 16-B aligned");
+    if (ld < c->n_kv * kHeadDim || ld % 8)
+        return fail(TF_ERR_INVALID_ARG, "ld=%d must be a multiple of 8 and >= n_kv * 128", ld);
+    return TF_OK;
+}
+
+bool attn_batch_supported(const tf_kv_batch *own, int32_t group, int32_t R, int32_t prefix_len) {
+    return group >= 1 && group <= 16 && R >= 1 && R <= TF_MAX_ROWS && R * group <= 128 && R <= own->max_len &&
+           prefix_len >= 0;
+}
+
+}  // namespace
+
+tf_status tf_qk_norm_rope(const void *x, int32_t x_fp32, int32_t ldx, int32_t n_seq, int32_t R, int32_t n_q,
+                          int32_t n_k, int32_t n_v, const uint16_t *q_weight, const uint16_t *k_weight, float eps,
+                          const uint64_t *turns, int32_t rot_dim, int32_t adjacent, const int64_t *pos,
+                          int64_t pos_offset, uint16_t *y, int32_t ldy, void *stream) {
+    if (n_seq < 1 || R < 1) return fail(TF_ERR_INVALID_ARG, "n_seq=%d and R=%d must be >= 1", n_seq, R);
+    if (n_q < 0 || n_k < 0 || n_v < 0 || n_q > 4096 || n_k > 4096 || n_v > 4096 || n_q + n_k + n_v < 1)
+        return fail(TF_ERR_INVALID_ARG, "bad head counts %d, %d, %d", n_q, n_k, n_v);
+    const int H = n_q + n_k + n_v;
+    if ((long long)n_seq * R * H > 0x7FFFFFFFLL)
+        return fail(TF_ERR_UNSUPPORTED, "n_seq=%d x R=%d rows of %d heads exceed one launch", n_seq, R, H);
+    if (!x || !y || !aligned(x, 16) || !aligned(y, 16))
+        return fail(TF_ERR_INVALID_ARG, "x, y must be non-null and 16-B aligned");
+    if (ldx < H * kHeadDim || ldx % (x_fp32 ? 4 : 8))
+        return fail(TF_ERR_INVALID_ARG, "ldx=%d must be >= %d and keep rows 16-B aligned", ldx, H * kHeadDim);
+    if (ldy < H * kHeadDim || ldy % 8)
+        return fail(TF_ERR_INVALID_ARG, "ldy=%d must be >= %d and a multiple of 8", ldy, H * kHeadDim);
+    if (x == y && (x_fp32 || ldx != ldy))
+        return fail(TF_ERR_INVALID_ARG, "in place needs bf16 x with ldx = ldy");
+    if (!q_weight != !k_weight) return fail(TF_ERR_INVALID_ARG, "q_weight and k_weight must both be given or both NULL");
+    if (q_weight && (!aligned(q_weight, 16) || !aligned(k_weight, 16)))
+        return fail(TF_ERR_INVALID_ARG, "q_weight, k_weight not 16-B aligned");
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(TF_ERR_INVALID_ARG, "bad eps");
+    if (rot_dim < 0 || rot_dim > kHeadDim || rot_dim % 8)
+        return fail(TF_ERR_UNSUPPORTED, "rot_dim=%d is not a multiple of 8 in [0, %d]", rot_dim, kHeadDim);
+    if (rot_dim > 0 && (!turns || !aligned(turns, 16) || !pos || !aligned(pos, 8)))
+        return fail(TF_ERR_INVALID_ARG, "a rotation needs turns (16-B aligned) and pos");
+    QkNormRopeArgs a{};
+    a.x = x;
+    a.x_fp32 = x_fp32 ? 1 : 0;
+    a.ldx = ldx;
+    a.n_seq = n_seq;
+    a.R = R;
+    a.n_q = n_q;
+    a.n_k = n_k;
+    a.n_v = n_v;
+    a.wq = q_weight;
+    a.wk = k_weight;
+    a.eps = eps;
+    a.turns = turns;
+    a.rot = rot_dim;
+    a.adjacent = adjacent ? 1 : 0;
+    a.pos = pos;
+    a.pos_offset = pos_offset;
+    a.y = y;
+    a.ldy = ldy;
+    cudaError_t e = launch_qk_norm_rope(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "tf_qk_norm_rope");
+    return ok();
+}
+
+tf_status tf_kv_store(const tf_kv_batch *c, const uint16_t *k_new, const uint16_t *v_new, int32_t ld, int32_t R,
+                      const int64_t *pos, void *ws, size_t ws_bytes, void *stream) {
+    tf_status st = check_kv_rows(c, R, k_new, v_new, ld, pos);
+    if (st != TF_OK) return st;
+    if ((st = check_ws(ws, ws_bytes, 256)) != TF_OK) return st;
+    cudaError_t e = launch_kv_store(kv_batch(*c), k_new, v_new, ld, R, pos, static_cast<int *>(ws),
+                                    static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "tf_kv_store");
+    return ok();
+}
+
+tf_status tf_kv_load(const tf_kv_batch *c, const int64_t *pos, int32_t R, uint16_t *k_out, uint16_t *v_out,
+                     int32_t ld, void *ws, size_t ws_bytes, void *stream) {
+    tf_status st = check_kv_rows(c, R, k_out, v_out, ld, pos);
+    if (st != TF_OK) return st;
+    if ((st = check_ws(ws, ws_bytes, 256)) != TF_OK) return st;
+    cudaError_t e = launch_kv_load(kv_batch(*c), pos, R, k_out, v_out, ld, static_cast<int *>(ws),
+                                   static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "tf_kv_load");
+    return ok();
+}
+
+size_t tf_attention_batch_workspace_bytes(const tf_kv_batch *own, int32_t group, int32_t R, int32_t prefix_len) {
+    if (!own || own->n_seq < 1 || own->n_seq > TF_MAX_SEQS || own->n_kv < 1 || own->n_kv > 128 || own->max_len <= 0 ||
+        own->max_len % kKvPart || !attn_batch_supported(own, group, R, prefix_len))
+        return 0;
+    return attn_batch_bytes(kv_batch(*own), prefix_len, group, R);
+}
+
+tf_status tf_attention_batch(const tf_kv_batch *own, const tf_kv_batch *prefix, int32_t prefix_len, int32_t group,
+                             const uint16_t *q, int32_t ldq, int32_t R, const int64_t *pos, uint16_t *out,
+                             int32_t ldo, void *ws, size_t ws_bytes, void *stream) {
+    tf_status st = check_batch(own, "own");
+    if (st != TF_OK) return st;
+    if (group < 1 || group > 16) return fail(TF_ERR_UNSUPPORTED, "group=%d outside [1, 16]", group);
+    if (R < 1 || R > TF_MAX_ROWS) return fail(TF_ERR_INVALID_ARG, "R=%d outside [1, %d]", R, TF_MAX_ROWS);
+    if (R * group > 128) return fail(TF_ERR_UNSUPPORTED, "R=%d x group=%d exceeds 128", R, group);
+    if (prefix_len < 0) return fail(TF_ERR_INVALID_ARG, "prefix_len=%d must be >= 0", prefix_len);
+    if (prefix_len > 0) {
+        if ((st = check_batch(prefix, "prefix")) != TF_OK) return st;
+        if (prefix->n_seq != 1 || prefix->n_kv != own->n_kv || prefix->format != own->format)
+            return fail(TF_ERR_INVALID_ARG, "prefix must be one sequence with own's n_kv and format");
+        if (prefix_len > prefix->max_len)
+            return fail(TF_ERR_INVALID_ARG, "prefix_len=%d exceeds the prefix's max_len=%d", prefix_len, prefix->max_len);
+    }
+    const int n_q = own->n_kv * group;
+    if (!q || !pos || !out || !aligned(pos, 8)) return fail(TF_ERR_INVALID_ARG, "null or misaligned q, pos or out");
+    if (!aligned(q, 16) || ldq < n_q * kHeadDim || ldq % 8)
+        return fail(TF_ERR_INVALID_ARG, "q must be 16-B aligned with ldq a multiple of 8 and >= %d", n_q * kHeadDim);
+    if (!aligned(out, 16) || ldo < n_q * kHeadDim || ldo % 8)
+        return fail(TF_ERR_INVALID_ARG, "out must be 16-B aligned with ldo a multiple of 8 and >= %d", n_q * kHeadDim);
+    if ((st = check_ws(ws, ws_bytes, tf_attention_batch_workspace_bytes(own, group, R, prefix_len))) != TF_OK) return st;
+    AttnBatchArgs a{};
+    a.own = kv_batch(*own);
+    if (prefix_len > 0) a.prefix = kv_batch(*prefix);
+    a.prefix_len = prefix_len;
+    a.group = group;
+    a.R = R;
+    a.q = q;
+    a.ldq = ldq;
+    a.pos = pos;
+    a.out = out;
+    a.ldo = ldo;
+    a.err = static_cast<int *>(ws);
+    cudaError_t e = launch_attn_batch(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "tf_attention_batch");
     return ok();
 }
 

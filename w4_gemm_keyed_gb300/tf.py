@@ -9,7 +9,9 @@ no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+from fractions import Fraction
 
 import torch
 
@@ -22,6 +24,9 @@ HEAD_DIM = 128
 TF_OP_LANE_GEMM, TF_OP_KEYED_SAMPLE, TF_OP_ATTENTION = 1, 2, 3
 MAX_ROWS = 16
 MAX_TOP_K = 64
+KV_FORMATS = {"bf16": 0, "e4m3": 1}
+
+_TWO_PI = Fraction("6.28318530717958647692528676655900576839433879875021164194988918461563281257241800")
 
 P = ctypes.c_void_p
 I32 = ctypes.c_int32
@@ -53,6 +58,11 @@ class MoeLayerC(ctypes.Structure):
 
 class KVCacheC(ctypes.Structure):
     _fields_ = [("k", P), ("v", P), ("n_kv", I32), ("max_len", I32)]
+
+
+class KVBatchC(ctypes.Structure):
+    _fields_ = [("k", P), ("v", P), ("k_scale", P), ("v_scale", P), ("n_seq", I32), ("n_kv", I32), ("max_len", I32),
+                ("format", I32)]
 
 
 class ModelC(ctypes.Structure):
@@ -94,6 +104,13 @@ SIGNATURES = [
     ("tf_kv_append", ctypes.c_int, [ctypes.POINTER(KVCacheC), P, P, I32, I32, P, P, SZ, P]),
     ("tf_attention_workspace_bytes", SZ, [ctypes.POINTER(KVCacheC), I32, I32]),
     ("tf_attention_verify", ctypes.c_int, [ctypes.POINTER(KVCacheC), I32, P, I32, I32, P, P, I32, P, SZ, P]),
+    ("tf_qk_norm_rope", ctypes.c_int, [P, I32, I32, I32, I32, I32, I32, I32, P, P, ctypes.c_float, P, I32, I32, P,
+                                       ctypes.c_int64, P, I32, P]),
+    ("tf_kv_store", ctypes.c_int, [ctypes.POINTER(KVBatchC), P, P, I32, I32, P, P, SZ, P]),
+    ("tf_kv_load", ctypes.c_int, [ctypes.POINTER(KVBatchC), P, I32, P, P, I32, P, SZ, P]),
+    ("tf_attention_batch_workspace_bytes", SZ, [ctypes.POINTER(KVBatchC), I32, I32, I32]),
+    ("tf_attention_batch", ctypes.c_int, [ctypes.POINTER(KVBatchC), ctypes.POINTER(KVBatchC), I32, I32, P, I32, I32,
+                                          P, P, I32, P, SZ, P]),
     ("tf_selfcheck_scratch_bytes", SZ, [I32]),
     ("tf_selfcheck_row_invariance", ctypes.c_int, [ctypes.POINTER(W4MatrixC), P, I32, P, SZ, P, SZ, P,
                                                    ctypes.POINTER(I32)]),
@@ -498,6 +515,175 @@ class KVCache:
             ws = workspace(self.workspace_bytes(group, R), device=q.device)
         _check(load().tf_attention_verify(ctypes.byref(self._c), group, _ptr(q), q.stride(0), R, _ptr(pos), _ptr(out),
                                           out.stride(0), _ptr(ws), ws.numel(), _stream(stream)))
+        return out
+
+
+# ---------------------------------------------------------------- a batch of sequences that continue one prompt
+def _bits16(t: torch.Tensor, name: str, cols: int):
+    """t: 2-D bf16 (or int16 bits) with unit inner stride and >= cols columns."""
+    if t.dim() != 2 or t.dtype not in (torch.bfloat16, torch.int16):
+        raise TFError(TF_ERR_INVALID_ARG, f"{name} must be a 2-D bf16 / int16 tensor, got {tuple(t.shape)} {t.dtype}")
+    if t.stride(1) != 1 or t.shape[1] < cols:
+        raise TFError(TF_ERR_INVALID_ARG, f"{name} must have unit inner stride and >= {cols} columns")
+
+
+def _bits16_out(t, name: str, rows: int, cols: int, device):
+    """t, or a new bf16 [rows][cols] tensor when it is None."""
+    if t is None:
+        return torch.empty((rows, cols), dtype=torch.bfloat16, device=device)
+    _bits16(t, name, cols)
+    if t.device != device or t.shape[0] < rows:
+        raise TFError(TF_ERR_INVALID_ARG, f"{name} must hold >= {rows} rows on {device}")
+    return t
+
+
+def _positions(pos: torch.Tensor, device) -> int:
+    if pos.dim() != 1 or pos.dtype != torch.int64 or pos.device != device or not pos.is_contiguous() or not len(pos):
+        raise TFError(TF_ERR_INVALID_ARG, f"pos must be a contiguous 1-D int64 tensor on {device}, one per sequence")
+    return pos.shape[0]
+
+
+def rope_turns(rot_dim: int, theta: float = 10000.0, inv_freq=None, device="cuda") -> torch.Tensor:
+    """Frequencies of a rotation over rot_dim elements for qk_norm_rope: int64 bits of
+    round(2^64 f / 2 pi) per pair, f = theta^(-2d/rot_dim) radians per position, or
+    inv_freq[d] (scaled variants bring their own)."""
+    if rot_dim % 8 or not 0 < rot_dim <= HEAD_DIM:
+        raise TFError(TF_ERR_UNSUPPORTED, f"rot_dim={rot_dim} is not a multiple of 8 in [8, {HEAD_DIM}]")
+    if inv_freq is None:
+        inv_freq = [theta ** (-2.0 * d / rot_dim) for d in range(rot_dim // 2)]
+    inv_freq = [float(f) for f in inv_freq]
+    if len(inv_freq) != rot_dim // 2 or not all(math.isfinite(f) for f in inv_freq):
+        raise TFError(TF_ERR_INVALID_ARG, f"inv_freq must hold {rot_dim // 2} finite frequencies")
+    # 2 pi to 80 digits keeps the quotient's error at the frequency's own rounding
+    units = [round(Fraction(f) / _TWO_PI * 2 ** 64) % 2 ** 64 for f in inv_freq]
+    return torch.tensor([u - 2 ** 64 if u >= 2 ** 63 else u for u in units], dtype=torch.int64, device=device)
+
+
+def qk_norm_rope(x: torch.Tensor, n_q: int, n_kv: int, pos: torch.Tensor, turns: torch.Tensor = None,
+                 q_weight: torch.Tensor = None, k_weight: torch.Tensor = None, eps: float = 1e-6,
+                 adjacent: bool = False, pos_offset: int = 0, n_v: int = None, out: torch.Tensor = None,
+                 stream=None) -> torch.Tensor:
+    """bf16 [rows][(n_q + n_kv + n_v) * 128]: the query and key heads of the projection
+    rows x (fp32, or bf16 / int16 bits) normalised (where weights are given) and turned
+    by their positions (where turns are), the n_v (default n_kv) value heads rounded.
+    Rows are sequence-major, len(rows) / len(pos) per sequence; row r of sequence b
+    turns by position pos[b] + pos_offset + r."""
+    n_v = n_kv if n_v is None else n_v
+    cols = (n_q + n_kv + n_v) * HEAD_DIM
+    if x.dtype == torch.float32:
+        if x.dim() != 2 or x.stride(1) != 1 or x.shape[1] < cols:
+            raise TFError(TF_ERR_INVALID_ARG, f"x must be 2-D with unit inner stride and >= {cols} columns")
+    else:
+        _bits16(x, "x", cols)
+    B = _positions(pos, x.device)
+    rows = x.shape[0]
+    if rows % B or not rows:
+        raise TFError(TF_ERR_INVALID_ARG, f"{rows} rows are not a positive multiple of {B} sequences")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and (w.dtype not in (torch.bfloat16, torch.int16) or w.numel() != HEAD_DIM or
+                              not w.is_contiguous() or w.device != x.device):
+            raise TFError(TF_ERR_INVALID_ARG, f"{name} must be {HEAD_DIM} contiguous bf16 values on {x.device}")
+    rot = 0
+    if turns is not None:
+        if turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous() or turns.device != x.device:
+            raise TFError(TF_ERR_INVALID_ARG, f"turns must be a contiguous 1-D int64 tensor on {x.device}")
+        rot = 2 * turns.shape[0]
+    out = _bits16_out(out, "out", rows, cols, x.device)
+    _check(load().tf_qk_norm_rope(_ptr(x), x.dtype == torch.float32, x.stride(0), B, rows // B, n_q, n_kv, n_v,
+                                  _ptr(q_weight), _ptr(k_weight), eps, _ptr(turns), rot, adjacent, _ptr(pos),
+                                  pos_offset, _ptr(out), out.stride(0), _stream(stream)))
+    return out
+
+
+class KVBatch:
+    """KV caches of n_seq sequences on the device, entries bf16 or E4M3 codes with
+    one power-of-two scale per 128-element vector (layouts in tf.h)."""
+
+    def __init__(self, n_seq: int, n_kv: int, max_len: int, fmt: str = "bf16", device="cuda"):
+        if fmt not in KV_FORMATS:
+            raise TFError(TF_ERR_UNSUPPORTED, f"fmt must be one of {sorted(KV_FORMATS)}, got {fmt!r}")
+        shape = (n_seq, n_kv, max_len, HEAD_DIM)
+        dtype = torch.int16 if fmt == "bf16" else torch.uint8
+        self.k, self.v = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
+        self.k_scale = self.v_scale = None
+        if fmt == "e4m3":
+            self.k_scale, self.v_scale = (torch.zeros(shape[:3], dtype=torch.uint8, device=device) for _ in range(2))
+        self.n_seq, self.n_kv, self.max_len, self.fmt = n_seq, n_kv, max_len, fmt
+        self._bind()
+
+    def _bind(self):
+        self._c = KVBatchC(_ptr(self.k), _ptr(self.v), _ptr(self.k_scale), _ptr(self.v_scale), self.n_seq, self.n_kv,
+                           self.max_len, KV_FORMATS[self.fmt])
+
+    @classmethod
+    def of(cls, cache: KVCache) -> "KVBatch":
+        """A batch of one sequence over the memory of an existing KVCache."""
+        b = cls.__new__(cls)
+        b.k, b.v, b.k_scale, b.v_scale = cache.k[None], cache.v[None], None, None
+        b.n_seq, b.n_kv, b.max_len, b.fmt = 1, cache.n_kv, cache.max_len, "bf16"
+        b._bind()
+        return b
+
+    def _rows(self, n: int) -> int:
+        if n % self.n_seq or not n:
+            raise TFError(TF_ERR_INVALID_ARG, f"{n} rows are not a positive multiple of {self.n_seq} sequences")
+        return n // self.n_seq
+
+    def _pos(self, pos: torch.Tensor):
+        if _positions(pos, self.k.device) != self.n_seq:
+            raise TFError(TF_ERR_INVALID_ARG, f"pos must hold {self.n_seq} positions")
+
+    def store(self, k_new: torch.Tensor, v_new: torch.Tensor, pos: torch.Tensor, ws: torch.Tensor = None, stream=None):
+        """Entries pos[b] + r of sequence b from rows b*R + r of k_new, v_new (bf16
+        [n_seq*R][n_kv*128]); returns the workspace whose status the call sets."""
+        cols = self.n_kv * HEAD_DIM
+        _bits16(k_new, "k_new", cols)
+        _bits16(v_new, "v_new", cols)
+        if k_new.shape[0] != v_new.shape[0] or k_new.stride(0) != v_new.stride(0):
+            raise TFError(TF_ERR_INVALID_ARG, "k_new and v_new must have the same rows and row stride")
+        R = self._rows(k_new.shape[0])
+        self._pos(pos)
+        if ws is None:
+            ws = workspace(256, device=self.k.device)
+        _check(load().tf_kv_store(self._c, _ptr(k_new), _ptr(v_new), k_new.stride(0), R, _ptr(pos), _ptr(ws),
+                                  ws.numel(), _stream(stream)))
+        return ws
+
+    def load(self, pos: torch.Tensor, R: int, k: torch.Tensor = None, v: torch.Tensor = None,
+             ws: torch.Tensor = None, stream=None):
+        """(k, v) bf16 [n_seq*R][n_kv*128]: the values of entries pos[b] + r."""
+        cols = self.n_kv * HEAD_DIM
+        dev = self.k.device
+        self._pos(pos)
+        k = _bits16_out(k, "k", self.n_seq * R, cols, dev)
+        v = _bits16_out(v, "v", self.n_seq * R, cols, dev)
+        if k.stride(0) != v.stride(0):
+            raise TFError(TF_ERR_INVALID_ARG, "k and v must have the same row stride")
+        if ws is None:
+            ws = workspace(256, device=dev)
+        _check(load().tf_kv_load(self._c, _ptr(pos), R, _ptr(k), _ptr(v), k.stride(0), _ptr(ws), ws.numel(),
+                                 _stream(stream)))
+        return k, v
+
+    def attention_workspace_bytes(self, group: int, R: int, prefix_len: int = 0) -> int:
+        return int(load().tf_attention_batch_workspace_bytes(self._c, group, R, prefix_len))
+
+    def attention(self, q: torch.Tensor, group: int, pos: torch.Tensor, prefix: "KVBatch" = None,
+                  prefix_len: int = 0, out: torch.Tensor = None, ws: torch.Tensor = None, stream=None) -> torch.Tensor:
+        """bf16 [n_seq*R][n_kv*group*128]: rows at own positions pos[b] + r attending over
+        entries 0..prefix_len-1 of the one-sequence batch `prefix` and 0..pos[b]+r of
+        their own; idle sequences' rows are zeros."""
+        cols = self.n_kv * group * HEAD_DIM
+        dev = self.k.device
+        _bits16(q, "q", cols)
+        R = self._rows(q.shape[0])
+        self._pos(pos)
+        out = _bits16_out(out, "out", q.shape[0], cols, dev)
+        if ws is None:
+            ws = workspace(self.attention_workspace_bytes(group, R, prefix_len), device=dev)
+        _check(load().tf_attention_batch(self._c, prefix._c if prefix is not None else None, prefix_len, group, _ptr(q),
+                                         q.stride(0), R, _ptr(pos), _ptr(out), out.stride(0), _ptr(ws), ws.numel(),
+                                         _stream(stream)))
         return out
 
 
