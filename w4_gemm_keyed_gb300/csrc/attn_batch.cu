@@ -3,84 +3,967 @@
 // Row r of sequence b (position pos[b] + r of its own cache) attends over the
 // shared prefix's entries 0 .. P - 1 and its own entries 0 .. pos[b] + r:
 //   s_t = q . k_t / sqrt(128),  o = sum_t e^(s_t - m) v_t / sum_t e^(s_t - m).
-// One warp takes one query vector and walks its keys in ascending order with a
-// running maximum m, weight sum l and output o in fp32.
+//
+// Keys are cut into parts: the prefix into parts of a length that depends on P
+// and the number of KV heads only, each sequence's own entries into parts of
+// kOwnPart.  An item is one part of one KV head with the query vectors that
+// read it: for a prefix part, up to 256 of the batch's n_seq * R * group vectors
+// (the prefix is read once for all of them, from HBM once and from L2 for the
+// rest), for an own part the sequence's R * group.  Within an item each vector
+// folds its keys in ascending order, 128 at a time, with a running maximum; the
+// parts' results (maximum m, weight sum l, unnormalised output o, fp32) are
+// joined per vector in ascending order by a second kernel.  So a row's bits
+// depend on its query, its position, P and the entries it sees alone:
+// matrix-product rows never mix, and keys past a row's last add exact zeros.
+//
+// Scores and outputs run on tcgen05 with 128 query vectors as M: S = Q K^T with
+// both operands in shared memory and S in tensor memory, then P (bf16, in place
+// of S) times V with P read from tensor memory.  With 8 vectors in a tile of 128
+// an SM still takes a 128-key tile in about 1,100 cycles where HBM delivers it in
+// 2,800, so few rows need no form of their own.
+#include <atomic>
+
+#include <cuda.h>
+
 #include "attn_batch.cuh"
+#include "tf_tcgen05.cuh"
+#include "w4_gemm.cuh"
 
 namespace tfk {
 
 namespace {
 
-constexpr float kLog2eOverSqrtD = 0.12751743074439720f;   // log2(e) / sqrt(128)
+constexpr float kScaleLog2 = 0.12751743074439720f;   // log2(e) / sqrt(128)
+// A vector's reference maximum moves only when a score passes it by more than
+// 2^8 in weight: weights stay below 2^8 (exact in the sums' exponents), and the
+// output is rescaled rarely.  The decision is the vector's own.
+constexpr float kMaxSlack = 8.0f / kScaleLog2;
 
-__device__ __forceinline__ float4 entry4(const KvBatch &c, int which, size_t entry, long long t, int lane) {
-    uint32_t lo, hi;
-    if (c.format == kKvE4m3) {
-        const uint8_t *p = static_cast<const uint8_t *>(which ? c.v : c.k) + entry * kHeadDim + e4m3_byte(4 * lane);
-        e4m3_expand(*reinterpret_cast<const uint32_t *>(p), e4m3_factor((which ? c.v_scale : c.k_scale)[entry]), lo, hi);
-    } else {
-        const uint16_t *p = static_cast<const uint16_t *>(which ? c.v : c.k) + entry * kHeadDim +
-                            (((lane >> 1) ^ int(t & 7)) << 3) + 4 * (lane & 1);
-        const uint2 w = *reinterpret_cast<const uint2 *>(p);
-        lo = w.x;
-        hi = w.y;
-    }
-    return make_float4(__uint_as_float(lo << 16), __uint_as_float(lo & 0xFFFF0000u), __uint_as_float(hi << 16),
-                       __uint_as_float(hi & 0xFFFF0000u));
+constexpr int kTile = 128;              // query vectors and keys per matrix product
+constexpr int kOwnPart = 512;           // own entries per part
+constexpr int kMinPrefixPart = 1024;    // shared entries per part, at least
+constexpr int kHalfBytes = kTile * 128; // 64 elements of 128 rows
+constexpr int kTileBytes = 2 * kHalfBytes;
+constexpr int kRing = 4;                // items known ahead
+constexpr int kGroups = 256;            // entries of the table of own parts
+constexpr int kSoftmaxWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kQueryWarp = 10, kQueryWarps = 2;
+constexpr int kExpandWarp = 12, kExpandWarps = 4;
+
+// What the cache's format changes: an E4M3 tile (16 KB and 128 scale bytes) is
+// copied into a raw stage and expanded by four more warps into a bf16 tile, so
+// the products are those of a bf16 cache holding the same values.
+template <bool E4M3>
+struct Form {
+    static constexpr int stages = E4M3 ? 3 : 5;         // bf16 K and V tiles in shared memory
+    static constexpr int raw = E4M3 ? 4 : 0;            // E4M3 tiles on their way
+    static constexpr int threads = E4M3 ? 512 : 384;
+    static constexpr int readers = kSoftmaxWarps + 1 + kQueryWarps + (E4M3 ? kExpandWarps : 0);  // of the item ring
+    // registers a thread: the softmax warps' and the others', together no more
+    // than the launch's share (128 a thread of 512, 168 of 384)
+    static constexpr int regs_softmax = E4M3 ? 184 : 208, regs_other = E4M3 ? 72 : 88;
+    static_assert(256 * regs_softmax + (threads - 256) * regs_other <= threads * (E4M3 ? 128 : 168), "register split");
+};
+constexpr int kRawBytes = kTile * kHeadDim;
+constexpr uint32_t kTmemCols = 512, kTmemS = 0, kTmemO = 256;
+
+struct Item {
+    int n_vec;          // query vectors (0: no more items)
+    int n_keys;         // entries of the part
+    int j, b;           // KV head, sequence (-1: prefix)
+    int vec0;           // first vector: (row * group + head) within KV head j
+    int key0;           // first entry
+    int lim0;           // part entry index of row 0's last visible entry (own), n_keys - 1 (prefix)
+    int stride;         // vectors per column quad of the partial output
+    long long part;     // index of the part's first (vector, column quad 0) in opart / 32, and in ml
+};
+
+// Prefix partials: [part][n_kv][tiles][32 quads][128 vectors][4]; own partials:
+// [part][n_seq][n_kv][32 quads][R * group][4].  Maxima and sums: the same
+// without the quads.  Quad-major so that a warp's 32 vectors store and load 512
+// consecutive bytes.
+struct Plan {
+    int n_vec, tiles, pairs;    // vectors, 128-vector tiles and pairs of them per KV head
+    int part, n_parts;          // prefix part length and count
+    int own_parts_max;
+    long long own0;             // index of the first own vector slot after the prefix's
+    long long slots;            // vector slots in all
+};
+
+__host__ __device__ inline int prefix_part(int prefix_len, int n_kv) {
+    // as many parts as make one item per SM when the batch is a single tile, but
+    // none shorter than kMinPrefixPart (joining parts costs traffic)
+    constexpr int kSms = 152;
+    const long long even = ((long long)prefix_len * n_kv + kSms - 1) / kSms;
+    const long long part = (even + kTile - 1) / kTile * kTile;
+    return int(part < kMinPrefixPart ? kMinPrefixPart : part);
 }
 
-__global__ void __launch_bounds__(128) attn_batch_kernel(AttnBatchArgs a) {
-    grid_dependency_wait();     // queries and entries come from the preceding grids
-    grid_launch_dependents();
-    const int n_q = a.own.n_kv * a.group, lane = threadIdx.x & 31;
-    const long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (item >= (long long)a.own.n_seq * a.R * n_q) return;
-    const int h = int(item % n_q), j = h / a.group;
-    const long long row = item / n_q;
-    const int b = int(row / a.R), r = int(row % a.R);
-    const long long p = seq_position(a.pos, b, a.R, a.own.max_len, a.err, lane == 0);
-    uint2 *out = reinterpret_cast<uint2 *>(a.out + (size_t)row * a.ldo + (size_t)h * kHeadDim) + lane;
-    if (p < 0) {
-        *out = make_uint2(0u, 0u);
-        return;
+Plan plan_of(const KvBatch &own, int prefix_len, int group, int R) {
+    Plan p;
+    p.n_vec = own.n_seq * R * group;
+    p.tiles = (p.n_vec + kTile - 1) / kTile;
+    p.pairs = (p.tiles + 1) / 2;
+    p.part = prefix_part(prefix_len, own.n_kv);
+    p.n_parts = (prefix_len + p.part - 1) / p.part;
+    p.own_parts_max = (own.max_len + kOwnPart - 1) / kOwnPart;
+    p.own0 = (long long)p.n_parts * own.n_kv * p.tiles * kTile;
+    p.slots = p.own0 + (long long)p.own_parts_max * own.n_kv * p.n_vec;
+    return p;
+}
+
+struct KernelArgs {
+    CUtensorMap map[4];     // prefix K, V; own K, V
+    AttnBatchArgs a;
+    Plan p;
+    float *opart;           // [slots][128]
+    float2 *ml;             // [slots]: (maximum score, weight sum)
+    unsigned *next;         // items taken beyond the first of each CTA; zero between calls
+};
+
+// A parity wait tells a phase from its neighbours only, so whoever waits on a
+// barrier waits on every one of its phases, and before the next can end.  Hence three barriers for scores:
+// S0 and S1 of one-tile items and S0 of two-tile items are read by the first
+// softmax group (0, 1, 0), S1 of two-tile items by the second (2).
+struct __align__(16) Shared {
+    uint64_t kv_full[5], kv_empty[5], raw_full[4], raw_empty[4];
+    uint64_t q_full[2], q_empty[2], s_full[3], p_full[2], o_done[2];
+    uint64_t item_full[kRing], item_empty[kRing], drain;
+    Item item[kRing];
+    int before[kGroups + 1];    // own parts of the sequence groups before each
+    uint32_t tmem;
+    int abort;
+};
+// query tiles, bf16 stages, raw stages, their scales, then Shared
+template <bool E4M3>
+constexpr size_t kSmemBytes = size_t(2 + Form<E4M3>::stages) * kTileBytes + size_t(Form<E4M3>::raw) * (kRawBytes + kTile) +
+                              sizeof(Shared);
+static_assert(kSmemBytes<false> <= 227 * 1024 && kSmemBytes<true> <= 227 * 1024, "shared memory");
+
+template <int N>
+__device__ __forceinline__ void regs_raise() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_lower() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// A wait that gives up after kWaitNs, or once any other role of the CTA has.
+constexpr unsigned long long kWaitNs = 2000000000ull;
+
+__device__ __forceinline__ unsigned long long now_ns() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
+
+__device__ __forceinline__ bool wait_slow(Shared *sh, uint64_t *bar, uint32_t parity, int *err) {
+    const unsigned long long t0 = now_ns();
+    do {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*reinterpret_cast<volatile int *>(&sh->abort)) return false;
+    } while (now_ns() - t0 < kWaitNs);
+    set_error(err, kDevTimeout);
+    *reinterpret_cast<volatile int *>(&sh->abort) = 1;
+    return false;
+}
+
+__device__ __forceinline__ bool wait_or_abort(Shared *sh, uint64_t *bar, uint32_t parity, int *err) {
+    return mbar_try_wait(bar, parity) || mbar_try_wait(bar, parity) || wait_slow(sh, bar, parity, err);
+}
+
+// The same without a report, for what is still in flight when a role ends.
+__device__ __forceinline__ void wait_drained(uint64_t *bar, uint32_t parity) {
+    const unsigned long long t0 = now_ns();
+    while (!mbar_try_wait(bar, parity) && now_ns() - t0 < kWaitNs) {
     }
-    const uint2 qw = *(reinterpret_cast<const uint2 *>(a.q + (size_t)row * a.ldq + (size_t)h * kHeadDim) + lane);
-    const float4 q = make_float4(__uint_as_float(qw.x << 16), __uint_as_float(qw.x & 0xFFFF0000u),
-                                 __uint_as_float(qw.y << 16), __uint_as_float(qw.y & 0xFFFF0000u));
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto walk = [&](const KvBatch &c, size_t base, long long n) {
-        for (long long t = 0; t < n; ++t) {
-            const float4 k = entry4(c, 0, base + t, t, lane);
-            float s = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, q.w * k.w)));
-#pragma unroll
-            for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, i);
-            s *= kLog2eOverSqrtD;
-            const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn;
-            const float scale = exp2f(m - ref), w = exp2f(s - ref);
-            const float4 v = entry4(c, 1, base + t, t, lane);
-            l = fmaf(l, scale, w);
-            o.x = fmaf(o.x, scale, w * v.x);
-            o.y = fmaf(o.y, scale, w * v.y);
-            o.z = fmaf(o.z, scale, w * v.z);
-            o.w = fmaf(o.w, scale, w * v.w);
-            m = mn;
+}
+
+// K and V tiles are taken in the order K0 K1 V0 K2 V1 ... V(n-1) of each item.
+__device__ __forceinline__ int k_order(int i) { return i == 0 ? 0 : 2 * i - 1; }
+__device__ __forceinline__ int v_order(int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; }
+// The tile at place t of that order: whether it is a V tile, and which.
+__device__ __forceinline__ bool order_is_v(int t, int n) { return t == 2 * n - 1 || (t != 0 && t % 2 == 0); }
+__device__ __forceinline__ int order_tile(int t, int n) {
+    return t == 2 * n - 1 ? n - 1 : (t == 0 ? 0 : (t % 2 == 0 ? t / 2 - 1 : (t + 1) / 2));
+}
+
+__device__ __forceinline__ bool bf16x2_nonfinite(uint32_t w) {
+    return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+__device__ __forceinline__ uint32_t bf16x2_finite(uint32_t w) {   // non-finite halves -> 0
+    if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+    if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
+    return w;
+}
+
+// ------------------------------------------------------------------ item order
+// Prefix items first (the longest), vector pairs fastest so that the CTAs working
+// on one part read it from L2; then own items, heads fastest.
+__device__ int own_parts(const KernelArgs &k, int b, bool report) {
+    const long long p = seq_position(k.a.pos, b, k.a.R, k.a.own.max_len, k.a.err, report);
+    return p < 0 ? 0 : int((p + k.a.R - 1) / kOwnPart) + 1;
+}
+
+__device__ Item item_of(const KernelArgs &k, const Shared *sh, long long i, int group_seqs) {
+    Item it{};
+    const int n_kv = k.a.own.n_kv, rg = k.a.R * k.a.group;
+    const long long n_prefix = (long long)k.p.n_parts * n_kv * k.p.pairs;
+    if (i < n_prefix) {
+        const int pair = int(i % k.p.pairs), cj = int(i / k.p.pairs), c = cj / n_kv;
+        it.j = cj % n_kv;
+        it.b = -1;
+        it.vec0 = pair * 2 * kTile;
+        it.n_vec = min(2 * kTile, k.p.n_vec - it.vec0);
+        it.key0 = c * k.p.part;
+        it.n_keys = min(k.p.part, k.a.prefix_len - it.key0);
+        it.lim0 = it.n_keys - 1;
+        it.stride = kTile;
+        it.part = ((long long)cj * k.p.tiles + 2 * pair) * kTile;
+        return it;
+    }
+    i -= n_prefix;
+    const int n_groups = (k.a.own.n_seq + group_seqs - 1) / group_seqs;
+    if (i >= (long long)sh->before[n_groups] * n_kv) return it;
+    int u = int(i / n_kv);
+    it.j = int(i % n_kv);
+    int lo = 0, hi = n_groups - 1;      // last group whose parts start at or before u
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (sh->before[mid] <= u)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    u -= sh->before[lo];
+    int b = lo * group_seqs;
+    for (int n; u >= (n = own_parts(k, b, false)); ++b) u -= n;
+    const long long p = k.a.pos[b];
+    it.b = b;
+    it.vec0 = b * rg;
+    it.n_vec = rg;
+    it.key0 = u * kOwnPart;
+    it.n_keys = int(min((long long)kOwnPart, p + k.a.R - it.key0));
+    it.lim0 = int(p - it.key0);
+    it.stride = rg;
+    it.part = k.p.own0 + (((long long)u * k.a.own.n_seq + b) * n_kv + it.j) * rg;
+    return it;
+}
+
+// ------------------------------------------------------------------ roles
+// One CTA per SM takes items from a common counter.
+//   warp 8      finds the next item and streams its K and V tiles by TMA
+//   warps 10-11 gather the item's query vectors
+//   warp 9      issues the products
+//   warps 12-15 expand E4M3 tiles (there alone)
+//   warps 0-7   softmax: a thread per vector.  Items of two tiles give one tile to
+//               each group of four warps; items of one tile use the second tile's
+//               S columns so that the next key tile's scores are computed
+//               while this one's are being exponentiated.
+
+template <bool E4M3>
+__device__ void produce(const KernelArgs &k, Shared *sh, uint8_t *stages) {
+    constexpr int kStages = E4M3 ? Form<E4M3>::raw : Form<E4M3>::stages;
+    uint64_t *const full = E4M3 ? sh->raw_full : sh->kv_full, *const empty = E4M3 ? sh->raw_empty : sh->kv_empty;
+    const int lane = threadIdx.x & 31, n_seq = k.a.own.n_seq;
+    const int group_seqs = (n_seq + kGroups - 1) / kGroups;
+    const int n_groups = (n_seq + group_seqs - 1) / group_seqs;
+    int total = 0;
+    for (int g0 = 0; g0 < n_groups; g0 += 32) {
+        int n = 0;
+        for (int b = (g0 + lane) * group_seqs; b < min(n_seq, (g0 + lane + 1) * group_seqs); ++b)
+            n += own_parts(k, b, blockIdx.x == 0);
+        int sum = n;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            if (lane >= o) sum += t;
         }
+        if (g0 + lane < n_groups) sh->before[g0 + lane] = total + sum - n;
+        total += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    }
+    if (lane == 0) sh->before[n_groups] = total;
+    __syncwarp();
+    if (lane != 0) return;
+
+    long long i = blockIdx.x;
+    unsigned loaded = 0;     // tiles so far
+    for (unsigned n = 0;; ++n) {
+        const int slot = n % kRing;
+        if (n >= kRing && !wait_or_abort(sh, &sh->item_empty[slot], (n / kRing - 1) & 1, k.a.err)) break;
+        const unsigned taken = atomicAdd(k.next, 1u);       // the item after this one
+        const Item it = item_of(k, sh, i, group_seqs);
+        sh->item[slot] = it;
+        mbar_arrive(&sh->item_full[slot]);
+        if (it.n_vec == 0) break;
+        const bool own = it.b >= 0;
+        const int tiles = (it.n_keys + kTile - 1) / kTile, outer = own ? it.b * k.a.own.n_kv + it.j : it.j;
+        const void *map_k = &k.map[own ? 2 : 0], *map_v = &k.map[own ? 3 : 1];
+        bool ok = true;
+        for (int t = 0; t < 2 * tiles && ok; ++t, ++loaded) {
+            const bool is_v = order_is_v(t, tiles);
+            const int row = it.key0 + order_tile(t, tiles) * kTile;
+            const int st = loaded % kStages;
+            if (loaded >= kStages) ok = wait_or_abort(sh, &empty[st], (loaded / kStages - 1) & 1, k.a.err);
+            if (!ok) break;
+            if constexpr (E4M3) {
+                const KvBatch &c = own ? k.a.own : k.a.prefix;
+                const uint32_t rows = uint32_t(min(kTile, it.key0 + it.n_keys - row)), scales = (rows + 15u) & ~15u;
+                const size_t entry = (size_t)outer * c.max_len + (size_t)row;
+                uint8_t *dst = stages + size_t(st) * kRawBytes;
+                mbar_arrive_expect_tx(&full[st], rows * kHeadDim + scales);
+                bulk_g2s(dst, static_cast<const uint8_t *>(is_v ? c.v : c.k) + entry * kHeadDim, rows * kHeadDim, &full[st]);
+                bulk_g2s(stages + size_t(kStages) * kRawBytes + st * kTile, (is_v ? c.v_scale : c.k_scale) + entry, scales,
+                         &full[st]);
+            } else {
+                uint8_t *dst = stages + size_t(st) * kTileBytes;
+                mbar_arrive_expect_tx(&full[st], kTileBytes);
+                tma_load_3d(dst, is_v ? map_v : map_k, 0, row, outer, &full[st]);
+                tma_load_3d(dst + kHalfBytes, is_v ? map_v : map_k, 64, row, outer, &full[st]);
+            }
+        }
+        if (!ok) break;
+        i = (long long)gridDim.x + taken;
+    }
+    // no copy outlives the CTA
+    for (unsigned t = loaded > kStages ? loaded - kStages : 0; t < loaded; ++t)
+        wait_drained(&full[t % kStages], (t / kStages) & 1);
+}
+
+// E4M3 tiles -> bf16 tiles, eight lanes an entry.  Rows of a V tile past the
+// part's last entry become zeros up to the 16-row step the product reads, and so
+// do entries marked NaN that some rows do not see (0 * NaN would reach those
+// rows; the rows that see them get the NaN back when the output is stored).
+__device__ void expand_tiles(const KernelArgs &k, Shared *sh, uint8_t *stages, const uint8_t *raw) {
+    constexpr int kStages = Form<true>::stages, kRaw = Form<true>::raw;
+    const int lane = threadIdx.x & 31, tid = threadIdx.x - 32 * kExpandWarp, group = tid & 7;
+    const uint8_t *scales = raw + size_t(kRaw) * kRawBytes;
+    unsigned done = 0;
+    for (unsigned n = 0;; ++n) {
+        const int slot = n % kRing;
+        if (!wait_or_abort(sh, &sh->item_full[slot], (n / kRing) & 1, k.a.err)) return;
+        const Item it = sh->item[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
+        if (it.n_vec == 0) return;
+        const int tiles = (it.n_keys + kTile - 1) / kTile;
+        for (int t = 0; t < 2 * tiles; ++t, ++done) {
+            const bool is_v = order_is_v(t, tiles);
+            const int key = order_tile(t, tiles) * kTile, valid = min(kTile, it.n_keys - key);
+            const int fill = is_v ? (valid + 15) & ~15 : valid, hidden = it.lim0 + 1 - key;
+            const int rs = done % kRaw, st = done % kStages;
+            if (!wait_or_abort(sh, &sh->raw_full[rs], (done / kRaw) & 1, k.a.err)) return;
+            if (done >= kStages && !wait_or_abort(sh, &sh->kv_empty[st], (done / kStages - 1) & 1, k.a.err)) return;
+            const uint8_t *src = raw + size_t(rs) * kRawBytes + 16 * group, *sc = scales + rs * kTile;
+            uint8_t *dst = stages + size_t(st) * kTileBytes;
+#pragma unroll 4
+            for (int row = tid >> 3; row < fill; row += 4 * kExpandWarps) {
+                uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+                const uint32_t sb = row < valid ? sc[row] : uint32_t(kScaleNan);
+                if (row < valid && !(is_v && sb == uint32_t(kScaleNan) && row >= hidden)) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(src + row * kHeadDim);
+                    const uint32_t f = e4m3_factor(sb);
+                    e4m3_expand(w.x, f, lo.x, lo.y);
+                    e4m3_expand(w.y, f, lo.z, lo.w);
+                    e4m3_expand(w.z, f, hi.x, hi.y);
+                    e4m3_expand(w.w, f, hi.z, hi.w);
+                }
+                uint8_t *p = dst + row * 128 + ((group ^ (row & 7)) << 4);
+                *reinterpret_cast<uint4 *>(p) = lo;
+                *reinterpret_cast<uint4 *>(p + kHalfBytes) = hi;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sh->kv_full[st]);
+                mbar_arrive(&sh->raw_empty[rs]);
+            }
+        }
+    }
+}
+
+// Queries of vector v: row v / group, columns (j * group + v % group) * 128, into
+// the swizzled K-major tile; tiles are filled to a multiple of 32 vectors.
+__device__ void gather_queries(const KernelArgs &k, Shared *sh, uint8_t *tiles) {
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kQueryWarp;
+    const int chunk = lane & 15, g = k.a.group;
+    unsigned uses[2] = {0, 0};
+    int next = 0;
+    for (unsigned n = 0;; ++n) {
+        const int slot = n % kRing;
+        if (!wait_or_abort(sh, &sh->item_full[slot], (n / kRing) & 1, k.a.err)) return;
+        const Item it = sh->item[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
+        if (it.n_vec == 0) return;
+        const bool two = it.n_vec > kTile;
+        for (int t = 0; t < (two ? 2 : 1); ++t) {
+            const int buf = two ? t : next;
+            if (uses[buf] > 0 && !wait_or_abort(sh, &sh->q_empty[buf], (uses[buf] - 1) & 1, k.a.err)) return;
+            ++uses[buf];
+            const int n_vec = min(kTile, it.n_vec - t * kTile), fill = (n_vec + 31) & ~31;
+            uint8_t *dst = tiles + buf * kTileBytes + (chunk >> 3) * kHalfBytes;
+            const uint16_t *src = k.a.q + (size_t)it.j * g * kHeadDim + chunk * 8;
+            for (int v0 = 2 * w + (lane >> 4); v0 < fill; v0 += 8 * 2 * kQueryWarps) {
+                uint4 x[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int v = v0 + u * 2 * kQueryWarps;
+                    x[u] = make_uint4(0u, 0u, 0u, 0u);
+                    if (v < n_vec) {
+                        const int gv = it.vec0 + t * kTile + v, row = gv / g;
+                        x[u] = *reinterpret_cast<const uint4 *>(src + (size_t)row * k.a.ldq + (gv - row * g) * kHeadDim);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int v = v0 + u * 2 * kQueryWarps;
+                    if (v < fill)
+                        *reinterpret_cast<uint4 *>(dst + v * 128 + (((chunk & 7) ^ (v & 7)) << 4)) = x[u];
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->q_full[buf]);
+        }
+        if (!two) next ^= 1;
+    }
+}
+
+// The last V tiles of an own part: rows past the sequence's last entry become
+// zeros (up to the 16-row step the product reads), and non-finite elements of
+// entries that some rows do not see become zero, since 0 * inf would reach
+// those rows; the rows that see them get them back when the output is stored.
+__device__ __forceinline__ void mend_values(uint8_t *v, int first_hidden, int valid, int lane) {
+    const int end = (valid + 15) & ~15;
+    for (int i = first_hidden * 16 + lane; i < end * 16; i += 32) {
+        const int row = i >> 4, c = i & 15;
+        uint4 *p = reinterpret_cast<uint4 *>(v + (c >> 3) * kHalfBytes + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+        if (row >= valid) {
+            *p = make_uint4(0u, 0u, 0u, 0u);
+        } else {
+            const uint4 x = *p;
+            if (bf16x2_nonfinite(x.x) || bf16x2_nonfinite(x.y) || bf16x2_nonfinite(x.z) || bf16x2_nonfinite(x.w))
+                *p = make_uint4(bf16x2_finite(x.x), bf16x2_finite(x.y), bf16x2_finite(x.z), bf16x2_finite(x.w));
+        }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+template <bool E4M3>
+__device__ void multiply(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint8_t *stages, uint32_t tmem) {
+    constexpr int kStages = Form<E4M3>::stages;
+    const int lane = threadIdx.x & 31;
+    unsigned taken = 0;                  // K and V tiles of the items before this one
+    unsigned q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
+    int next = 0;
+    bool ok = true;
+    const uint32_t q_addr = smem_u32(q_tiles), st_addr = smem_u32(stages);
+
+    for (unsigned n = 0; ok; ++n) {
+        const int slot = n % kRing;
+        if (!wait_or_abort(sh, &sh->item_full[slot], (n / kRing) & 1, k.a.err)) break;
+        const Item it = sh->item[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
+        if (it.n_vec == 0) break;
+        const bool two = it.n_vec > kTile;
+        const int tiles = (it.n_keys + kTile - 1) / kTile;
+        const int q0 = two ? 0 : next;
+        auto stage_of = [&](int order) { return (taken + order) % kStages; };
+        auto wait_tile = [&](int order) {
+            ok = ok && wait_or_abort(sh, &sh->kv_full[stage_of(order)], ((taken + order) / kStages) & 1, k.a.err);
+            return ok;
+        };
+        auto wait_probs = [&](int buf) {
+            ok = ok && wait_or_abort(sh, &sh->p_full[buf], p_uses[buf]++ & 1, k.a.err);
+            return ok;
+        };
+        // S[s] = Q[qb] K(i)^T over the keys of tile i (rounded up to 16)
+        auto scores = [&](int qb, int s, int i) {
+            if (lane == 0) {
+                const int keys = min(kTile, it.n_keys - i * kTile);
+                const uint32_t idesc = umma_idesc_bf16(kTile, (keys + 15) & ~15, false);
+                const uint32_t a = q_addr + qb * kTileBytes, b = st_addr + stage_of(k_order(i)) * kTileBytes;
+                tc_fence_after();
+#pragma unroll
+                for (int d = 0; d < 8; ++d) {
+                    const uint32_t off = (d >> 2) * kHalfBytes + (d & 3) * 32;
+                    tc_mma_ss(tmem + kTmemS + s * kTile, umma_desc_sw128(a + off, 16, 1024),
+                              umma_desc_sw128(b + off, 16, 1024), idesc, d > 0);
+                }
+                tc_commit(&sh->s_full[two && s ? 2 : s]);
+            }
+            __syncwarp();
+        };
+        // O[o] (+)= P[s] V(i)
+        auto outputs = [&](int o, int s, int i) {
+            if (lane == 0) {
+                const int keys = min(kTile, it.n_keys - i * kTile), steps = (keys + 15) >> 4;
+                const uint32_t idesc = umma_idesc_bf16(kTile, kHeadDim, true);
+                const uint32_t b = st_addr + stage_of(v_order(i, tiles)) * kTileBytes;
+                tc_fence_after();
+                for (int t = 0; t < steps; ++t)
+                    tc_mma_ts(tmem + kTmemO + o * kHeadDim, tmem + kTmemS + s * kTile + 8 * t,
+                              umma_desc_sw128(b + t * 2048, kHalfBytes, 1024), idesc, i > 0 || t > 0);
+                tc_commit(&sh->o_done[o]);
+            }
+            __syncwarp();
+        };
+        auto release = [&](int order) {
+            if (lane == 0) tc_commit(&sh->kv_empty[stage_of(order)]);
+        };
+        auto release_q = [&](int qb) {
+            if (lane == 0) tc_commit(&sh->q_empty[qb]);
+        };
+        for (int t = 0; t < (two ? 2 : 1) && ok; ++t) {
+            const int qb = two ? t : q0;
+            ok = wait_or_abort(sh, &sh->q_full[qb], q_uses[qb]++ & 1, k.a.err);
+        }
+        if (!ok || !wait_tile(k_order(0))) break;
+        scores(q0, 0, 0);
+        if (two) scores(1, 1, 0);
+        release(k_order(0));
+        if (tiles == 1) {
+            release_q(q0);
+            if (two) release_q(1);
+        }
+        for (int i = 0; i < tiles && ok; ++i) {
+            const bool more = i + 1 < tiles;
+            const int s = two ? 0 : i & 1;
+            if (!two && more) {
+                if (!wait_tile(k_order(i + 1))) break;
+                scores(q0, (i + 1) & 1, i + 1);
+                release(k_order(i + 1));
+                if (i + 2 == tiles) release_q(q0);
+            }
+            if (!wait_probs(s) || !wait_tile(v_order(i, tiles))) break;
+            if (!E4M3 && it.b >= 0) {
+                const int valid = min(kTile, it.n_keys - i * kTile);
+                const int hidden = max(0, it.lim0 + 1 - i * kTile);
+                if (hidden < kTile)
+                    mend_values(stages + stage_of(v_order(i, tiles)) * size_t(kTileBytes), min(hidden, valid), valid, lane);
+            }
+            outputs(0, s, i);
+            if (two) {
+                if (more) {
+                    if (!wait_tile(k_order(i + 1))) break;
+                    scores(0, 0, i + 1);
+                }
+                if (!wait_probs(1)) break;
+                outputs(1, 1, i);
+                if (more) {
+                    scores(1, 1, i + 1);
+                    release(k_order(i + 1));
+                    if (i + 2 == tiles) {
+                        release_q(0);
+                        release_q(1);
+                    }
+                }
+            }
+            release(v_order(i, tiles));
+        }
+        taken += 2 * tiles;
+        if (!two) next ^= 1;
+    }
+    // no product outlives the CTA, whichever way the loop ended
+    if (lane == 0) {
+        tc_commit(&sh->drain);
+        wait_drained(&sh->drain, 0);
+    }
+    __syncwarp();
+}
+
+// Rows that see an own entry with non-finite values get them back: mend_values
+// took them out of the product.  x: one element of the output, d its index.
+template <bool E4M3>
+__device__ __forceinline__ float with_nonfinite(const KernelArgs &k, const Item &it, int first, int last, int d, float x) {
+    for (int t = first; t <= last; ++t) {
+        const long long pos = (long long)it.key0 + t;
+        const size_t entry = ((size_t)it.b * k.a.own.n_kv + it.j) * k.a.own.max_len + (size_t)pos;
+        if constexpr (E4M3) {
+            if (k.a.own.v_scale[entry] == kScaleNan) x = __uint_as_float(0x7FC00000u);
+        } else {
+            const uint16_t v =
+                static_cast<const uint16_t *>(k.a.own.v)[entry * kHeadDim + 8 * ((d >> 3) ^ int(pos & 7)) + (d & 7)];
+            if ((v & 0x7F80u) == 0x7F80u) x += __uint_as_float(uint32_t(v) << 16);
+        }
+    }
+    return x;
+}
+
+// Whether any value of the part's entries first .. last (at most 15) is not finite; whole warp.
+template <bool E4M3>
+__device__ __forceinline__ bool any_nonfinite(const KernelArgs &k, const Item &it, int first, int last, int lane) {
+    bool bad = false;
+    if constexpr (E4M3) {
+        if (first + lane <= last)
+            bad = k.a.own.v_scale[((size_t)it.b * k.a.own.n_kv + it.j) * k.a.own.max_len + (size_t)(it.key0 + first + lane)] ==
+                  kScaleNan;
+    } else {
+        for (int i = first * 16 + lane; i < (last + 1) * 16; i += 32) {
+            const size_t entry = ((size_t)it.b * k.a.own.n_kv + it.j) * k.a.own.max_len + (size_t)(it.key0 + (i >> 4));
+            const uint4 x =
+                *(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(k.a.own.v) + entry * kHeadDim) + (i & 15));
+            bad |= bf16x2_nonfinite(x.x) || bf16x2_nonfinite(x.y) || bf16x2_nonfinite(x.z) || bf16x2_nonfinite(x.w);
+        }
+    }
+    return __any_sync(0xFFFFFFFFu, bad);
+}
+
+template <bool E4M3>
+__device__ void softmax(const KernelArgs &k, Shared *sh, uint32_t tmem) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wg = warp >> 2;
+    const uint32_t my_lanes = uint32_t(32 * (warp & 3)) << 16;
+    const uint32_t t_o = tmem + kTmemO + wg * kHeadDim + my_lanes;
+    unsigned s_uses[2] = {0, 0}, o_uses = 0;     // the second group counts its barrier in s_uses[1]
+    for (unsigned n = 0;; ++n) {
+        const int slot = n % kRing;
+        if (!wait_or_abort(sh, &sh->item_full[slot], (n / kRing) & 1, k.a.err)) return;
+        const Item it = sh->item[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
+        if (it.n_vec == 0) return;
+        const bool two = it.n_vec > kTile;
+        const int tiles = (it.n_keys + kTile - 1) / kTile;
+        if (wg == 1 && !two) continue;
+        const int v = 32 * (warp & 3) + lane;               // vector within the tile
+        const int n_here = it.n_vec - wg * kTile;           // of this tile (may exceed 128)
+        const bool active = 32 * (warp & 3) < n_here;
+        const int lim = it.b < 0 ? it.lim0 : it.lim0 + min(v, it.n_vec - 1) / k.a.group;     // last visible part entry
+        float m = -INFINITY, l = 0.f;
+        for (int i = 0; i < tiles; ++i) {
+            const int buf = two ? wg : i & 1;
+            if (!wait_or_abort(sh, &sh->s_full[wg ? 2 : buf], s_uses[buf]++ & 1, k.a.err)) return;
+            bool seen = i == 0;     // whether the previous tile's product into the output is known to be done
+            if (active) {
+                tc_fence_after();
+                const uint32_t t_s = tmem + kTmemS + buf * kTile + my_lanes;
+                const int last = lim - i * kTile;
+                const bool part_seen = __any_sync(0xFFFFFFFFu, last < kTile - 1);
+                // 64 scores at a time in registers: the upper half for its maximum
+                // first, and once more after the lower half's weights have been stored
+                uint32_t x[64];
+                float mt[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                auto load = [&](int c0) {
+                    tc_ld32(t_s + c0, x);
+                    tc_ld32(t_s + c0 + 32, x + 32);
+                    tc_wait_ld();
+                    tc_pin32(x);
+                    tc_pin32(x + 32);
+                    if (part_seen) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) x[c] = c0 + c <= last ? x[c] : 0xFF800000u;
+                    }
+                };
+                load(64);
+#pragma unroll
+                for (int c = 0; c < 64; ++c) mt[c & 3] = fmaxf(mt[c & 3], __uint_as_float(x[c]));
+                load(0);
+#pragma unroll
+                for (int c = 0; c < 64; ++c) mt[c & 3] = fmaxf(mt[c & 3], __uint_as_float(x[c]));
+                const float top = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
+                const bool moved = top > m + kMaxSlack;     // true for the first visible scores (m = -inf)
+                float scale = 1.f;
+                if (moved) {
+                    scale = ex2_approx((m - top) * kScaleLog2);
+                    m = top;
+                    l *= scale;
+                }
+                if (i > 0 && __any_sync(0xFFFFFFFFu, moved)) {
+                    // outputs so far, once the last product into them is done
+                    if (!wait_or_abort(sh, &sh->o_done[wg], (o_uses + i - 1) & 1, k.a.err)) return;
+                    seen = true;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[32];
+                        tc_ld32(t_o + 32 * c, o);
+                        tc_wait_ld();
+                        tc_pin32(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale);
+                        tc_st32(t_o + 32 * c, o);
+                    }
+                    tc_wait_st();
+                }
+                const float mc = m == -INFINITY ? 0.f : m * kScaleLog2;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (h == 1) load(64);
+                    uint32_t p[32];
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const float a = ex2_approx(fmaf(__uint_as_float(x[2 * c]), kScaleLog2, -mc));
+                        const float b = ex2_approx(fmaf(__uint_as_float(x[2 * c + 1]), kScaleLog2, -mc));
+                        sum[2 * (c & 1)] += a;
+                        sum[2 * (c & 1) + 1] += b;
+                        // weights meet V as bf16 (off by at most 2^-9 of each, like V itself);
+                        // the sum keeps them whole
+                        const __nv_bfloat162 pk = __floats2bfloat162_rn(a, b);
+                        p[c] = *reinterpret_cast<const uint32_t *>(&pk);
+                    }
+                    tc_st32(t_s + 32 * h, p);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tc_wait_st();
+            }
+            // every phase is waited on; this one was over long ago
+            if (!seen && !wait_or_abort(sh, &sh->o_done[wg], (o_uses + i - 1) & 1, k.a.err)) return;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->p_full[buf]);
+        }
+        o_uses += tiles;
+        // entries that only some rows see
+        const int first = max(0, it.lim0 + 1), end = it.n_keys - 1;
+        const bool bad = active && it.b >= 0 && first <= end && any_nonfinite<E4M3>(k, it, first, end, lane);
+        if (!wait_or_abort(sh, &sh->o_done[wg], (o_uses - 1) & 1, k.a.err)) return;
+        if (!active) continue;
+        tc_fence_after();
+        const bool store = v < n_here;
+        const long long part = it.part + (wg ? kTile : 0);
+        float4 *dst = reinterpret_cast<float4 *>(k.opart + part * kHeadDim) + v;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tc_ld32(t_o + 32 * c, o);
+            tc_wait_ld();
+            tc_pin32(o);
+            if (store) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    dst[(size_t)(8 * c + e) * it.stride] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                                       __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+            }
+        }
+        if (store) k.ml[part + v] = make_float2(m, l);
+        if (bad && store) {
+            float *o = reinterpret_cast<float *>(dst);
+            for (int d = 0; d < kHeadDim; ++d) {
+                float *e = o + (size_t)(d >> 2) * it.stride * 4 + (d & 3);
+                *e = with_nonfinite<E4M3>(k, it, first, min(lim, end), d, *e);
+            }
+        }
+        tc_fence_before();      // the reads of O precede this warp's next arrival on p_full
+    }
+}
+
+template <bool E4M3>
+__global__ void __launch_bounds__(Form<E4M3>::threads, 1) attn_batch_kernel(const __grid_constant__ KernelArgs k) {
+    using F = Form<E4M3>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *q_tiles = smem, *stages = smem + 2 * kTileBytes, *raw = stages + size_t(F::stages) * kTileBytes;
+    Shared *sh = reinterpret_cast<Shared *>(raw + size_t(F::raw) * (kRawBytes + kTile));
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < F::stages; ++i) {
+            mbar_init(&sh->kv_full[i], E4M3 ? kExpandWarps : 1);
+            mbar_init(&sh->kv_empty[i], 1);
+        }
+        for (int i = 0; i < F::raw; ++i) {
+            mbar_init(&sh->raw_full[i], 1);
+            mbar_init(&sh->raw_empty[i], kExpandWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh->q_full[i], kQueryWarps);
+            mbar_init(&sh->q_empty[i], 1);
+            mbar_init(&sh->p_full[i], 4);
+            mbar_init(&sh->o_done[i], 1);
+        }
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&sh->item_full[i], 1);
+            mbar_init(&sh->item_empty[i], F::readers);
+        }
+        for (int i = 0; i < 3; ++i) mbar_init(&sh->s_full[i], 1);
+        mbar_init(&sh->drain, 1);
+        sh->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) tc_alloc(&sh->tmem, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh->tmem;
+    grid_dependency_wait();     // queries, positions and entries come from the preceding grids
+    grid_launch_dependents();
+    if (warp < kSoftmaxWarps) {
+        regs_raise<F::regs_softmax>();
+        softmax<E4M3>(k, sh, tmem);
+    } else {
+        regs_lower<F::regs_other>();
+        if (warp == kProducerWarp)
+            produce<E4M3>(k, sh, E4M3 ? raw : stages);
+        else if (warp == kMmaWarp)
+            multiply<E4M3>(k, sh, q_tiles, stages, tmem);
+        else if (warp < kExpandWarp)
+            gather_queries(k, sh, q_tiles);
+        else if constexpr (E4M3)
+            expand_tiles(k, sh, stages, raw);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tc_dealloc(tmem, kTmemCols);
+}
+
+// ------------------------------------------------------------------ joining the parts
+// A CTA takes 32 query vectors of one KV head: lane = vector, warp = column quad.
+// Parts are joined in ascending order (prefix, then own) against their common
+// maximum; HBM and L2 bound it: 520 bytes per vector and part.
+constexpr int kJoinUnroll = 8, kJoinChunk = 64;
+
+__global__ void __launch_bounds__(1024) attn_batch_join_kernel(AttnBatchArgs a, Plan p, const float *opart,
+                                                               const float2 *ml, unsigned *next) {
+    __shared__ float s_f[kJoinChunk][32], s_l[kJoinChunk][32];
+    __shared__ uint2 s_out[32][33];
+    grid_dependency_wait();     // partial results come from the preceding grid
+    grid_launch_dependents();
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *next = 0u;
+    const int lane = threadIdx.x & 31, quad = threadIdx.x >> 5, n_kv = a.own.n_kv, rg = a.R * a.group, j = blockIdx.y;
+    const int v = blockIdx.x * 32 + lane;
+    int n = 0, b = 0;
+    if (v < p.n_vec) {
+        b = v / rg;
+        const long long pos = seq_position(a.pos, b, a.R, a.own.max_len, a.err, false);
+        if (pos >= 0) n = p.n_parts + int((pos + (v - b * rg) / a.group) / kOwnPart) + 1;
+    }
+    int n_max = n;
+    for (int o = 16; o > 0; o >>= 1) n_max = max(n_max, __shfl_xor_sync(0xFFFFFFFFu, n_max, o));
+    // vector slot of part c (prefix parts first)
+    const long long slot0 = ((long long)j * p.tiles + v / kTile) * kTile, step0 = (long long)n_kv * p.tiles * kTile;
+    const long long slot1 = p.own0 + ((long long)b * n_kv + j) * rg, step1 = (long long)a.own.n_seq * n_kv * rg;
+    const int in0 = v % kTile, in1 = v - b * rg;
+    auto ml_of = [&](int c) {
+        return c < p.n_parts ? ml[slot0 + c * step0 + in0] : ml[slot1 + (c - p.n_parts) * step1 + in1];
     };
-    walk(a.prefix, (size_t)j * a.prefix.max_len, a.prefix_len);
-    walk(a.own, ((size_t)b * a.own.n_kv + j) * a.own.max_len, p + r + 1);
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(__fdiv_rn(o.x, l), __fdiv_rn(o.y, l));
-    const __nv_bfloat162 hi = __floats2bfloat162_rn(__fdiv_rn(o.z, l), __fdiv_rn(o.w, l));
-    *out = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+    float top = -INFINITY;
+    for (int c = quad; c < n; c += 32) top = fmaxf(top, ml_of(c).x);
+    s_f[quad][lane] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 32; ++w) top = fmaxf(top, s_f[w][lane]);
+    if (top == -INFINITY) top = 0.f;
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c0 = 0; c0 < n_max; c0 += kJoinChunk) {
+        __syncthreads();        // s_f is free again
+        for (int c = quad; c < min(kJoinChunk, n - c0); c += 32) {
+            const float2 w = ml_of(c0 + c);
+            const float f = ex2_approx((w.x - top) * kScaleLog2);
+            s_f[c][lane] = f;
+            s_l[c][lane] = w.y * f;
+        }
+        __syncthreads();
+        const int end = min(n, c0 + kJoinChunk);
+        for (int c = c0; c < end; c += kJoinUnroll) {
+            float4 x[kJoinUnroll];
+#pragma unroll
+            for (int u = 0; u < kJoinUnroll; ++u) {
+                const int cu = min(c + u, end - 1);
+                const long long at = cu < p.n_parts ? (slot0 + cu * step0) * 32 + quad * kTile + in0
+                                                    : (slot1 + (cu - p.n_parts) * step1) * 32 + quad * rg + in1;
+                x[u] = __ldcs(reinterpret_cast<const float4 *>(opart) + at);
+            }
+#pragma unroll
+            for (int u = 0; u < kJoinUnroll; ++u) {
+                if (c + u >= end) break;
+                const float f = s_f[c + u - c0][lane];
+                l += s_l[c + u - c0][lane];
+                o.x = fmaf(x[u].x, f, o.x);
+                o.y = fmaf(x[u].y, f, o.y);
+                o.z = fmaf(x[u].z, f, o.z);
+                o.w = fmaf(x[u].w, f, o.w);
+            }
+        }
+    }
+    const bool idle = n == 0;
+    uint2 r = make_uint2(0u, 0u);
+    if (!idle) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(__fdiv_rn(o.x, l), __fdiv_rn(o.y, l));
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(__fdiv_rn(o.z, l), __fdiv_rn(o.w, l));
+        r = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+    }
+    s_out[lane][quad] = r;
+    __syncthreads();
+    const int vo = blockIdx.x * 32 + quad;      // a warp stores one vector's 256 bytes
+    if (vo < p.n_vec) {
+        const int row = vo / a.group;
+        *(reinterpret_cast<uint2 *>(a.out + (size_t)row * a.ldo + (size_t)(j * a.group + vo - row * a.group) * kHeadDim) +
+          lane) = s_out[quad][lane];
+    }
+}
+
+bool encode_cache(CUtensorMap *m, const void *base, int rows, int max_len, int outer, const char **why) {
+    // innermost first: an entry's 128 elements, entries, (sequence, head).  The cache
+    // is stored with its 16-byte chunks already permuted by position, as the
+    // 128-byte swizzle wants them in shared memory, so the copy permutes nothing.
+    cuuint64_t dims[3] = {cuuint64_t(kHeadDim), cuuint64_t(rows), cuuint64_t(outer)};
+    cuuint64_t strides[2] = {cuuint64_t(kHeadDim) * 2, cuuint64_t(max_len) * kHeadDim * 2};
+    cuuint32_t box[3] = {64, kTile, 1};
+    cuuint32_t ones[3] = {1, 1, 1};
+    const auto fn = tensor_map_encoder();
+    if (!fn) {
+        *why = "cuTensorMapEncodeTiled is unavailable";
+        return false;
+    }
+    if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, ones,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
+        *why = "cuTensorMapEncodeTiled rejected the cache layout";
+        return false;
+    }
+    return true;
 }
 
 }  // namespace
 
-size_t attn_batch_bytes(const KvBatch &, int, int, int) { return 256; }
+size_t attn_batch_bytes(const KvBatch &own, int prefix_len, int group, int R) {
+    const Plan p = plan_of(own, prefix_len, group, R);
+    return 512 + size_t(p.slots) * (kHeadDim * sizeof(float) + sizeof(float2));
+}
 
-cudaError_t launch_attn_batch(const AttnBatchArgs &a, cudaStream_t s) {
-    const long long items = (long long)a.own.n_seq * a.R * a.own.n_kv * a.group;
-    return launch_pdl(attn_batch_kernel, dim3(unsigned((items + 3) / 4)), dim3(128), 0, s, a);
+cudaError_t launch_attn_batch(const AttnBatchArgs &a, cudaStream_t s, const char **why) {
+    static std::atomic<bool> opted_in[kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices || !opted_in[dev]) {
+        e = cudaFuncSetAttribute(attn_batch_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 int(kSmemBytes<false>));
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(attn_batch_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     int(kSmemBytes<true>));
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < kMaxDevices) opted_in[dev] = true;
+    }
+    KernelArgs k{};
+    k.a = a;
+    k.p = plan_of(a.own, a.prefix_len, a.group, a.R);
+    char *base = static_cast<char *>(a.ws);
+    k.next = reinterpret_cast<unsigned *>(base + 256);
+    k.opart = reinterpret_cast<float *>(base + 512);
+    k.ml = reinterpret_cast<float2 *>(base + 512 + size_t(k.p.slots) * kHeadDim * sizeof(float));
+    const bool e4m3 = a.own.format == kKvE4m3;
+    if (!e4m3) {
+        const KvBatch &pre = a.prefix_len > 0 ? a.prefix : a.own;
+        const int pre_rows = a.prefix_len > 0 ? a.prefix_len : a.own.max_len;
+        if (!encode_cache(&k.map[0], pre.k, pre_rows, pre.max_len, pre.n_kv, why) ||
+            !encode_cache(&k.map[1], pre.v, pre_rows, pre.max_len, pre.n_kv, why) ||
+            !encode_cache(&k.map[2], a.own.k, a.own.max_len, a.own.max_len, a.own.n_seq * a.own.n_kv, why) ||
+            !encode_cache(&k.map[3], a.own.v, a.own.max_len, a.own.max_len, a.own.n_seq * a.own.n_kv, why))
+            return cudaErrorInvalidValue;
+    }
+    const long long items = (long long)a.own.n_kv * ((long long)k.p.n_parts * k.p.pairs +
+                                                     (long long)a.own.n_seq * k.p.own_parts_max);
+    const int sms = device_sm_count();
+    const dim3 grid(unsigned(items < sms ? items : sms));
+    e = e4m3 ? launch_pdl(attn_batch_kernel<true>, grid, dim3(Form<true>::threads), kSmemBytes<true>, s, k)
+             : launch_pdl(attn_batch_kernel<false>, grid, dim3(Form<false>::threads), kSmemBytes<false>, s, k);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(attn_batch_join_kernel, dim3((k.p.n_vec + 31) / 32, a.own.n_kv), dim3(1024), 0, s, a, k.p,
+                      (const float *)k.opart, (const float2 *)k.ml, k.next);
 }
 
 }  // namespace tfk

@@ -15,9 +15,11 @@ struct AttnBatchArgs {
     uint16_t *out;          // bf16 [n_seq * R][ldo]
     int ldo;
     int *err;
+    void *ws;               // attn_batch_bytes() of scratch, its first 256 bytes the status word
 };
 
 size_t attn_batch_bytes(const KvBatch &own, int prefix_len, int group, int R);
-cudaError_t launch_attn_batch(const AttnBatchArgs &a, cudaStream_t s);
+// *why is set where the failure is not a CUDA call's.
+cudaError_t launch_attn_batch(const AttnBatchArgs &a, cudaStream_t s, const char **why);
 
 }  // namespace tfk

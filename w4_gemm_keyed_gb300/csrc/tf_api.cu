@@ -982,8 +982,10 @@ tf_status tf_attention_batch(const tf_kv_batch *own, const tf_kv_batch *prefix, 
     a.out = out;
     a.ldo = ldo;
     a.err = static_cast<int *>(ws);
-    cudaError_t e = launch_attn_batch(a, static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return cuda_fail(e, "tf_attention_batch");
+    a.ws = ws;
+    const char *why = "";
+    cudaError_t e = launch_attn_batch(a, static_cast<cudaStream_t>(stream), &why);
+    if (e != cudaSuccess) return fail(TF_ERR_CUDA, "tf_attention_batch: %s %s", cudaGetErrorString(e), why);
     return ok();
 }
 
