@@ -172,6 +172,11 @@ __device__ __forceinline__ bool wait_or_abort(Shared *sh, uint64_t *bar, uint32_
     return mbar_try_wait(bar, parity) || mbar_try_wait(bar, parity) || wait_slow(sh, bar, parity, err);
 }
 
+// The same for a converged warp, with one answer.
+__device__ __forceinline__ bool warp_wait(Shared *sh, uint64_t *bar, uint32_t parity, int *err) {
+    return __all_sync(0xFFFFFFFFu, wait_or_abort(sh, bar, parity, err));
+}
+
 // The same without a report, for what is still in flight when a role ends.
 __device__ __forceinline__ void wait_drained(uint64_t *bar, uint32_t parity) {
     const unsigned long long t0 = now_ns();
@@ -382,7 +387,8 @@ __device__ void expand_tiles(const KernelArgs &k, Shared *sh, uint8_t *stages, c
 }
 
 // Queries of vector v: row v / group, columns (j * group + v % group) * 128, into
-// the swizzled K-major tile; tiles are filled to a multiple of 32 vectors.
+// the swizzled K-major tile; tiles are filled to a multiple of 32 vectors (with
+// repeats of the last: rows of a product never mix).
 __device__ void gather_queries(const KernelArgs &k, Shared *sh, uint8_t *tiles) {
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kQueryWarp;
     const int chunk = lane & 15, g = k.a.group;
@@ -403,24 +409,12 @@ __device__ void gather_queries(const KernelArgs &k, Shared *sh, uint8_t *tiles) 
             const int n_vec = min(kTile, it.n_vec - t * kTile), fill = (n_vec + 31) & ~31;
             uint8_t *dst = tiles + buf * kTileBytes + (chunk >> 3) * kHalfBytes;
             const uint16_t *src = k.a.q + (size_t)it.j * g * kHeadDim + chunk * 8;
-            for (int v0 = 2 * w + (lane >> 4); v0 < fill; v0 += 8 * 2 * kQueryWarps) {
-                uint4 x[8];
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const int v = v0 + u * 2 * kQueryWarps;
-                    x[u] = make_uint4(0u, 0u, 0u, 0u);
-                    if (v < n_vec) {
-                        const int gv = it.vec0 + t * kTile + v, row = gv / g;
-                        x[u] = *reinterpret_cast<const uint4 *>(src + (size_t)row * k.a.ldq + (gv - row * g) * kHeadDim);
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const int v = v0 + u * 2 * kQueryWarps;
-                    if (v < fill)
-                        *reinterpret_cast<uint4 *>(dst + v * 128 + (((chunk & 7) ^ (v & 7)) << 4)) = x[u];
-                }
+            for (int v = 2 * w + (lane >> 4); v < fill; v += 2 * kQueryWarps) {
+                const int gv = it.vec0 + t * kTile + min(v, n_vec - 1), row = gv / g;
+                cp_async_16(dst + v * 128 + (((chunk & 7) ^ (v & 7)) << 4),
+                            src + (size_t)row * k.a.ldq + (gv - row * g) * kHeadDim);
             }
+            cp_async_wait_all();
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh->q_full[buf]);
@@ -454,6 +448,7 @@ template <bool E4M3>
 __device__ void multiply(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint8_t *stages, uint32_t tmem) {
     constexpr int kStages = Form<E4M3>::stages;
     const int lane = threadIdx.x & 31;
+    const uint32_t leader = elect_one();
     unsigned taken = 0;                  // K and V tiles of the items before this one
     unsigned q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
     int next = 0;
@@ -462,63 +457,61 @@ __device__ void multiply(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint
 
     for (unsigned n = 0; ok; ++n) {
         const int slot = n % kRing;
-        if (!wait_or_abort(sh, &sh->item_full[slot], (n / kRing) & 1, k.a.err)) break;
-        const Item it = sh->item[slot];
-        __syncwarp();
+        if (!warp_wait(sh, &sh->item_full[slot], (n / kRing) & 1, k.a.err)) break;
+        // broadcast: the same in all lanes, and known to be
+        const int n_vec = __shfl_sync(0xFFFFFFFFu, sh->item[slot].n_vec, 0);
+        const int n_keys = __shfl_sync(0xFFFFFFFFu, sh->item[slot].n_keys, 0);
+        const int lim0 = __shfl_sync(0xFFFFFFFFu, sh->item[slot].lim0, 0);
+        const int seq = __shfl_sync(0xFFFFFFFFu, sh->item[slot].b, 0);
         if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
-        if (it.n_vec == 0) break;
-        const bool two = it.n_vec > kTile;
-        const int tiles = (it.n_keys + kTile - 1) / kTile;
+        __syncwarp();
+        if (n_vec == 0) break;
+        const bool two = n_vec > kTile;
+        const int tiles = (n_keys + kTile - 1) / kTile;
         const int q0 = two ? 0 : next;
         auto stage_of = [&](int order) { return (taken + order) % kStages; };
         auto wait_tile = [&](int order) {
-            ok = ok && wait_or_abort(sh, &sh->kv_full[stage_of(order)], ((taken + order) / kStages) & 1, k.a.err);
+            ok = ok && warp_wait(sh, &sh->kv_full[stage_of(order)], ((taken + order) / kStages) & 1, k.a.err);
             return ok;
         };
         auto wait_probs = [&](int buf) {
-            ok = ok && wait_or_abort(sh, &sh->p_full[buf], p_uses[buf]++ & 1, k.a.err);
+            ok = ok && warp_wait(sh, &sh->p_full[buf], p_uses[buf]++ & 1, k.a.err);
             return ok;
         };
         // S[s] = Q[qb] K(i)^T over the keys of tile i (rounded up to 16)
         auto scores = [&](int qb, int s, int i) {
-            if (lane == 0) {
-                const int keys = min(kTile, it.n_keys - i * kTile);
-                const uint32_t idesc = umma_idesc_bf16(kTile, (keys + 15) & ~15, false);
-                const uint32_t a = q_addr + qb * kTileBytes, b = st_addr + stage_of(k_order(i)) * kTileBytes;
-                tc_fence_after();
+            const int keys = min(kTile, n_keys - i * kTile);
+            const uint32_t idesc = umma_idesc_bf16(kTile, (keys + 15) & ~15, false);
+            const uint64_t a = umma_desc_sw128(q_addr + qb * kTileBytes, 16, 1024);
+            const uint64_t b = umma_desc_sw128(st_addr + stage_of(k_order(i)) * kTileBytes, 16, 1024);
+            tc_fence_after();
 #pragma unroll
-                for (int d = 0; d < 8; ++d) {
-                    const uint32_t off = (d >> 2) * kHalfBytes + (d & 3) * 32;
-                    tc_mma_ss(tmem + kTmemS + s * kTile, umma_desc_sw128(a + off, 16, 1024),
-                              umma_desc_sw128(b + off, 16, 1024), idesc, d > 0);
-                }
-                tc_commit(&sh->s_full[two && s ? 2 : s]);
+            for (int d = 0; d < 8; ++d) {
+                const uint64_t off = ((d >> 2) * kHalfBytes + (d & 3) * 32) >> 4;
+                tc_mma_ss(leader, tmem + kTmemS + s * kTile, a + off, b + off, idesc, d > 0);
             }
-            __syncwarp();
+            tc_commit(leader, &sh->s_full[two && s ? 2 : s]);
         };
         // O[o] (+)= P[s] V(i)
         auto outputs = [&](int o, int s, int i) {
-            if (lane == 0) {
-                const int keys = min(kTile, it.n_keys - i * kTile), steps = (keys + 15) >> 4;
-                const uint32_t idesc = umma_idesc_bf16(kTile, kHeadDim, true);
-                const uint32_t b = st_addr + stage_of(v_order(i, tiles)) * kTileBytes;
-                tc_fence_after();
-                for (int t = 0; t < steps; ++t)
-                    tc_mma_ts(tmem + kTmemO + o * kHeadDim, tmem + kTmemS + s * kTile + 8 * t,
-                              umma_desc_sw128(b + t * 2048, kHalfBytes, 1024), idesc, i > 0 || t > 0);
-                tc_commit(&sh->o_done[o]);
+            const int keys = min(kTile, n_keys - i * kTile), steps = (keys + 15) >> 4;
+            const uint32_t idesc = umma_idesc_bf16(kTile, kHeadDim, true);
+            const uint64_t b = umma_desc_sw128(st_addr + stage_of(v_order(i, tiles)) * kTileBytes, kHalfBytes, 1024);
+            const uint32_t d = tmem + kTmemO + o * kHeadDim, a = tmem + kTmemS + s * kTile;
+            tc_fence_after();
+            if (steps == 8) {
+#pragma unroll
+                for (int t = 0; t < 8; ++t) tc_mma_ts(leader, d, a + 8 * t, b + t * 128, idesc, i > 0 || t > 0);
+            } else {
+                for (int t = 0; t < steps; ++t) tc_mma_ts(leader, d, a + 8 * t, b + t * 128, idesc, i > 0 || t > 0);
             }
-            __syncwarp();
+            tc_commit(leader, &sh->o_done[o]);
         };
-        auto release = [&](int order) {
-            if (lane == 0) tc_commit(&sh->kv_empty[stage_of(order)]);
-        };
-        auto release_q = [&](int qb) {
-            if (lane == 0) tc_commit(&sh->q_empty[qb]);
-        };
+        auto release = [&](int order) { tc_commit(leader, &sh->kv_empty[stage_of(order)]); };
+        auto release_q = [&](int qb) { tc_commit(leader, &sh->q_empty[qb]); };
         for (int t = 0; t < (two ? 2 : 1) && ok; ++t) {
             const int qb = two ? t : q0;
-            ok = wait_or_abort(sh, &sh->q_full[qb], q_uses[qb]++ & 1, k.a.err);
+            ok = warp_wait(sh, &sh->q_full[qb], q_uses[qb]++ & 1, k.a.err);
         }
         if (!ok || !wait_tile(k_order(0))) break;
         scores(q0, 0, 0);
@@ -538,9 +531,9 @@ __device__ void multiply(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint
                 if (i + 2 == tiles) release_q(q0);
             }
             if (!wait_probs(s) || !wait_tile(v_order(i, tiles))) break;
-            if (!E4M3 && it.b >= 0) {
-                const int valid = min(kTile, it.n_keys - i * kTile);
-                const int hidden = max(0, it.lim0 + 1 - i * kTile);
+            if (!E4M3 && seq >= 0) {
+                const int valid = min(kTile, n_keys - i * kTile);
+                const int hidden = max(0, lim0 + 1 - i * kTile);
                 if (hidden < kTile)
                     mend_values(stages + stage_of(v_order(i, tiles)) * size_t(kTileBytes), min(hidden, valid), valid, lane);
             }
@@ -567,11 +560,9 @@ __device__ void multiply(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint
         if (!two) next ^= 1;
     }
     // no product outlives the CTA, whichever way the loop ended
-    if (lane == 0) {
-        tc_commit(&sh->drain);
-        wait_drained(&sh->drain, 0);
-    }
     __syncwarp();
+    tc_commit(leader, &sh->drain);
+    wait_drained(&sh->drain, 0);
 }
 
 // Rows that see an own entry with non-finite values get them back: mend_values
