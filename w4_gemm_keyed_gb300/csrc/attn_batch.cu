@@ -126,7 +126,7 @@ struct KernelArgs {
 // softmax group (0, 1, 0), S1 of two-tile items by the second (2).
 struct __align__(16) Shared {
     uint64_t kv_full[5], kv_empty[5], raw_full[4], raw_empty[4];
-    uint64_t q_full[2], q_empty[2], s_full[3], p_full[2], o_done[2];
+    uint64_t q_full[2], q_empty[2], s_full[3], p_full[2][2], o_done[2];
     uint64_t item_full[kRing], item_empty[kRing], drain;
     Item item[kRing];
     int before[kGroups + 1];    // own parts of the sequence groups before each
@@ -191,6 +191,30 @@ __device__ __forceinline__ int v_order(int i, int n) { return i == n - 1 ? 2 * n
 __device__ __forceinline__ bool order_is_v(int t, int n) { return t == 2 * n - 1 || (t != 0 && t % 2 == 0); }
 __device__ __forceinline__ int order_tile(int t, int n) {
     return t == 2 * n - 1 ? n - 1 : (t == 0 ? 0 : (t % 2 == 0 ? t / 2 - 1 : (t + 1) / 2));
+}
+
+// Two fp32 operations in one instruction, each rounded as the single one is.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    return uint64_t(__float_as_uint(a)) | (uint64_t(__float_as_uint(b)) << 32);
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
+    a = __uint_as_float(uint32_t(v));
+    b = __uint_as_float(uint32_t(v >> 32));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 __device__ __forceinline__ bool bf16x2_nonfinite(uint32_t w) {
@@ -388,7 +412,7 @@ __device__ void expand_tiles(const KernelArgs &k, Shared *sh, uint8_t *stages, c
 
 // Queries of vector v: row v / group, columns (j * group + v % group) * 128, into
 // the swizzled K-major tile; tiles are filled to a multiple of 32 vectors (with
-// repeats of the last: rows of a product never mix).
+// repeats of the first: rows of a product never mix).
 __device__ void gather_queries(const KernelArgs &k, Shared *sh, uint8_t *tiles) {
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kQueryWarp;
     const int chunk = lane & 15, g = k.a.group;
@@ -409,10 +433,19 @@ __device__ void gather_queries(const KernelArgs &k, Shared *sh, uint8_t *tiles) 
             const int n_vec = min(kTile, it.n_vec - t * kTile), fill = (n_vec + 31) & ~31;
             uint8_t *dst = tiles + buf * kTileBytes + (chunk >> 3) * kHalfBytes;
             const uint16_t *src = k.a.q + (size_t)it.j * g * kHeadDim + chunk * 8;
-            for (int v = 2 * w + (lane >> 4); v < fill; v += 2 * kQueryWarps) {
-                const int gv = it.vec0 + t * kTile + min(v, n_vec - 1), row = gv / g;
-                cp_async_16(dst + v * 128 + (((chunk & 7) ^ (v & 7)) << 4),
-                            src + (size_t)row * k.a.ldq + (gv - row * g) * kHeadDim);
+            constexpr int kStep = 2 * kQueryWarps;      // vectors both warps take at a time
+            const int v0 = 2 * w + (lane >> 4), dr = kStep / g, dh = kStep - dr * g;
+            int row = (it.vec0 + t * kTile + v0) / g, h = it.vec0 + t * kTile + v0 - row * g;
+            for (int v = v0; v < fill; v += kStep) {
+                // past the last vector: any row of the batch will do, so the first
+                const uint16_t *from = v < n_vec ? src + (size_t)row * k.a.ldq + h * kHeadDim : src;
+                cp_async_16(dst + v * 128 + (((chunk & 7) ^ (v & 7)) << 4), from);
+                row += dr;
+                h += dh;
+                if (h >= g) {
+                    h -= g;
+                    ++row;
+                }
             }
             cp_async_wait_all();
             fence_proxy_async_smem();
@@ -474,10 +507,6 @@ __device__ void multiply(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint
             ok = ok && warp_wait(sh, &sh->kv_full[stage_of(order)], ((taken + order) / kStages) & 1, k.a.err);
             return ok;
         };
-        auto wait_probs = [&](int buf) {
-            ok = ok && warp_wait(sh, &sh->p_full[buf], p_uses[buf]++ & 1, k.a.err);
-            return ok;
-        };
         // S[s] = Q[qb] K(i)^T over the keys of tile i (rounded up to 16)
         auto scores = [&](int qb, int s, int i) {
             const int keys = min(kTile, n_keys - i * kTile);
@@ -492,20 +521,30 @@ __device__ void multiply(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint
             }
             tc_commit(leader, &sh->s_full[two && s ? 2 : s]);
         };
-        // O[o] (+)= P[s] V(i)
+        // O[o] (+)= P[s] V(i), 64 keys at a time as their weights arrive
         auto outputs = [&](int o, int s, int i) {
-            const int keys = min(kTile, n_keys - i * kTile), steps = (keys + 15) >> 4;
+            const int steps = (min(kTile, n_keys - i * kTile) + 15) >> 4;
             const uint32_t idesc = umma_idesc_bf16(kTile, kHeadDim, true);
             const uint64_t b = umma_desc_sw128(st_addr + stage_of(v_order(i, tiles)) * kTileBytes, kHalfBytes, 1024);
             const uint32_t d = tmem + kTmemO + o * kHeadDim, a = tmem + kTmemS + s * kTile;
-            tc_fence_after();
-            if (steps == 8) {
 #pragma unroll
-                for (int t = 0; t < 8; ++t) tc_mma_ts(leader, d, a + 8 * t, b + t * 128, idesc, i > 0 || t > 0);
-            } else {
-                for (int t = 0; t < steps; ++t) tc_mma_ts(leader, d, a + 8 * t, b + t * 128, idesc, i > 0 || t > 0);
+            for (int h = 0; h < 2; ++h) {
+                if (h == 1) ok = ok && warp_wait(sh, &sh->p_full[s][1], p_uses[s] & 1, k.a.err);
+                if (!ok) return;
+                tc_fence_after();
+                if (steps >= 4 * h + 4) {
+#pragma unroll
+                    for (int t = 4 * h; t < 4 * h + 4; ++t) tc_mma_ts(leader, d, a + 8 * t, b + t * 128, idesc, i > 0 || t > 0);
+                } else {
+                    for (int t = 4 * h; t < steps; ++t) tc_mma_ts(leader, d, a + 8 * t, b + t * 128, idesc, i > 0 || t > 0);
+                }
             }
+            ++p_uses[s];
             tc_commit(leader, &sh->o_done[o]);
+        };
+        auto wait_probs = [&](int s) {      // the first 64 keys' weights
+            ok = ok && warp_wait(sh, &sh->p_full[s][0], p_uses[s] & 1, k.a.err);
+            return ok;
         };
         auto release = [&](int order) { tc_commit(leader, &sh->kv_empty[stage_of(order)]); };
         auto release_q = [&](int qb) { tc_commit(leader, &sh->q_empty[qb]); };
@@ -647,12 +686,15 @@ __device__ void softmax(const KernelArgs &k, Shared *sh, uint32_t tmem) {
                         for (int c = 0; c < 64; ++c) x[c] = c0 + c <= last ? x[c] : 0xFF800000u;
                     }
                 };
+                auto widen = [&]() {
+#pragma unroll
+                    for (int c = 0; c < 64; c += 2)
+                        mt[(c >> 1) & 3] = max3(mt[(c >> 1) & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+                };
                 load(64);
-#pragma unroll
-                for (int c = 0; c < 64; ++c) mt[c & 3] = fmaxf(mt[c & 3], __uint_as_float(x[c]));
+                widen();
                 load(0);
-#pragma unroll
-                for (int c = 0; c < 64; ++c) mt[c & 3] = fmaxf(mt[c & 3], __uint_as_float(x[c]));
+                widen();
                 const float top = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
                 const bool moved = top > m + kMaxSlack;     // true for the first visible scores (m = -inf)
                 float scale = 1.f;
@@ -679,32 +721,44 @@ __device__ void softmax(const KernelArgs &k, Shared *sh, uint32_t tmem) {
                     tc_wait_st();
                 }
                 const float mc = m == -INFINITY ? 0.f : m * kScaleLog2;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t scale2 = pack2(kScaleLog2, kScaleLog2), shift2 = pack2(-mc, -mc);
+                uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if (h == 1) load(64);
-                    uint32_t p[32];
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
-                        const float a = ex2_approx(fmaf(__uint_as_float(x[2 * c]), kScaleLog2, -mc));
-                        const float b = ex2_approx(fmaf(__uint_as_float(x[2 * c + 1]), kScaleLog2, -mc));
-                        sum[2 * (c & 1)] += a;
-                        sum[2 * (c & 1) + 1] += b;
+                        float a, b;
+                        unpack2(fma2(pack2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), scale2, shift2), a, b);
+                        a = ex2_approx(a);
+                        b = ex2_approx(b);
+                        sum2[c & 1] = add2(sum2[c & 1], pack2(a, b));
                         // weights meet V as bf16 (off by at most 2^-9 of each, like V itself);
                         // the sum keeps them whole
                         const __nv_bfloat162 pk = __floats2bfloat162_rn(a, b);
-                        p[c] = *reinterpret_cast<const uint32_t *>(&pk);
+                        x[c] = *reinterpret_cast<const uint32_t *>(&pk);
                     }
-                    tc_st32(t_s + 32 * h, p);
+                    tc_st32(t_s + 32 * h, x);
+                    if (h == 0) {       // the product with the first 64 keys may start
+                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh->p_full[buf][0]);
+                    }
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                float s0, s1, s2, s3;
+                unpack2(sum2[0], s0, s1);
+                unpack2(sum2[1], s2, s3);
+                l += (s0 + s1) + (s2 + s3);
                 tc_wait_st();
+            } else if (lane == 0) {
+                mbar_arrive(&sh->p_full[buf][0]);
             }
             // every phase is waited on; this one was over long ago
             if (!seen && !wait_or_abort(sh, &sh->o_done[wg], (o_uses + i - 1) & 1, k.a.err)) return;
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->p_full[buf]);
+            if (lane == 0) mbar_arrive(&sh->p_full[buf][1]);
         }
         o_uses += tiles;
         // entries that only some rows see
@@ -760,7 +814,8 @@ __global__ void __launch_bounds__(Form<E4M3>::threads, 1) attn_batch_kernel(cons
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh->q_full[i], kQueryWarps);
             mbar_init(&sh->q_empty[i], 1);
-            mbar_init(&sh->p_full[i], 4);
+            mbar_init(&sh->p_full[i][0], 4);
+            mbar_init(&sh->p_full[i][1], 4);
             mbar_init(&sh->o_done[i], 1);
         }
         for (int i = 0; i < kRing; ++i) {
