@@ -46,7 +46,7 @@ constexpr int kHalfBytes = kTile * 128; // 64 elements of 128 rows
 constexpr int kTileBytes = 2 * kHalfBytes;
 constexpr int kRing = 4;                // items known ahead
 constexpr int kGroups = 256;            // entries of the table of own parts
-constexpr int kSoftmaxWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kQueryWarp = 10, kQueryWarps = 2;
+constexpr int kSoftmaxWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kQueryWarp = 10;
 constexpr int kExpandWarp = 12, kExpandWarps = 4;
 
 // What the cache's format changes: an E4M3 tile (16 KB and 128 scale bytes) is
@@ -54,10 +54,10 @@ constexpr int kExpandWarp = 12, kExpandWarps = 4;
 // the products are those of a bf16 cache holding the same values.
 template <bool E4M3>
 struct Form {
-    static constexpr int stages = E4M3 ? 3 : 5;         // bf16 K and V tiles in shared memory
-    static constexpr int raw = E4M3 ? 4 : 0;            // E4M3 tiles on their way
+    static constexpr int stages = E4M3 ? 4 : 5;         // bf16 K and V tiles in shared memory
+    static constexpr int raw = E4M3 ? 2 : 0;            // E4M3 tiles on their way
     static constexpr int threads = E4M3 ? 512 : 384;
-    static constexpr int readers = kSoftmaxWarps + 1 + kQueryWarps + (E4M3 ? kExpandWarps : 0);  // of the item ring
+    static constexpr int readers = kSoftmaxWarps + 2 + (E4M3 ? kExpandWarps : 0);  // of the item ring
     // registers a thread: the softmax warps' and the others', together no more
     // than the launch's share (128 a thread of 512, 168 of 384)
     static constexpr int regs_softmax = E4M3 ? 184 : 208, regs_other = E4M3 ? 72 : 88;
@@ -77,12 +77,12 @@ struct Item {
     long long part;     // index of the part's first (vector, column quad 0) in opart / 32, and in ml
 };
 
-// Prefix partials: [part][n_kv][tiles][32 quads][128 vectors][4]; own partials:
+// Prefix partials: [part][n_kv][tiles][32 quads][tile vectors][4]; own partials:
 // [part][n_seq][n_kv][32 quads][R * group][4].  Maxima and sums: the same
 // without the quads.  Quad-major so that a warp's 32 vectors store and load 512
 // consecutive bytes.
 struct Plan {
-    int n_vec, tiles, pairs;    // vectors, 128-vector tiles and pairs of them per KV head
+    int n_vec, tile, tiles, pairs;      // vectors; per tile; tiles and pairs of them per KV head
     int part, n_parts;          // prefix part length and count
     int own_parts_max;
     long long own0;             // index of the first own vector slot after the prefix's
@@ -101,18 +101,19 @@ __host__ __device__ inline int prefix_part(int prefix_len, int n_kv) {
 Plan plan_of(const KvBatch &own, int prefix_len, int group, int R) {
     Plan p;
     p.n_vec = own.n_seq * R * group;
-    p.tiles = (p.n_vec + kTile - 1) / kTile;
+    p.tile = kTile / group * group;     // whole rows, so that a tile of queries is one box to TMA
+    p.tiles = (p.n_vec + p.tile - 1) / p.tile;
     p.pairs = (p.tiles + 1) / 2;
     p.part = prefix_part(prefix_len, own.n_kv);
     p.n_parts = (prefix_len + p.part - 1) / p.part;
     p.own_parts_max = (own.max_len + kOwnPart - 1) / kOwnPart;
-    p.own0 = (long long)p.n_parts * own.n_kv * p.tiles * kTile;
+    p.own0 = (long long)p.n_parts * own.n_kv * p.tiles * p.tile;
     p.slots = p.own0 + (long long)p.own_parts_max * own.n_kv * p.n_vec;
     return p;
 }
 
 struct KernelArgs {
-    CUtensorMap map[4];     // prefix K, V; own K, V
+    CUtensorMap map[5];     // prefix K, V; own K, V (bf16 caches); queries
     AttnBatchArgs a;
     Plan p;
     float *opart;           // [slots][128]
@@ -242,13 +243,13 @@ __device__ Item item_of(const KernelArgs &k, const Shared *sh, long long i, int 
         const int pair = int(i % k.p.pairs), cj = int(i / k.p.pairs), c = cj / n_kv;
         it.j = cj % n_kv;
         it.b = -1;
-        it.vec0 = pair * 2 * kTile;
-        it.n_vec = min(2 * kTile, k.p.n_vec - it.vec0);
+        it.vec0 = pair * 2 * k.p.tile;
+        it.n_vec = min(2 * k.p.tile, k.p.n_vec - it.vec0);
         it.key0 = c * k.p.part;
         it.n_keys = min(k.p.part, k.a.prefix_len - it.key0);
         it.lim0 = it.n_keys - 1;
-        it.stride = kTile;
-        it.part = ((long long)cj * k.p.tiles + 2 * pair) * kTile;
+        it.stride = k.p.tile;
+        it.part = ((long long)cj * k.p.tiles + 2 * pair) * k.p.tile;
         return it;
     }
     i -= n_prefix;
@@ -282,7 +283,7 @@ __device__ Item item_of(const KernelArgs &k, const Shared *sh, long long i, int 
 // ------------------------------------------------------------------ roles
 // One CTA per SM takes items from a common counter.
 //   warp 8      finds the next item and streams its K and V tiles by TMA
-//   warps 10-11 gather the item's query vectors
+//   warp 10     streams the items' query vectors
 //   warp 9      issues the products
 //   warps 12-15 expand E4M3 tiles (there alone)
 //   warps 0-7   softmax: a thread per vector.  Items of two tiles give one tile to
@@ -410,50 +411,40 @@ __device__ void expand_tiles(const KernelArgs &k, Shared *sh, uint8_t *stages, c
     }
 }
 
-// Queries of vector v: row v / group, columns (j * group + v % group) * 128, into
-// the swizzled K-major tile; tiles are filled to a multiple of 32 vectors (with
-// repeats of the first: rows of a product never mix).
-__device__ void gather_queries(const KernelArgs &k, Shared *sh, uint8_t *tiles) {
-    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kQueryWarp;
-    const int chunk = lane & 15, g = k.a.group;
+// The query vectors of a tile, whole rows of the KV head's `group` query heads,
+// as one box of (64 elements, heads, rows) per half, swizzled into a K-major tile.
+// Rows of the box past the item's (another sequence's, or zeros past the last)
+// fill vectors that nothing reads: rows of a product never mix.
+__device__ void load_queries(const KernelArgs &k, Shared *sh, uint8_t *tiles) {
+    if ((threadIdx.x & 31) != 0) return;
+    const int g = k.a.group;
+    const uint32_t half_bytes = uint32_t(k.p.tile) * 128u;
     unsigned uses[2] = {0, 0};
     int next = 0;
     for (unsigned n = 0;; ++n) {
         const int slot = n % kRing;
-        if (!wait_or_abort(sh, &sh->item_full[slot], (n / kRing) & 1, k.a.err)) return;
+        if (!wait_or_abort(sh, &sh->item_full[slot], (n / kRing) & 1, k.a.err)) break;
         const Item it = sh->item[slot];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
-        if (it.n_vec == 0) return;
-        const bool two = it.n_vec > kTile;
-        for (int t = 0; t < (two ? 2 : 1); ++t) {
+        mbar_arrive(&sh->item_empty[slot]);
+        if (it.n_vec == 0) break;
+        const bool two = it.n_vec > k.p.tile;
+        bool ok = true;
+        for (int t = 0; t < (two ? 2 : 1) && ok; ++t) {
             const int buf = two ? t : next;
-            if (uses[buf] > 0 && !wait_or_abort(sh, &sh->q_empty[buf], (uses[buf] - 1) & 1, k.a.err)) return;
+            if (uses[buf] > 0) ok = wait_or_abort(sh, &sh->q_empty[buf], (uses[buf] - 1) & 1, k.a.err);
+            if (!ok) break;
             ++uses[buf];
-            const int n_vec = min(kTile, it.n_vec - t * kTile), fill = (n_vec + 31) & ~31;
-            uint8_t *dst = tiles + buf * kTileBytes + (chunk >> 3) * kHalfBytes;
-            const uint16_t *src = k.a.q + (size_t)it.j * g * kHeadDim + chunk * 8;
-            constexpr int kStep = 2 * kQueryWarps;      // vectors both warps take at a time
-            const int v0 = 2 * w + (lane >> 4), dr = kStep / g, dh = kStep - dr * g;
-            int row = (it.vec0 + t * kTile + v0) / g, h = it.vec0 + t * kTile + v0 - row * g;
-            for (int v = v0; v < fill; v += kStep) {
-                // past the last vector: any row of the batch will do, so the first
-                const uint16_t *from = v < n_vec ? src + (size_t)row * k.a.ldq + h * kHeadDim : src;
-                cp_async_16(dst + v * 128 + (((chunk & 7) ^ (v & 7)) << 4), from);
-                row += dr;
-                h += dh;
-                if (h >= g) {
-                    h -= g;
-                    ++row;
-                }
-            }
-            cp_async_wait_all();
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->q_full[buf]);
+            const int row = it.vec0 / g + t * (k.p.tile / g);
+            mbar_arrive_expect_tx(&sh->q_full[buf], 2 * half_bytes);
+            tma_load_3d(tiles + buf * kTileBytes, &k.map[4], 0, it.j * g, row, &sh->q_full[buf]);
+            tma_load_3d(tiles + buf * kTileBytes + kHalfBytes, &k.map[4], 64, it.j * g, row, &sh->q_full[buf]);
         }
+        if (!ok) break;
         if (!two) next ^= 1;
     }
+    // no copy outlives the CTA
+    for (int buf = 0; buf < 2; ++buf)
+        if (uses[buf] > 0) wait_drained(&sh->q_full[buf], (uses[buf] - 1) & 1);
 }
 
 // The last V tiles of an own part: rows past the sequence's last entry become
@@ -499,7 +490,7 @@ __device__ void multiply(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint
         if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
         __syncwarp();
         if (n_vec == 0) break;
-        const bool two = n_vec > kTile;
+        const bool two = n_vec > k.p.tile;
         const int tiles = (n_keys + kTile - 1) / kTile;
         const int q0 = two ? 0 : next;
         auto stage_of = [&](int order) { return (taken + order) % kStages; };
@@ -654,11 +645,11 @@ __device__ void softmax(const KernelArgs &k, Shared *sh, uint32_t tmem) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
         if (it.n_vec == 0) return;
-        const bool two = it.n_vec > kTile;
+        const bool two = it.n_vec > k.p.tile;
         const int tiles = (it.n_keys + kTile - 1) / kTile;
         if (wg == 1 && !two) continue;
         const int v = 32 * (warp & 3) + lane;               // vector within the tile
-        const int n_here = it.n_vec - wg * kTile;           // of this tile (may exceed 128)
+        const int n_here = min(k.p.tile, it.n_vec - wg * k.p.tile);     // of this tile
         const bool active = 32 * (warp & 3) < n_here;
         const int lim = it.b < 0 ? it.lim0 : it.lim0 + min(v, it.n_vec - 1) / k.a.group;     // last visible part entry
         float m = -INFINITY, l = 0.f;
@@ -768,7 +759,7 @@ __device__ void softmax(const KernelArgs &k, Shared *sh, uint32_t tmem) {
         if (!active) continue;
         tc_fence_after();
         const bool store = v < n_here;
-        const long long part = it.part + (wg ? kTile : 0);
+        const long long part = it.part + (wg ? k.p.tile : 0);
         float4 *dst = reinterpret_cast<float4 *>(k.opart + part * kHeadDim) + v;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -812,7 +803,7 @@ __global__ void __launch_bounds__(Form<E4M3>::threads, 1) attn_batch_kernel(cons
             mbar_init(&sh->raw_empty[i], kExpandWarps);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh->q_full[i], kQueryWarps);
+            mbar_init(&sh->q_full[i], 1);
             mbar_init(&sh->q_empty[i], 1);
             mbar_init(&sh->p_full[i][0], 4);
             mbar_init(&sh->p_full[i][1], 4);
@@ -843,9 +834,9 @@ __global__ void __launch_bounds__(Form<E4M3>::threads, 1) attn_batch_kernel(cons
             produce<E4M3>(k, sh, E4M3 ? raw : stages);
         else if (warp == kMmaWarp)
             multiply<E4M3>(k, sh, q_tiles, stages, tmem);
-        else if (warp < kExpandWarp)
-            gather_queries(k, sh, q_tiles);
-        else if constexpr (E4M3)
+        else if (warp == kQueryWarp)
+            load_queries(k, sh, q_tiles);
+        else if (E4M3 && warp >= kExpandWarp)
             expand_tiles(k, sh, stages, raw);
     }
     tc_fence_before();
@@ -855,19 +846,23 @@ __global__ void __launch_bounds__(Form<E4M3>::threads, 1) attn_batch_kernel(cons
 }
 
 // ------------------------------------------------------------------ joining the parts
-// A CTA takes 32 query vectors of one KV head: lane = vector, warp = column quad.
-// Parts are joined in ascending order (prefix, then own) against their common
-// maximum; HBM and L2 bound it: 520 bytes per vector and part.
-constexpr int kJoinUnroll = 8, kJoinChunk = 64;
+// A CTA takes 32 query vectors (lanes) and four column quads of one KV head; its
+// 16 warps are the quads times four runs of consecutive parts.  A run's parts are
+// folded in ascending order (prefix parts first) against the maximum of all the
+// vector's parts, then the runs in ascending order: an order that the number of
+// the vector's parts fixes.  520 bytes per vector and part from HBM or L2 bound it
+// where there are many vectors; where there are few, the chain of two loads does.
+constexpr int kJoinRuns = 4, kJoinQuads = 4, kJoinUnroll = 5;
 
-__global__ void __launch_bounds__(1024) attn_batch_join_kernel(AttnBatchArgs a, Plan p, const float *opart,
-                                                               const float2 *ml, unsigned *next) {
-    __shared__ float s_f[kJoinChunk][32], s_l[kJoinChunk][32];
-    __shared__ uint2 s_out[32][33];
+__global__ void __launch_bounds__(32 * kJoinRuns * kJoinQuads, 2) attn_batch_join_kernel(
+    AttnBatchArgs a, Plan p, const float *opart, const float2 *ml, unsigned *next) {
+    __shared__ float s_top[kJoinRuns][32], s_l[kJoinRuns][32];
+    __shared__ float4 s_o[kJoinRuns][kJoinQuads][32];
     grid_dependency_wait();     // partial results come from the preceding grid
     grid_launch_dependents();
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *next = 0u;
-    const int lane = threadIdx.x & 31, quad = threadIdx.x >> 5, n_kv = a.own.n_kv, rg = a.R * a.group, j = blockIdx.y;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *next = 0u;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, run = warp / kJoinQuads, col = warp % kJoinQuads;
+    const int quad = blockIdx.z * kJoinQuads + col, n_kv = a.own.n_kv, rg = a.R * a.group, j = blockIdx.y;
     const int v = blockIdx.x * 32 + lane;
     int n = 0, b = 0;
     if (v < p.n_vec) {
@@ -875,92 +870,103 @@ __global__ void __launch_bounds__(1024) attn_batch_join_kernel(AttnBatchArgs a, 
         const long long pos = seq_position(a.pos, b, a.R, a.own.max_len, a.err, false);
         if (pos >= 0) n = p.n_parts + int((pos + (v - b * rg) / a.group) / kOwnPart) + 1;
     }
-    int n_max = n;
-    for (int o = 16; o > 0; o >>= 1) n_max = max(n_max, __shfl_xor_sync(0xFFFFFFFFu, n_max, o));
-    // vector slot of part c (prefix parts first)
-    const long long slot0 = ((long long)j * p.tiles + v / kTile) * kTile, step0 = (long long)n_kv * p.tiles * kTile;
+    const int c_begin = n * run / kJoinRuns, c_end = n * (run + 1) / kJoinRuns;
+    // vector slot of part c
+    const int tile = v / p.tile, in0 = v - tile * p.tile, in1 = v - b * rg;
+    const long long slot0 = ((long long)j * p.tiles + tile) * p.tile, step0 = (long long)n_kv * p.tiles * p.tile;
     const long long slot1 = p.own0 + ((long long)b * n_kv + j) * rg, step1 = (long long)a.own.n_seq * n_kv * rg;
-    const int in0 = v % kTile, in1 = v - b * rg;
-    auto ml_of = [&](int c) {
-        return c < p.n_parts ? ml[slot0 + c * step0 + in0] : ml[slot1 + (c - p.n_parts) * step1 + in1];
-    };
-    float top = -INFINITY;
-    for (int c = quad; c < n; c += 32) top = fmaxf(top, ml_of(c).x);
-    s_f[quad][lane] = top;
-    __syncthreads();
+    float2 w[kJoinUnroll];
+    float4 x[kJoinUnroll];
+    auto load = [&](int c) {        // parts c .. c + kJoinUnroll - 1 of this run
 #pragma unroll
-    for (int w = 0; w < 32; ++w) top = fmaxf(top, s_f[w][lane]);
+        for (int u = 0; u < kJoinUnroll; ++u) {
+            w[u] = make_float2(-INFINITY, 0.f);
+            if (c + u < c_end) {
+                const bool shared = c + u < p.n_parts;
+                const long long slot = shared ? slot0 + (c + u) * step0 : slot1 + (c + u - p.n_parts) * step1;
+                w[u] = ml[slot + (shared ? in0 : in1)];
+                x[u] = __ldcs(reinterpret_cast<const float4 *>(opart) + slot * 32 + quad * (shared ? p.tile : rg) +
+                              (shared ? in0 : in1));
+            }
+        }
+    };
+    load(c_begin);
+    float top = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kJoinUnroll; ++u) top = fmaxf(top, w[u].x);
+    for (int c = c_begin + kJoinUnroll; c < c_end; ++c)
+        top = fmaxf(top, (c < p.n_parts ? ml[slot0 + c * step0 + in0] : ml[slot1 + (c - p.n_parts) * step1 + in1]).x);
+    if (col == 0) s_top[run][lane] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(s_top[0][lane], s_top[1][lane]), fmaxf(s_top[2][lane], s_top[3][lane]));
     if (top == -INFINITY) top = 0.f;
     float l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c0 = 0; c0 < n_max; c0 += kJoinChunk) {
-        __syncthreads();        // s_f is free again
-        for (int c = quad; c < min(kJoinChunk, n - c0); c += 32) {
-            const float2 w = ml_of(c0 + c);
-            const float f = ex2_approx((w.x - top) * kScaleLog2);
-            s_f[c][lane] = f;
-            s_l[c][lane] = w.y * f;
-        }
-        __syncthreads();
-        const int end = min(n, c0 + kJoinChunk);
-        for (int c = c0; c < end; c += kJoinUnroll) {
-            float4 x[kJoinUnroll];
+    for (int c = c_begin; c < c_end; c += kJoinUnroll) {
+        if (c > c_begin) load(c);
 #pragma unroll
-            for (int u = 0; u < kJoinUnroll; ++u) {
-                const int cu = min(c + u, end - 1);
-                const long long at = cu < p.n_parts ? (slot0 + cu * step0) * 32 + quad * kTile + in0
-                                                    : (slot1 + (cu - p.n_parts) * step1) * 32 + quad * rg + in1;
-                x[u] = __ldcs(reinterpret_cast<const float4 *>(opart) + at);
-            }
-#pragma unroll
-            for (int u = 0; u < kJoinUnroll; ++u) {
-                if (c + u >= end) break;
-                const float f = s_f[c + u - c0][lane];
-                l += s_l[c + u - c0][lane];
-                o.x = fmaf(x[u].x, f, o.x);
-                o.y = fmaf(x[u].y, f, o.y);
-                o.z = fmaf(x[u].z, f, o.z);
-                o.w = fmaf(x[u].w, f, o.w);
-            }
+        for (int u = 0; u < kJoinUnroll; ++u) {
+            if (c + u >= c_end) break;
+            const float f = ex2_approx((w[u].x - top) * kScaleLog2);
+            l = fmaf(w[u].y, f, l);
+            o.x = fmaf(x[u].x, f, o.x);
+            o.y = fmaf(x[u].y, f, o.y);
+            o.z = fmaf(x[u].z, f, o.z);
+            o.w = fmaf(x[u].w, f, o.w);
         }
     }
-    const bool idle = n == 0;
-    uint2 r = make_uint2(0u, 0u);
-    if (!idle) {
+    s_o[run][col][lane] = o;
+    if (col == 0) s_l[run][lane] = l;
+    __syncthreads();
+    if (run != 0 || v >= p.n_vec) return;
+    l = s_l[0][lane];
+#pragma unroll
+    for (int i = 1; i < kJoinRuns; ++i) {
+        const float4 t = s_o[i][col][lane];
+        l += s_l[i][lane];
+        o = make_float4(o.x + t.x, o.y + t.y, o.z + t.z, o.w + t.w);
+    }
+    uint2 r = make_uint2(0u, 0u);       // idle
+    if (n > 0) {
         const __nv_bfloat162 lo = __floats2bfloat162_rn(__fdiv_rn(o.x, l), __fdiv_rn(o.y, l));
         const __nv_bfloat162 hi = __floats2bfloat162_rn(__fdiv_rn(o.z, l), __fdiv_rn(o.w, l));
         r = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
     }
-    s_out[lane][quad] = r;
-    __syncthreads();
-    const int vo = blockIdx.x * 32 + quad;      // a warp stores one vector's 256 bytes
-    if (vo < p.n_vec) {
-        const int row = vo / a.group;
-        *(reinterpret_cast<uint2 *>(a.out + (size_t)row * a.ldo + (size_t)(j * a.group + vo - row * a.group) * kHeadDim) +
-          lane) = s_out[quad][lane];
-    }
+    const int row = v / a.group;
+    *(reinterpret_cast<uint2 *>(a.out + (size_t)row * a.ldo + (size_t)(j * a.group + v - row * a.group) * kHeadDim) + quad) = r;
 }
 
-bool encode_cache(CUtensorMap *m, const void *base, int rows, int max_len, int outer, const char **why) {
-    // innermost first: an entry's 128 elements, entries, (sequence, head).  The cache
-    // is stored with its 16-byte chunks already permuted by position, as the
-    // 128-byte swizzle wants them in shared memory, so the copy permutes nothing.
-    cuuint64_t dims[3] = {cuuint64_t(kHeadDim), cuuint64_t(rows), cuuint64_t(outer)};
-    cuuint64_t strides[2] = {cuuint64_t(kHeadDim) * 2, cuuint64_t(max_len) * kHeadDim * 2};
-    cuuint32_t box[3] = {64, kTile, 1};
-    cuuint32_t ones[3] = {1, 1, 1};
+bool encode(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
+            const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle, const char **why) {
+    const cuuint32_t ones[3] = {1, 1, 1};
     const auto fn = tensor_map_encoder();
     if (!fn) {
         *why = "cuTensorMapEncodeTiled is unavailable";
         return false;
     }
     if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, ones,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
-        *why = "cuTensorMapEncodeTiled rejected the cache layout";
+        *why = "cuTensorMapEncodeTiled rejected the layout";
         return false;
     }
     return true;
+}
+
+// Innermost first: an entry's 128 elements, entries, (sequence, head).  The cache
+// is stored with its 16-byte chunks already permuted by position, as the
+// 128-byte swizzle wants them in shared memory, so the copy permutes nothing.
+bool encode_cache(CUtensorMap *m, const void *base, int rows, int max_len, int outer, const char **why) {
+    return encode(m, base, {cuuint64_t(kHeadDim), cuuint64_t(rows), cuuint64_t(outer)},
+                  {cuuint64_t(kHeadDim) * 2, cuuint64_t(max_len) * kHeadDim * 2}, {64, kTile, 1},
+                  CU_TENSOR_MAP_SWIZZLE_NONE, why);
+}
+
+// Innermost first: a head's 128 elements, heads, rows.
+bool encode_queries(CUtensorMap *m, const AttnBatchArgs &a, const char **why) {
+    return encode(m, a.q, {cuuint64_t(kHeadDim), cuuint64_t(a.own.n_kv) * a.group, cuuint64_t(a.own.n_seq) * a.R},
+                  {cuuint64_t(kHeadDim) * 2, cuuint64_t(a.ldq) * 2},
+                  {64, cuuint32_t(a.group), cuuint32_t(kTile / a.group)}, CU_TENSOR_MAP_SWIZZLE_128B, why);
 }
 
 }  // namespace
@@ -992,6 +998,7 @@ cudaError_t launch_attn_batch(const AttnBatchArgs &a, cudaStream_t s, const char
     k.opart = reinterpret_cast<float *>(base + 512);
     k.ml = reinterpret_cast<float2 *>(base + 512 + size_t(k.p.slots) * kHeadDim * sizeof(float));
     const bool e4m3 = a.own.format == kKvE4m3;
+    if (!encode_queries(&k.map[4], a, why)) return cudaErrorInvalidValue;
     if (!e4m3) {
         const KvBatch &pre = a.prefix_len > 0 ? a.prefix : a.own;
         const int pre_rows = a.prefix_len > 0 ? a.prefix_len : a.own.max_len;
@@ -1008,7 +1015,7 @@ cudaError_t launch_attn_batch(const AttnBatchArgs &a, cudaStream_t s, const char
     e = e4m3 ? launch_pdl(attn_batch_kernel<true>, grid, dim3(Form<true>::threads), kSmemBytes<true>, s, k)
              : launch_pdl(attn_batch_kernel<false>, grid, dim3(Form<false>::threads), kSmemBytes<false>, s, k);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_batch_join_kernel, dim3((k.p.n_vec + 31) / 32, a.own.n_kv), dim3(1024), 0, s, a, k.p,
+    return launch_pdl(attn_batch_join_kernel, dim3((k.p.n_vec + 31) / 32, a.own.n_kv, 32 / kJoinQuads), dim3(32 * kJoinRuns * kJoinQuads), 0, s, a, k.p,
                       (const float *)k.opart, (const float2 *)k.ml, k.next);
 }
 
