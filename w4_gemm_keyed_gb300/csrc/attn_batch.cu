@@ -47,21 +47,21 @@ constexpr int kTileBytes = 2 * kHalfBytes;
 constexpr int kRing = 4;                // items known ahead
 constexpr int kGroups = 256;            // entries of the table of own parts
 constexpr int kSoftmaxWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kQueryWarp = 10;
-constexpr int kExpandWarp = 12, kExpandWarps = 4;
+constexpr int kExpandWarp = 12, kExpandWarps = 8;
 
 // What the cache's format changes: an E4M3 tile (16 KB and 128 scale bytes) is
-// copied into a raw stage and expanded by four more warps into a bf16 tile, so
+// copied into a raw stage and expanded by eight more warps into a bf16 tile, so
 // the products are those of a bf16 cache holding the same values.
 template <bool E4M3>
 struct Form {
     static constexpr int stages = E4M3 ? 4 : 5;         // bf16 K and V tiles in shared memory
     static constexpr int raw = E4M3 ? 2 : 0;            // E4M3 tiles on their way
-    static constexpr int threads = E4M3 ? 512 : 384;
+    static constexpr int threads = E4M3 ? 640 : 384;
     static constexpr int readers = kSoftmaxWarps + 2 + (E4M3 ? kExpandWarps : 0);  // of the item ring
     // registers a thread: the softmax warps' and the others', together no more
-    // than the launch's share (128 a thread of 512, 168 of 384)
-    static constexpr int regs_softmax = E4M3 ? 184 : 208, regs_other = E4M3 ? 72 : 88;
-    static_assert(256 * regs_softmax + (threads - 256) * regs_other <= threads * (E4M3 ? 128 : 168), "register split");
+    // than the launch's share (96 a thread of 640, 168 of 384)
+    static constexpr int regs_softmax = E4M3 ? 144 : 208, regs_other = E4M3 ? 64 : 88;
+    static_assert(256 * regs_softmax + (threads - 256) * regs_other <= threads * (E4M3 ? 96 : 168), "register split");
 };
 constexpr int kRawBytes = kTile * kHeadDim;
 constexpr uint32_t kTmemCols = 512, kTmemS = 0, kTmemO = 256;
@@ -90,10 +90,13 @@ struct Plan {
 };
 
 __host__ __device__ inline int prefix_part(int prefix_len, int n_kv) {
-    // as many parts as make one item per SM when the batch is a single tile, but
-    // none shorter than kMinPrefixPart (joining parts costs traffic)
-    constexpr int kSms = 152;
-    const long long even = ((long long)prefix_len * n_kv + kSms - 1) / kSms;
+    // Parts that make about kItems items where the batch is a single tile, none
+    // shorter than kMinPrefixPart.  Few rows want many parts (each SM streams one),
+    // many rows few (each is stored and joined per vector).  12 rows over 130001
+    // entries / 512 rows over 32768, 4 and 8 heads: 152 items 57 / 546 us, 100
+    // items 56 / 522 us, 76 items 67 / 512 us.
+    constexpr int kItems = 100;
+    const long long even = ((long long)prefix_len * n_kv + kItems - 1) / kItems;
     const long long part = (even + kTile - 1) / kTile * kTile;
     return int(part < kMinPrefixPart ? kMinPrefixPart : part);
 }
@@ -149,39 +152,24 @@ __device__ __forceinline__ void regs_lower() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// A wait that gives up after kWaitNs, or once any other role of the CTA has.
-constexpr unsigned long long kWaitNs = 2000000000ull;
-
-__device__ __forceinline__ unsigned long long now_ns() {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-    return t;
-}
-
-__device__ __forceinline__ bool wait_slow(Shared *sh, uint64_t *bar, uint32_t parity, int *err) {
-    const unsigned long long t0 = now_ns();
-    do {
-        if (mbar_try_wait(bar, parity)) return true;
+// A wait that gives up after kWaitLimit polls, or once any other role of the CTA has.
+__device__ __forceinline__ bool wait_or_abort(Shared *sh, uint64_t *bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity) || mbar_try_wait(bar, parity)) return true;
+    for (uint32_t i = 0; !mbar_try_wait(bar, parity); ++i) {
+        if (i == kWaitLimit) *reinterpret_cast<volatile int *>(&sh->abort) = 1;
         if (*reinterpret_cast<volatile int *>(&sh->abort)) return false;
-    } while (now_ns() - t0 < kWaitNs);
-    set_error(err, kDevTimeout);
-    *reinterpret_cast<volatile int *>(&sh->abort) = 1;
-    return false;
-}
-
-__device__ __forceinline__ bool wait_or_abort(Shared *sh, uint64_t *bar, uint32_t parity, int *err) {
-    return mbar_try_wait(bar, parity) || mbar_try_wait(bar, parity) || wait_slow(sh, bar, parity, err);
+    }
+    return true;
 }
 
 // The same for a converged warp, with one answer.
-__device__ __forceinline__ bool warp_wait(Shared *sh, uint64_t *bar, uint32_t parity, int *err) {
-    return __all_sync(0xFFFFFFFFu, wait_or_abort(sh, bar, parity, err));
+__device__ __forceinline__ bool warp_wait(Shared *sh, uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xFFFFFFFFu, wait_or_abort(sh, bar, parity));
 }
 
-// The same without a report, for what is still in flight when a role ends.
+// The same for what is still in flight when a role ends.
 __device__ __forceinline__ void wait_drained(uint64_t *bar, uint32_t parity) {
-    const unsigned long long t0 = now_ns();
-    while (!mbar_try_wait(bar, parity) && now_ns() - t0 < kWaitNs) {
+    for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait(bar, parity); ++i) {
     }
 }
 
@@ -285,7 +273,7 @@ __device__ Item item_of(const KernelArgs &k, const Shared *sh, long long i, int 
 //   warp 8      finds the next item and streams its K and V tiles by TMA
 //   warp 10     streams the items' query vectors
 //   warp 9      issues the products
-//   warps 12-15 expand E4M3 tiles (there alone)
+//   warps 12-19 expand E4M3 tiles (there alone)
 //   warps 0-7   softmax: a thread per vector.  Items of two tiles give one tile to
 //               each group of four warps; items of one tile use the second tile's
 //               S columns so that the next key tile's scores are computed
@@ -319,7 +307,7 @@ __device__ void produce(const KernelArgs &k, Shared *sh, uint8_t *stages) {
     unsigned loaded = 0;     // tiles so far
     for (unsigned n = 0;; ++n) {
         const int slot = n % kRing;
-        if (n >= kRing && !wait_or_abort(sh, &sh->item_empty[slot], (n / kRing - 1) & 1, k.a.err)) break;
+        if (n >= kRing && !wait_or_abort(sh, &sh->item_empty[slot], (n / kRing - 1) & 1)) break;
         const unsigned taken = atomicAdd(k.next, 1u);       // the item after this one
         const Item it = item_of(k, sh, i, group_seqs);
         sh->item[slot] = it;
@@ -333,7 +321,7 @@ __device__ void produce(const KernelArgs &k, Shared *sh, uint8_t *stages) {
             const bool is_v = order_is_v(t, tiles);
             const int row = it.key0 + order_tile(t, tiles) * kTile;
             const int st = loaded % kStages;
-            if (loaded >= kStages) ok = wait_or_abort(sh, &empty[st], (loaded / kStages - 1) & 1, k.a.err);
+            if (loaded >= kStages) ok = wait_or_abort(sh, &empty[st], (loaded / kStages - 1) & 1);
             if (!ok) break;
             if constexpr (E4M3) {
                 const KvBatch &c = own ? k.a.own : k.a.prefix;
@@ -370,7 +358,7 @@ __device__ void expand_tiles(const KernelArgs &k, Shared *sh, uint8_t *stages, c
     unsigned done = 0;
     for (unsigned n = 0;; ++n) {
         const int slot = n % kRing;
-        if (!wait_or_abort(sh, &sh->item_full[slot], (n / kRing) & 1, k.a.err)) return;
+        if (!wait_or_abort(sh, &sh->item_full[slot], (n / kRing) & 1)) return;
         const Item it = sh->item[slot];
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
@@ -381,8 +369,8 @@ __device__ void expand_tiles(const KernelArgs &k, Shared *sh, uint8_t *stages, c
             const int key = order_tile(t, tiles) * kTile, valid = min(kTile, it.n_keys - key);
             const int fill = is_v ? (valid + 15) & ~15 : valid, hidden = it.lim0 + 1 - key;
             const int rs = done % kRaw, st = done % kStages;
-            if (!wait_or_abort(sh, &sh->raw_full[rs], (done / kRaw) & 1, k.a.err)) return;
-            if (done >= kStages && !wait_or_abort(sh, &sh->kv_empty[st], (done / kStages - 1) & 1, k.a.err)) return;
+            if (!wait_or_abort(sh, &sh->raw_full[rs], (done / kRaw) & 1)) return;
+            if (done >= kStages && !wait_or_abort(sh, &sh->kv_empty[st], (done / kStages - 1) & 1)) return;
             const uint8_t *src = raw + size_t(rs) * kRawBytes + 16 * group, *sc = scales + rs * kTile;
             uint8_t *dst = stages + size_t(st) * kTileBytes;
 #pragma unroll 4
@@ -423,7 +411,7 @@ __device__ void load_queries(const KernelArgs &k, Shared *sh, uint8_t *tiles) {
     int next = 0;
     for (unsigned n = 0;; ++n) {
         const int slot = n % kRing;
-        if (!wait_or_abort(sh, &sh->item_full[slot], (n / kRing) & 1, k.a.err)) break;
+        if (!wait_or_abort(sh, &sh->item_full[slot], (n / kRing) & 1)) break;
         const Item it = sh->item[slot];
         mbar_arrive(&sh->item_empty[slot]);
         if (it.n_vec == 0) break;
@@ -431,7 +419,7 @@ __device__ void load_queries(const KernelArgs &k, Shared *sh, uint8_t *tiles) {
         bool ok = true;
         for (int t = 0; t < (two ? 2 : 1) && ok; ++t) {
             const int buf = two ? t : next;
-            if (uses[buf] > 0) ok = wait_or_abort(sh, &sh->q_empty[buf], (uses[buf] - 1) & 1, k.a.err);
+            if (uses[buf] > 0) ok = wait_or_abort(sh, &sh->q_empty[buf], (uses[buf] - 1) & 1);
             if (!ok) break;
             ++uses[buf];
             const int row = it.vec0 / g + t * (k.p.tile / g);
@@ -481,7 +469,7 @@ __device__ void multiply(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint
 
     for (unsigned n = 0; ok; ++n) {
         const int slot = n % kRing;
-        if (!warp_wait(sh, &sh->item_full[slot], (n / kRing) & 1, k.a.err)) break;
+        if (!warp_wait(sh, &sh->item_full[slot], (n / kRing) & 1)) break;
         // broadcast: the same in all lanes, and known to be
         const int n_vec = __shfl_sync(0xFFFFFFFFu, sh->item[slot].n_vec, 0);
         const int n_keys = __shfl_sync(0xFFFFFFFFu, sh->item[slot].n_keys, 0);
@@ -495,19 +483,19 @@ __device__ void multiply(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint
         const int q0 = two ? 0 : next;
         auto stage_of = [&](int order) { return (taken + order) % kStages; };
         auto wait_tile = [&](int order) {
-            ok = ok && warp_wait(sh, &sh->kv_full[stage_of(order)], ((taken + order) / kStages) & 1, k.a.err);
+            ok = ok && warp_wait(sh, &sh->kv_full[stage_of(order)], ((taken + order) / kStages) & 1);
             return ok;
         };
         // S[s] = Q[qb] K(i)^T over the keys of tile i (rounded up to 16)
         auto scores = [&](int qb, int s, int i) {
             const int keys = min(kTile, n_keys - i * kTile);
             const uint32_t idesc = umma_idesc_bf16(kTile, (keys + 15) & ~15, false);
-            const uint64_t a = umma_desc_sw128(q_addr + qb * kTileBytes, 16, 1024);
-            const uint64_t b = umma_desc_sw128(st_addr + stage_of(k_order(i)) * kTileBytes, 16, 1024);
+            const uint32_t a = umma_desc_low(q_addr + qb * kTileBytes, 16);
+            const uint32_t b = umma_desc_low(st_addr + stage_of(k_order(i)) * kTileBytes, 16);
             tc_fence_after();
 #pragma unroll
             for (int d = 0; d < 8; ++d) {
-                const uint64_t off = ((d >> 2) * kHalfBytes + (d & 3) * 32) >> 4;
+                const uint32_t off = ((d >> 2) * kHalfBytes + (d & 3) * 32) >> 4;
                 tc_mma_ss(leader, tmem + kTmemS + s * kTile, a + off, b + off, idesc, d > 0);
             }
             tc_commit(leader, &sh->s_full[two && s ? 2 : s]);
@@ -516,11 +504,11 @@ __device__ void multiply(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint
         auto outputs = [&](int o, int s, int i) {
             const int steps = (min(kTile, n_keys - i * kTile) + 15) >> 4;
             const uint32_t idesc = umma_idesc_bf16(kTile, kHeadDim, true);
-            const uint64_t b = umma_desc_sw128(st_addr + stage_of(v_order(i, tiles)) * kTileBytes, kHalfBytes, 1024);
+            const uint32_t b = umma_desc_low(st_addr + stage_of(v_order(i, tiles)) * kTileBytes, kHalfBytes);
             const uint32_t d = tmem + kTmemO + o * kHeadDim, a = tmem + kTmemS + s * kTile;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                if (h == 1) ok = ok && warp_wait(sh, &sh->p_full[s][1], p_uses[s] & 1, k.a.err);
+                if (h == 1) ok = ok && warp_wait(sh, &sh->p_full[s][1], p_uses[s] & 1);
                 if (!ok) return;
                 tc_fence_after();
                 if (steps >= 4 * h + 4) {
@@ -534,14 +522,14 @@ __device__ void multiply(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint
             tc_commit(leader, &sh->o_done[o]);
         };
         auto wait_probs = [&](int s) {      // the first 64 keys' weights
-            ok = ok && warp_wait(sh, &sh->p_full[s][0], p_uses[s] & 1, k.a.err);
+            ok = ok && warp_wait(sh, &sh->p_full[s][0], p_uses[s] & 1);
             return ok;
         };
         auto release = [&](int order) { tc_commit(leader, &sh->kv_empty[stage_of(order)]); };
         auto release_q = [&](int qb) { tc_commit(leader, &sh->q_empty[qb]); };
         for (int t = 0; t < (two ? 2 : 1) && ok; ++t) {
             const int qb = two ? t : q0;
-            ok = warp_wait(sh, &sh->q_full[qb], q_uses[qb]++ & 1, k.a.err);
+            ok = warp_wait(sh, &sh->q_full[qb], q_uses[qb]++ & 1);
         }
         if (!ok || !wait_tile(k_order(0))) break;
         scores(q0, 0, 0);
@@ -640,7 +628,7 @@ __device__ void softmax(const KernelArgs &k, Shared *sh, uint32_t tmem) {
     unsigned s_uses[2] = {0, 0}, o_uses = 0;     // the second group counts its barrier in s_uses[1]
     for (unsigned n = 0;; ++n) {
         const int slot = n % kRing;
-        if (!wait_or_abort(sh, &sh->item_full[slot], (n / kRing) & 1, k.a.err)) return;
+        if (!wait_or_abort(sh, &sh->item_full[slot], (n / kRing) & 1)) return;
         const Item it = sh->item[slot];
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
@@ -655,7 +643,7 @@ __device__ void softmax(const KernelArgs &k, Shared *sh, uint32_t tmem) {
         float m = -INFINITY, l = 0.f;
         for (int i = 0; i < tiles; ++i) {
             const int buf = two ? wg : i & 1;
-            if (!wait_or_abort(sh, &sh->s_full[wg ? 2 : buf], s_uses[buf]++ & 1, k.a.err)) return;
+            if (!wait_or_abort(sh, &sh->s_full[wg ? 2 : buf], s_uses[buf]++ & 1)) return;
             bool seen = i == 0;     // whether the previous tile's product into the output is known to be done
             if (active) {
                 tc_fence_after();
@@ -696,7 +684,7 @@ __device__ void softmax(const KernelArgs &k, Shared *sh, uint32_t tmem) {
                 }
                 if (i > 0 && __any_sync(0xFFFFFFFFu, moved)) {
                     // outputs so far, once the last product into them is done
-                    if (!wait_or_abort(sh, &sh->o_done[wg], (o_uses + i - 1) & 1, k.a.err)) return;
+                    if (!wait_or_abort(sh, &sh->o_done[wg], (o_uses + i - 1) & 1)) return;
                     seen = true;
                     tc_fence_after();
 #pragma unroll
@@ -746,7 +734,7 @@ __device__ void softmax(const KernelArgs &k, Shared *sh, uint32_t tmem) {
                 mbar_arrive(&sh->p_full[buf][0]);
             }
             // every phase is waited on; this one was over long ago
-            if (!seen && !wait_or_abort(sh, &sh->o_done[wg], (o_uses + i - 1) & 1, k.a.err)) return;
+            if (!seen && !wait_or_abort(sh, &sh->o_done[wg], (o_uses + i - 1) & 1)) return;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh->p_full[buf][1]);
@@ -755,7 +743,7 @@ __device__ void softmax(const KernelArgs &k, Shared *sh, uint32_t tmem) {
         // entries that only some rows see
         const int first = max(0, it.lim0 + 1), end = it.n_keys - 1;
         const bool bad = active && it.b >= 0 && first <= end && any_nonfinite<E4M3>(k, it, first, end, lane);
-        if (!wait_or_abort(sh, &sh->o_done[wg], (o_uses - 1) & 1, k.a.err)) return;
+        if (!wait_or_abort(sh, &sh->o_done[wg], (o_uses - 1) & 1)) return;
         if (!active) continue;
         tc_fence_after();
         const bool store = v < n_here;
@@ -842,6 +830,7 @@ __global__ void __launch_bounds__(Form<E4M3>::threads, 1) attn_batch_kernel(cons
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (threadIdx.x == 0 && sh->abort) set_error(k.a.err, kDevTimeout);
     if (warp == kMmaWarp) tc_dealloc(tmem, kTmemCols);
 }
 

@@ -15,10 +15,11 @@ namespace tfk {
 //   MN-major (rows are K, 64 elements of M or N each): sbo = bytes between 8-row
 //     groups of K, lbo = bytes between 64-element blocks of M or N.
 // Bits: address >> 4 (0-13), lbo >> 4 (16-29), sbo >> 4 (32-45), version 1
-// (46), 128-byte swizzle = 2 (61-63).
-__device__ __forceinline__ uint64_t umma_desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(lbo >> 4) << 16) | (uint64_t(sbo >> 4) << 32) |
-           (uint64_t(1) << 46) | (uint64_t(2) << 61);
+// (46), 128-byte swizzle = 2 (61-63).  The upper word is the same for every
+// operand here (sbo = 1024), so operands are passed as their lower words.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t umma_desc_low(uint32_t addr, uint32_t lbo) {
+    return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
 }
 
 // Instruction descriptor, kind::f16: fp32 accumulator, bf16 operands, A
@@ -43,23 +44,25 @@ __device__ __forceinline__ uint32_t elect_one() {
 // then stay in uniform registers, where a branch would have each of them moved
 // there for each product (measured: about 130 cycles a product).
 
-// D[tmem] (+)= A * B, A and B in shared memory.
-__device__ __forceinline__ void tc_mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+// D[tmem] (+)= A * B, A and B in shared memory (lower words of their descriptors).
+__device__ __forceinline__ void tc_mma_ss(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                           uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "mov.b64 a, {%1, %6};\n\tmov.b64 b, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(leader), "n"(kDescHigh)
         : "memory");
 }
 
 // The same with A in tensor memory (lane = row, two 16-bit elements of K per column).
-__device__ __forceinline__ void tc_mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void tc_mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                           uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "mov.b64 b, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(leader), "n"(kDescHigh)
         : "memory");
 }
 
