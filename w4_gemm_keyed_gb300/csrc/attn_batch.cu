@@ -41,7 +41,7 @@ constexpr float kMaxSlack = 8.0f / kScaleLog2;
 
 constexpr int kTile = 128;              // query vectors and keys per matrix product
 constexpr int kOwnPart = 512;           // own entries per part
-constexpr int kMinPrefixPart = 1024;    // shared entries per part, at least
+constexpr int kMinPrefixPart = 512;     // shared entries per part, at least
 constexpr int kHalfBytes = kTile * 128; // 64 elements of 128 rows
 constexpr int kTileBytes = 2 * kHalfBytes;
 constexpr int kRing = 4;                // items known ahead
@@ -133,7 +133,7 @@ struct __align__(16) Shared {
     uint64_t q_full[2], q_empty[2], s_full[3], p_full[2][2], o_done[2];
     uint64_t item_full[kRing], item_empty[kRing], drain;
     Item item[kRing];
-    int before[kGroups + 1];    // own parts of the sequence groups before each
+    unsigned before[kGroups + 1];   // own parts of the sequence groups before each
     uint32_t tmem;
     int abort;
 };
@@ -223,13 +223,13 @@ __device__ int own_parts(const KernelArgs &k, int b, bool report) {
     return p < 0 ? 0 : int((p + k.a.R - 1) / kOwnPart) + 1;
 }
 
-__device__ Item item_of(const KernelArgs &k, const Shared *sh, long long i, int group_seqs) {
+__device__ Item item_of(const KernelArgs &k, const Shared *sh, unsigned i, int group_seqs) {
     Item it{};
-    const int n_kv = k.a.own.n_kv, rg = k.a.R * k.a.group;
-    const long long n_prefix = (long long)k.p.n_parts * n_kv * k.p.pairs;
+    const unsigned n_kv = k.a.own.n_kv, rg = k.a.R * k.a.group, pairs = k.p.pairs;
+    const unsigned n_prefix = k.p.n_parts * n_kv * pairs;
     if (i < n_prefix) {
-        const int pair = int(i % k.p.pairs), cj = int(i / k.p.pairs), c = cj / n_kv;
-        it.j = cj % n_kv;
+        const unsigned cj = idx_div(i, pairs), pair = i - cj * pairs, c = idx_div(cj, n_kv);
+        it.j = cj - c * n_kv;
         it.b = -1;
         it.vec0 = pair * 2 * k.p.tile;
         it.n_vec = min(2 * k.p.tile, k.p.n_vec - it.vec0);
@@ -242,9 +242,9 @@ __device__ Item item_of(const KernelArgs &k, const Shared *sh, long long i, int 
     }
     i -= n_prefix;
     const int n_groups = (k.a.own.n_seq + group_seqs - 1) / group_seqs;
-    if (i >= (long long)sh->before[n_groups] * n_kv) return it;
-    int u = int(i / n_kv);
-    it.j = int(i % n_kv);
+    if (i >= sh->before[n_groups] * n_kv) return it;
+    int u = idx_div(i, n_kv);
+    it.j = i - u * n_kv;
     int lo = 0, hi = n_groups - 1;      // last group whose parts start at or before u
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -303,15 +303,15 @@ __device__ void produce(const KernelArgs &k, Shared *sh, uint8_t *stages) {
     __syncwarp();
     if (lane != 0) return;
 
-    long long i = blockIdx.x;
+    unsigned i = blockIdx.x;
     unsigned loaded = 0;     // tiles so far
     for (unsigned n = 0;; ++n) {
         const int slot = n % kRing;
         if (n >= kRing && !wait_or_abort(sh, &sh->item_empty[slot], (n / kRing - 1) & 1)) break;
-        const unsigned taken = atomicAdd(k.next, 1u);       // the item after this one
         const Item it = item_of(k, sh, i, group_seqs);
         sh->item[slot] = it;
         mbar_arrive(&sh->item_full[slot]);
+        const unsigned taken = atomicAdd(k.next, 1u);       // the item after this one
         if (it.n_vec == 0) break;
         const bool own = it.b >= 0;
         const int tiles = (it.n_keys + kTile - 1) / kTile, outer = own ? it.b * k.a.own.n_kv + it.j : it.j;
@@ -340,7 +340,7 @@ __device__ void produce(const KernelArgs &k, Shared *sh, uint8_t *stages) {
             }
         }
         if (!ok) break;
-        i = (long long)gridDim.x + taken;
+        i = gridDim.x + taken;
     }
     // no copy outlives the CTA
     for (unsigned t = loaded > kStages ? loaded - kStages : 0; t < loaded; ++t)
@@ -665,15 +665,15 @@ __device__ void softmax(const KernelArgs &k, Shared *sh, uint32_t tmem) {
                         for (int c = 0; c < 64; ++c) x[c] = c0 + c <= last ? x[c] : 0xFF800000u;
                     }
                 };
-                auto widen = [&]() {
+                // rolled, here and below: the loop bodies are long, and instructions are
+                // fetched anew for every role that runs between
+#pragma unroll 1
+                for (int c0 = 64; c0 >= 0; c0 -= 64) {
+                    load(c0);
 #pragma unroll
                     for (int c = 0; c < 64; c += 2)
                         mt[(c >> 1) & 3] = max3(mt[(c >> 1) & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-                };
-                load(64);
-                widen();
-                load(0);
-                widen();
+                }
                 const float top = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
                 const bool moved = top > m + kMaxSlack;     // true for the first visible scores (m = -inf)
                 float scale = 1.f;
@@ -702,7 +702,7 @@ __device__ void softmax(const KernelArgs &k, Shared *sh, uint32_t tmem) {
                 const float mc = m == -INFINITY ? 0.f : m * kScaleLog2;
                 const uint64_t scale2 = pack2(kScaleLog2, kScaleLog2), shift2 = pack2(-mc, -mc);
                 uint64_t sum2[2] = {0ull, 0ull};
-#pragma unroll
+#pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     if (h == 1) load(64);
 #pragma unroll
@@ -807,6 +807,8 @@ __global__ void __launch_bounds__(Form<E4M3>::threads, 1) attn_batch_kernel(cons
         fence_mbar_init();
     }
     if (warp == kMmaWarp) tc_alloc(&sh->tmem, kTmemCols);
+    if (warp == kProducerWarp && (threadIdx.x & 31) < 5 && (!E4M3 || (threadIdx.x & 31) == 4))
+        prefetch_tensormap(&k.map[threadIdx.x & 31]);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -847,9 +849,6 @@ __global__ void __launch_bounds__(32 * kJoinRuns * kJoinQuads, 2) attn_batch_joi
     AttnBatchArgs a, Plan p, const float *opart, const float2 *ml, unsigned *next) {
     __shared__ float s_top[kJoinRuns][32], s_l[kJoinRuns][32];
     __shared__ float4 s_o[kJoinRuns][kJoinQuads][32];
-    grid_dependency_wait();     // partial results come from the preceding grid
-    grid_launch_dependents();
-    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *next = 0u;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, run = warp / kJoinQuads, col = warp % kJoinQuads;
     const int quad = blockIdx.z * kJoinQuads + col, n_kv = a.own.n_kv, rg = a.R * a.group, j = blockIdx.y;
     const int v = blockIdx.x * 32 + lane;
@@ -859,6 +858,11 @@ __global__ void __launch_bounds__(32 * kJoinRuns * kJoinQuads, 2) attn_batch_joi
         const long long pos = seq_position(a.pos, b, a.R, a.own.max_len, a.err, false);
         if (pos >= 0) n = p.n_parts + int((pos + (v - b * rg) / a.group) / kOwnPart) + 1;
     }
+    // Positions come from before the attention grid, which had waited for them when it
+    // let this grid start; the partial results come from that grid itself.
+    grid_dependency_wait();
+    grid_launch_dependents();
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *next = 0u;
     const int c_begin = n * run / kJoinRuns, c_end = n * (run + 1) / kJoinRuns;
     // vector slot of part c
     const int tile = v / p.tile, in0 = v - tile * p.tile, in1 = v - b * rg;

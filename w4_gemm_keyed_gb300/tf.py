@@ -519,28 +519,36 @@ class KVCache:
 
 
 # ---------------------------------------------------------------- a batch of sequences that continue one prompt
-def _bits16(t: torch.Tensor, name: str, cols: int):
-    """t: 2-D bf16 (or int16 bits) with unit inner stride and >= cols columns."""
-    if t.dim() != 2 or t.dtype not in (torch.bfloat16, torch.int16):
-        raise TFError(TF_ERR_INVALID_ARG, f"{name} must be a 2-D bf16 / int16 tensor, got {tuple(t.shape)} {t.dtype}")
-    if t.stride(1) != 1 or t.shape[1] < cols:
-        raise TFError(TF_ERR_INVALID_ARG, f"{name} must have unit inner stride and >= {cols} columns")
+# These calls are as short as the kernels they launch, so each tensor is looked at
+# once, in few Python operations, and messages are made only on refusal.
+_BITS16 = (torch.bfloat16, torch.int16)
 
 
-def _bits16_out(t, name: str, rows: int, cols: int, device):
-    """t, or a new bf16 [rows][cols] tensor when it is None."""
-    if t is None:
-        return torch.empty((rows, cols), dtype=torch.bfloat16, device=device)
-    _bits16(t, name, cols)
-    if t.device != device or t.shape[0] < rows:
-        raise TFError(TF_ERR_INVALID_ARG, f"{name} must hold >= {rows} rows on {device}")
-    return t
+def _refuse(message: str):
+    raise TFError(TF_ERR_INVALID_ARG, message)
+
+
+def _bits16(t: torch.Tensor, name: str, rows: int, cols: int, device) -> int:
+    """Row stride of t: bf16 (or int16 bits) [>= rows][>= cols] with unit inner stride on `device`."""
+    shape = t.shape
+    if (len(shape) != 2 or t.dtype not in _BITS16 or t.device != device or shape[0] < rows or shape[1] < cols
+            or t.stride(1) != 1):
+        _refuse(f"{name} must be a bf16 / int16 [>= {rows}][>= {cols}] tensor with unit inner stride on {device}, "
+                f"got {tuple(shape)} {t.dtype} on {t.device}")
+    return t.stride(0)
 
 
 def _positions(pos: torch.Tensor, device) -> int:
-    if pos.dim() != 1 or pos.dtype != torch.int64 or pos.device != device or not pos.is_contiguous() or not len(pos):
-        raise TFError(TF_ERR_INVALID_ARG, f"pos must be a contiguous 1-D int64 tensor on {device}, one per sequence")
-    return pos.shape[0]
+    shape = pos.shape
+    if (len(shape) != 1 or pos.dtype is not torch.int64 or pos.device != device or not pos.is_contiguous()
+            or not shape[0]):
+        _refuse(f"pos must be a contiguous 1-D int64 tensor on {device}, one per sequence")
+    return shape[0]
+
+
+def _cuda(device):
+    if device.type != "cuda":
+        _refuse(f"expected CUDA tensors, got one on {device}")
 
 
 def rope_turns(rot_dim: int, theta: float = 10000.0, inv_freq=None, device="cuda") -> torch.Tensor:
@@ -570,29 +578,39 @@ def qk_norm_rope(x: torch.Tensor, n_q: int, n_kv: int, pos: torch.Tensor, turns:
     turns by position pos[b] + pos_offset + r."""
     n_v = n_kv if n_v is None else n_v
     cols = (n_q + n_kv + n_v) * HEAD_DIM
-    if x.dtype == torch.float32:
-        if x.dim() != 2 or x.stride(1) != 1 or x.shape[1] < cols:
-            raise TFError(TF_ERR_INVALID_ARG, f"x must be 2-D with unit inner stride and >= {cols} columns")
-    else:
-        _bits16(x, "x", cols)
-    B = _positions(pos, x.device)
-    rows = x.shape[0]
+    dev, shape = x.device, x.shape
+    _cuda(dev)
+    fp32 = x.dtype is torch.float32
+    if len(shape) != 2 or not (fp32 or x.dtype in _BITS16) or shape[1] < cols or x.stride(1) != 1:
+        _refuse(f"x must be fp32 or bf16 / int16 [rows][>= {cols}] with unit inner stride, got {tuple(shape)} {x.dtype}")
+    B, rows = _positions(pos, dev), shape[0]
     if rows % B or not rows:
-        raise TFError(TF_ERR_INVALID_ARG, f"{rows} rows are not a positive multiple of {B} sequences")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and (w.dtype not in (torch.bfloat16, torch.int16) or w.numel() != HEAD_DIM or
-                              not w.is_contiguous() or w.device != x.device):
-            raise TFError(TF_ERR_INVALID_ARG, f"{name} must be {HEAD_DIM} contiguous bf16 values on {x.device}")
+        _refuse(f"{rows} rows are not a positive multiple of {B} sequences")
+    wq = wk = turned = None
     rot = 0
+    if q_weight is not None:
+        wq = _head_weight(q_weight, "q_weight", dev)
+    if k_weight is not None:
+        wk = _head_weight(k_weight, "k_weight", dev)
     if turns is not None:
-        if turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous() or turns.device != x.device:
-            raise TFError(TF_ERR_INVALID_ARG, f"turns must be a contiguous 1-D int64 tensor on {x.device}")
-        rot = 2 * turns.shape[0]
-    out = _bits16_out(out, "out", rows, cols, x.device)
-    _check(load().tf_qk_norm_rope(_ptr(x), x.dtype == torch.float32, x.stride(0), B, rows // B, n_q, n_kv, n_v,
-                                  _ptr(q_weight), _ptr(k_weight), eps, _ptr(turns), rot, adjacent, _ptr(pos),
-                                  pos_offset, _ptr(out), out.stride(0), _stream(stream)))
+        if turns.dtype is not torch.int64 or turns.dim() != 1 or not turns.is_contiguous() or turns.device != dev:
+            _refuse(f"turns must be a contiguous 1-D int64 tensor on {dev}")
+        rot, turned = 2 * turns.shape[0], turns.data_ptr()
+    if out is None:
+        out, ldo = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev), cols
+    else:
+        ldo = _bits16(out, "out", rows, cols, dev)
+    st = load().tf_qk_norm_rope(x.data_ptr(), fp32, x.stride(0), B, rows // B, n_q, n_kv, n_v, wq, wk, eps, turned, rot,
+                                adjacent, pos.data_ptr(), pos_offset, out.data_ptr(), ldo, _stream(stream))
+    if st:
+        _check(st)
     return out
+
+
+def _head_weight(w: torch.Tensor, name: str, device) -> int:
+    if w.dtype not in _BITS16 or w.numel() != HEAD_DIM or not w.is_contiguous() or w.device != device:
+        _refuse(f"{name} must be {HEAD_DIM} contiguous bf16 values on {device}")
+    return w.data_ptr()
 
 
 class KVBatch:
@@ -612,6 +630,7 @@ class KVBatch:
         self._bind()
 
     def _bind(self):
+        self.device = self.k.device
         self._c = KVBatchC(_ptr(self.k), _ptr(self.v), _ptr(self.k_scale), _ptr(self.v_scale), self.n_seq, self.n_kv,
                            self.max_len, KV_FORMATS[self.fmt])
 
@@ -626,43 +645,51 @@ class KVBatch:
 
     def _rows(self, n: int) -> int:
         if n % self.n_seq or not n:
-            raise TFError(TF_ERR_INVALID_ARG, f"{n} rows are not a positive multiple of {self.n_seq} sequences")
+            _refuse(f"{n} rows are not a positive multiple of {self.n_seq} sequences")
         return n // self.n_seq
 
-    def _pos(self, pos: torch.Tensor):
-        if _positions(pos, self.k.device) != self.n_seq:
-            raise TFError(TF_ERR_INVALID_ARG, f"pos must hold {self.n_seq} positions")
+    def _pos(self, pos: torch.Tensor) -> int:
+        if _positions(pos, self.device) != self.n_seq:
+            _refuse(f"pos must hold {self.n_seq} positions")
+        return pos.data_ptr()
 
     def store(self, k_new: torch.Tensor, v_new: torch.Tensor, pos: torch.Tensor, ws: torch.Tensor = None, stream=None):
         """Entries pos[b] + r of sequence b from rows b*R + r of k_new, v_new (bf16
         [n_seq*R][n_kv*128]); returns the workspace whose status the call sets."""
-        cols = self.n_kv * HEAD_DIM
-        _bits16(k_new, "k_new", cols)
-        _bits16(v_new, "v_new", cols)
-        if k_new.shape[0] != v_new.shape[0] or k_new.stride(0) != v_new.stride(0):
-            raise TFError(TF_ERR_INVALID_ARG, "k_new and v_new must have the same rows and row stride")
-        R = self._rows(k_new.shape[0])
-        self._pos(pos)
+        n, cols, dev = k_new.shape[0], self.n_kv * HEAD_DIM, self.device
+        ld = _bits16(k_new, "k_new", 1, cols, dev)
+        if _bits16(v_new, "v_new", 1, cols, dev) != ld or v_new.shape[0] != n:
+            _refuse("k_new and v_new must have the same rows and row stride")
+        R, at = self._rows(n), self._pos(pos)
         if ws is None:
-            ws = workspace(256, device=self.k.device)
-        _check(load().tf_kv_store(self._c, _ptr(k_new), _ptr(v_new), k_new.stride(0), R, _ptr(pos), _ptr(ws),
-                                  ws.numel(), _stream(stream)))
+            ws = workspace(256, device=dev)
+        st = load().tf_kv_store(self._c, k_new.data_ptr(), v_new.data_ptr(), ld, R, at, _ptr(ws), ws.numel(),
+                                _stream(stream))
+        if st:
+            _check(st)
         return ws
 
     def load(self, pos: torch.Tensor, R: int, k: torch.Tensor = None, v: torch.Tensor = None,
              ws: torch.Tensor = None, stream=None):
         """(k, v) bf16 [n_seq*R][n_kv*128]: the values of entries pos[b] + r."""
-        cols = self.n_kv * HEAD_DIM
-        dev = self.k.device
-        self._pos(pos)
-        k = _bits16_out(k, "k", self.n_seq * R, cols, dev)
-        v = _bits16_out(v, "v", self.n_seq * R, cols, dev)
-        if k.stride(0) != v.stride(0):
-            raise TFError(TF_ERR_INVALID_ARG, "k and v must have the same row stride")
+        n, cols, dev = self.n_seq * R, self.n_kv * HEAD_DIM, self.device
+        at = self._pos(pos)
+        if not 0 < R <= self.max_len:
+            _refuse(f"R={R} outside [1, max_len={self.max_len}]")
+        if k is None and v is None:
+            k = torch.empty((n, cols), dtype=torch.bfloat16, device=dev)
+            v, ld = torch.empty_like(k), cols
+        else:
+            k = torch.empty_like(v) if k is None else k
+            v = torch.empty_like(k) if v is None else v
+            ld = _bits16(k, "k", n, cols, dev)
+            if _bits16(v, "v", n, cols, dev) != ld:
+                _refuse("k and v must have the same row stride")
         if ws is None:
             ws = workspace(256, device=dev)
-        _check(load().tf_kv_load(self._c, _ptr(pos), R, _ptr(k), _ptr(v), k.stride(0), _ptr(ws), ws.numel(),
-                                 _stream(stream)))
+        st = load().tf_kv_load(self._c, at, R, k.data_ptr(), v.data_ptr(), ld, _ptr(ws), ws.numel(), _stream(stream))
+        if st:
+            _check(st)
         return k, v
 
     def attention_workspace_bytes(self, group: int, R: int, prefix_len: int = 0) -> int:
@@ -673,17 +700,20 @@ class KVBatch:
         """bf16 [n_seq*R][n_kv*group*128]: rows at own positions pos[b] + r attending over
         entries 0..prefix_len-1 of the one-sequence batch `prefix` and 0..pos[b]+r of
         their own; idle sequences' rows are zeros."""
-        cols = self.n_kv * group * HEAD_DIM
-        dev = self.k.device
-        _bits16(q, "q", cols)
-        R = self._rows(q.shape[0])
-        self._pos(pos)
-        out = _bits16_out(out, "out", q.shape[0], cols, dev)
+        cols, dev, n = self.n_kv * group * HEAD_DIM, self.device, q.shape[0]
+        ldq = _bits16(q, "q", 1, cols, dev)
+        R, at = self._rows(n), self._pos(pos)
+        if out is None:
+            out, ldo = torch.empty((n, cols), dtype=torch.bfloat16, device=dev), cols
+        else:
+            ldo = _bits16(out, "out", n, cols, dev)
         if ws is None:
             ws = workspace(self.attention_workspace_bytes(group, R, prefix_len), device=dev)
-        _check(load().tf_attention_batch(self._c, prefix._c if prefix is not None else None, prefix_len, group, _ptr(q),
-                                         q.stride(0), R, _ptr(pos), _ptr(out), out.stride(0), _ptr(ws), ws.numel(),
-                                         _stream(stream)))
+        st = load().tf_attention_batch(self._c, prefix._c if prefix is not None else None, prefix_len, group,
+                                       q.data_ptr(), ldq, R, at, out.data_ptr(), ldo, _ptr(ws), ws.numel(),
+                                       _stream(stream))
+        if st:
+            _check(st)
         return out
 
 
