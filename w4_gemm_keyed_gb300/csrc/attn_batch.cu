@@ -182,24 +182,6 @@ __device__ __forceinline__ int order_tile(int t, int n) {
     return t == 2 * n - 1 ? n - 1 : (t == 0 ? 0 : (t % 2 == 0 ? t / 2 - 1 : (t + 1) / 2));
 }
 
-// Two fp32 operations in one instruction, each rounded as the single one is.
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-    return uint64_t(__float_as_uint(a)) | (uint64_t(__float_as_uint(b)) << 32);
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
-    a = __uint_as_float(uint32_t(v));
-    b = __uint_as_float(uint32_t(v >> 32));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));

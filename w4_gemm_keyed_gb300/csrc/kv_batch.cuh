@@ -83,6 +83,30 @@ __device__ __forceinline__ void e4m3_expand(uint32_t w, uint32_t factor, uint32_
     hi = mul_bf16x2((w & 0x80008000u) | ((w >> 4) & 0x07F007F0u), factor);
 }
 
+// Two fp32 operations in one instruction, each rounded as the single one is.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    return uint64_t(__float_as_uint(a)) | (uint64_t(__float_as_uint(b)) << 32);
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
+    a = __uint_as_float(uint32_t(v));
+    b = __uint_as_float(uint32_t(v >> 32));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 struct QkNormRopeArgs {
     const void *x;          // fp32 or bf16 [n_seq * R][ldx]
     int x_fp32, ldx;
