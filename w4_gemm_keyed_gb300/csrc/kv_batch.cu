@@ -39,7 +39,7 @@ __device__ __forceinline__ uint32_t narrow2(uint64_t v) {
 }
 
 template <bool FP32>
-__global__ void __launch_bounds__(256) qk_norm_rope_kernel(QkNormRopeArgs a, int heads_per_warp, int runs) {
+__global__ void __launch_bounds__(256, 3) qk_norm_rope_kernel(QkNormRopeArgs a, int heads_per_warp, int runs) {
     grid_dependency_wait();     // x comes from the preceding grid
     grid_launch_dependents();
     const int lane = threadIdx.x & 31, half = lane >> 4, sub = lane & 15;
@@ -145,26 +145,62 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(QkNormRopeArgs a, int
 }
 
 // ------------------------------------------------------- cache writes and reads
-// A CTA takes some rows of one sequence, all heads, K and V; 16 lanes move one
-// vector (K or V of one row and head), 16 bytes of bf16 each, four vectors in
-// flight.  Consecutive half warps take consecutive heads of a row (the rows are
-// contiguous); a head's entries of consecutive rows are written by one CTA.
-constexpr int kVecUnroll = 4, kVecThreads = 256, kVecHalfWarps = kVecThreads / 16;
+// A CTA takes some rows of one sequence, all heads; 16 lanes move a row's K and V
+// vectors of one head, 16 bytes of bf16 a lane each, two heads in flight.
+// Consecutive half warps take consecutive heads of a row (which the rows hold
+// together); a head's entries of consecutive rows are one CTA's.
+constexpr int kVecUnroll = 2, kVecThreads = 256, kVecHalfWarps = kVecThreads / 16;
 
-int rows_per_cta(int n_kv) { return n_kv < 32 ? 32 / n_kv : 1; }
+int rows_per_cta(int n_kv) { return n_kv < 64 ? 64 / n_kv : 1; }
 
-struct Vec {
-    int j, which, r;        // head, K or V, row within the CTA's
-    bool any;
+// The (row, head) places of one half warp, in steps of kVecHalfWarps.
+struct Places {
+    int r, j, dr, dj, n_kv;
+    __device__ __forceinline__ explicit Places(int n_kv_) : n_kv(n_kv_) {
+        const int at = threadIdx.x >> 4;
+        r = at / n_kv;
+        j = at - r * n_kv;
+        dr = kVecHalfWarps / n_kv;
+        dj = kVecHalfWarps - dr * n_kv;
+    }
+    __device__ __forceinline__ void step() {
+        r += dr;
+        j += dj;
+        if (j >= n_kv) {
+            j -= n_kv;
+            ++r;
+        }
+    }
 };
-__device__ __forceinline__ Vec vec_of(int u, int n_kv, int rows) {
-    Vec v;
-    v.any = u < 2 * rows * n_kv;
-    v.which = u >= rows * n_kv;
-    if (v.which) u -= rows * n_kv;
-    v.r = idx_div(u, n_kv);
-    v.j = u - v.r * n_kv;
-    return v;
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// One vector's 16-byte share of a lane -> its eight codes; s: the vector's scale byte.
+__device__ __forceinline__ uint2 e4m3_codes(const uint4 &x, int &s) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t m = max_u16x2(max_u16x2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), max_u16x2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+    const uint32_t peers = 0xFFFFu << (threadIdx.x & 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = max_u16x2(m, __shfl_xor_sync(peers, m, o));
+    s = e4m3_scale_byte(max(m & 0xFFFFu, m >> 16));
+    if (s == kScaleNan) return make_uint2(0u, 0u);
+    const float inv = __uint_as_float(uint32_t(254 - s) << 23);    // 2^-e
+    uint32_t code[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        // bytes 0, 2 | 1, 3 of a word hold elements 0, 1 | 2, 3
+        const uint32_t a = w[2 * e], d = w[2 * e + 1];
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(__uint_as_float(a << 16) * inv, __uint_as_float(d << 16) * inv),
+                                                     __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+            make_float2(__uint_as_float(a & 0xFFFF0000u) * inv, __uint_as_float(d & 0xFFFF0000u) * inv), __NV_SATFINITE, __NV_E4M3);
+        code[e] = lo | (hi << 16);
+    }
+    return make_uint2(code[0], code[1]);
 }
 
 template <bool E4M3>
@@ -175,52 +211,39 @@ __global__ void __launch_bounds__(kVecThreads) kv_store_kernel(KvBatch c, const 
     const int lane = threadIdx.x & 15, b = blockIdx.y, r0 = blockIdx.x * rows_cta, rows = min(rows_cta, R - r0);
     const long long p = seq_position(pos, b, R, c.max_len, err, blockIdx.x == 0 && threadIdx.x == 0);
     if (p < 0) return;
-    const size_t row0 = (size_t)b * R + r0;
-    for (int u0 = threadIdx.x >> 4; u0 < 2 * rows * c.n_kv; u0 += kVecUnroll * kVecHalfWarps) {
-        uint4 x[kVecUnroll];
+    const size_t row0 = ((size_t)b * R + r0) * ld + 8 * lane;
+    const long long t0 = p + r0;
+    Places at(c.n_kv);
+    while (at.r < rows) {
+        uint4 x[kVecUnroll][2];
+        size_t entry[kVecUnroll];
+        bool any[kVecUnroll];
 #pragma unroll
         for (int i = 0; i < kVecUnroll; ++i) {
-            const Vec u = vec_of(u0 + i * kVecHalfWarps, c.n_kv, rows);
-            if (u.any)
-                x[i] = *reinterpret_cast<const uint4 *>((u.which ? v_new : k_new) + (row0 + u.r) * ld + u.j * kHeadDim + 8 * lane);
+            any[i] = at.r < rows;
+            if (any[i]) {
+                const size_t from = row0 + (size_t)at.r * ld + at.j * kHeadDim;
+                x[i][0] = *reinterpret_cast<const uint4 *>(k_new + from);
+                x[i][1] = *reinterpret_cast<const uint4 *>(v_new + from);
+                entry[i] = (size_t)(b * c.n_kv + at.j) * c.max_len + (size_t)(t0 + at.r);
+            }
+            at.step();
         }
 #pragma unroll
         for (int i = 0; i < kVecUnroll; ++i) {
-            const Vec u = vec_of(u0 + i * kVecHalfWarps, c.n_kv, rows);
-            if (!u.any) break;
-            const long long t = p + r0 + u.r;
-            const size_t entry = ((size_t)b * c.n_kv + u.j) * c.max_len + (size_t)t;
+            if (!any[i]) break;
             if constexpr (!E4M3) {
-                uint16_t *dst = static_cast<uint16_t *>(u.which ? c.v : c.k) + entry * kHeadDim + ((lane ^ int(t & 7)) << 3);
-                *reinterpret_cast<uint4 *>(dst) = x[i];
+                const size_t to = entry[i] * kHeadDim + ((lane ^ int(entry[i] & 7)) << 3);     // max_len % 8 = 0
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(c.k) + to) = x[i][0];
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(c.v) + to) = x[i][1];
             } else {
-                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                uint32_t m = 0;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) m = max(m, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
-                const uint32_t peers = 0xFFFFu << (threadIdx.x & 16);
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(peers, m, o));
-                const int s = e4m3_scale_byte(m);
-                uint32_t code[2] = {0u, 0u};
-                if (s != kScaleNan) {
-                    const float inv = __uint_as_float(uint32_t(254 - s) << 23);    // 2^-e
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        // bytes 0, 2 | 1, 3 of a word hold elements 0, 1 | 2, 3
-                        const uint32_t a = w[2 * e], d = w[2 * e + 1];
-                        const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-                            make_float2(__uint_as_float(a << 16) * inv, __uint_as_float(d << 16) * inv), __NV_SATFINITE, __NV_E4M3);
-                        const uint32_t hi =
-                            __nv_cvt_float2_to_fp8x2(make_float2(__uint_as_float(a & 0xFFFF0000u) * inv,
-                                                                 __uint_as_float(d & 0xFFFF0000u) * inv),
-                                                     __NV_SATFINITE, __NV_E4M3);
-                        code[e] = lo | (hi << 16);
-                    }
-                }
-                uint8_t *dst = static_cast<uint8_t *>(u.which ? c.v : c.k) + entry * kHeadDim + 16 * (lane & 7) + 8 * (lane >> 3);
-                *reinterpret_cast<uint2 *>(dst) = make_uint2(code[0], code[1]);
-                if (lane == 0) (u.which ? c.v_scale : c.k_scale)[entry] = uint8_t(s);
+                const size_t to = entry[i] * kHeadDim + 16 * (lane & 7) + 8 * (lane >> 3);
+                int sk, sv;
+                const uint2 ck = e4m3_codes(x[i][0], sk), cv = e4m3_codes(x[i][1], sv);
+                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(c.k) + to) = ck;
+                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(c.v) + to) = cv;
+                if (lane == 0) c.k_scale[entry[i]] = uint8_t(sk);
+                if (lane == 1) c.v_scale[entry[i]] = uint8_t(sv);
             }
         }
     }
@@ -233,40 +256,49 @@ __global__ void __launch_bounds__(kVecThreads) kv_load_kernel(KvBatch c, const i
     grid_launch_dependents();
     const int lane = threadIdx.x & 15, b = blockIdx.y, r0 = blockIdx.x * rows_cta, rows = min(rows_cta, R - r0);
     const long long p = seq_position(pos, b, R, c.max_len, err, blockIdx.x == 0 && threadIdx.x == 0);
-    const size_t row0 = (size_t)b * R + r0;
-    for (int u0 = threadIdx.x >> 4; u0 < 2 * rows * c.n_kv; u0 += kVecUnroll * kVecHalfWarps) {
-        uint4 x[kVecUnroll];
-        uint32_t f[kVecUnroll];
+    const size_t row0 = ((size_t)b * R + r0) * ld + 8 * lane;
+    const long long t0 = p + r0;
+    Places at(c.n_kv);
+    while (at.r < rows) {
+        uint4 x[kVecUnroll][2];
+        uint32_t f[kVecUnroll][2];
+        size_t to[kVecUnroll];
+        bool any[kVecUnroll];
 #pragma unroll
         for (int i = 0; i < kVecUnroll; ++i) {
-            const Vec u = vec_of(u0 + i * kVecHalfWarps, c.n_kv, rows);
-            x[i] = make_uint4(0u, 0u, 0u, 0u);
-            f[i] = 0u;
-            if (!u.any || p < 0) continue;
-            const long long t = p + r0 + u.r;
-            const size_t entry = ((size_t)b * c.n_kv + u.j) * c.max_len + (size_t)t;
-            if constexpr (!E4M3) {
-                x[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(u.which ? c.v : c.k) + entry * kHeadDim +
-                                                        ((lane ^ int(t & 7)) << 3));
-            } else {
-                const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(u.which ? c.v : c.k) +
-                                                                 entry * kHeadDim + 16 * (lane & 7) + 8 * (lane >> 3));
-                x[i].x = w.x;
-                x[i].y = w.y;
-                f[i] = (u.which ? c.v_scale : c.k_scale)[entry];
+            any[i] = at.r < rows;
+            x[i][0] = x[i][1] = make_uint4(0u, 0u, 0u, 0u);
+            to[i] = row0 + (size_t)at.r * ld + at.j * kHeadDim;
+            if (any[i] && p >= 0) {
+                const size_t entry = (size_t)(b * c.n_kv + at.j) * c.max_len + (size_t)(t0 + at.r);
+                if constexpr (!E4M3) {
+                    const size_t from = entry * kHeadDim + ((lane ^ int(entry & 7)) << 3);      // max_len % 8 = 0
+                    x[i][0] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(c.k) + from);
+                    x[i][1] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(c.v) + from);
+                } else {
+                    const size_t from = entry * kHeadDim + 16 * (lane & 7) + 8 * (lane >> 3);
+                    const uint2 wk = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(c.k) + from);
+                    const uint2 wv = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(c.v) + from);
+                    x[i][0].x = wk.x, x[i][0].y = wk.y, x[i][1].x = wv.x, x[i][1].y = wv.y;
+                    f[i][0] = c.k_scale[entry];
+                    f[i][1] = c.v_scale[entry];
+                }
             }
+            at.step();
         }
 #pragma unroll
         for (int i = 0; i < kVecUnroll; ++i) {
-            const Vec u = vec_of(u0 + i * kVecHalfWarps, c.n_kv, rows);
-            if (!u.any) break;
-            uint4 y = x[i];
-            if (E4M3 && p >= 0) {
-                const uint32_t factor = e4m3_factor(f[i]);
-                e4m3_expand(x[i].x, factor, y.x, y.y);
-                e4m3_expand(x[i].y, factor, y.z, y.w);
+            if (!any[i]) break;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                uint4 y = x[i][w];
+                if (E4M3 && p >= 0) {
+                    const uint32_t factor = e4m3_factor(f[i][w]);
+                    e4m3_expand(x[i][w].x, factor, y.x, y.y);
+                    e4m3_expand(x[i][w].y, factor, y.z, y.w);
+                }
+                *reinterpret_cast<uint4 *>((w ? v_out : k_out) + to[i]) = y;
             }
-            *reinterpret_cast<uint4 *>((u.which ? v_out : k_out) + (row0 + u.r) * ld + u.j * kHeadDim + 8 * lane) = y;
         }
     }
 }
