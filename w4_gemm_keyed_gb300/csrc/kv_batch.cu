@@ -39,7 +39,7 @@ __device__ __forceinline__ uint32_t narrow2(uint64_t v) {
 }
 
 template <bool FP32>
-__global__ void __launch_bounds__(256, 3) qk_norm_rope_kernel(QkNormRopeArgs a, int heads_per_warp, int runs) {
+__global__ void __launch_bounds__(256, FP32 ? 2 : 3) qk_norm_rope_kernel(QkNormRopeArgs a, int heads_per_warp, int runs) {
     grid_dependency_wait();     // x comes from the preceding grid
     grid_launch_dependents();
     const int lane = threadIdx.x & 31, half = lane >> 4, sub = lane & 15;

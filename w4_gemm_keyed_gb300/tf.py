@@ -531,24 +531,17 @@ def _refuse(message: str):
 def _bits16(t: torch.Tensor, name: str, rows: int, cols: int, device) -> int:
     """Row stride of t: bf16 (or int16 bits) [>= rows][>= cols] with unit inner stride on `device`."""
     shape = t.shape
-    if (len(shape) != 2 or t.dtype not in _BITS16 or t.device != device or shape[0] < rows or shape[1] < cols
-            or t.stride(1) != 1):
+    ld, unit = t.stride() if len(shape) == 2 else (0, 0)
+    if unit != 1 or t.dtype not in _BITS16 or shape[0] < rows or shape[1] < cols or t.device != device:
         _refuse(f"{name} must be a bf16 / int16 [>= {rows}][>= {cols}] tensor with unit inner stride on {device}, "
                 f"got {tuple(shape)} {t.dtype} on {t.device}")
-    return t.stride(0)
+    return ld
 
 
 def _positions(pos: torch.Tensor, device) -> int:
-    shape = pos.shape
-    if (len(shape) != 1 or pos.dtype is not torch.int64 or pos.device != device or not pos.is_contiguous()
-            or not shape[0]):
+    if pos.dtype is not torch.int64 or pos.stride() != (1,) or pos.device != device or not pos.numel():
         _refuse(f"pos must be a contiguous 1-D int64 tensor on {device}, one per sequence")
-    return shape[0]
-
-
-def _cuda(device):
-    if device.type != "cuda":
-        _refuse(f"expected CUDA tensors, got one on {device}")
+    return pos.numel()
 
 
 def rope_turns(rot_dim: int, theta: float = 10000.0, inv_freq=None, device="cuda") -> torch.Tensor:
@@ -579,10 +572,11 @@ def qk_norm_rope(x: torch.Tensor, n_q: int, n_kv: int, pos: torch.Tensor, turns:
     n_v = n_kv if n_v is None else n_v
     cols = (n_q + n_kv + n_v) * HEAD_DIM
     dev, shape = x.device, x.shape
-    _cuda(dev)
     fp32 = x.dtype is torch.float32
-    if len(shape) != 2 or not (fp32 or x.dtype in _BITS16) or shape[1] < cols or x.stride(1) != 1:
-        _refuse(f"x must be fp32 or bf16 / int16 [rows][>= {cols}] with unit inner stride, got {tuple(shape)} {x.dtype}")
+    ldx, unit = x.stride() if len(shape) == 2 else (0, 0)
+    if unit != 1 or not (fp32 or x.dtype in _BITS16) or shape[1] < cols or not x.is_cuda:
+        _refuse(f"x must be a CUDA fp32 or bf16 / int16 [rows][>= {cols}] tensor with unit inner stride, got "
+                f"{tuple(shape)} {x.dtype} on {dev}")
     B, rows = _positions(pos, dev), shape[0]
     if rows % B or not rows:
         _refuse(f"{rows} rows are not a positive multiple of {B} sequences")
@@ -593,14 +587,14 @@ def qk_norm_rope(x: torch.Tensor, n_q: int, n_kv: int, pos: torch.Tensor, turns:
     if k_weight is not None:
         wk = _head_weight(k_weight, "k_weight", dev)
     if turns is not None:
-        if turns.dtype is not torch.int64 or turns.dim() != 1 or not turns.is_contiguous() or turns.device != dev:
+        if turns.dtype is not torch.int64 or turns.stride() != (1,) or turns.device != dev:
             _refuse(f"turns must be a contiguous 1-D int64 tensor on {dev}")
-        rot, turned = 2 * turns.shape[0], turns.data_ptr()
+        rot, turned = 2 * turns.numel(), turns.data_ptr()
     if out is None:
         out, ldo = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev), cols
     else:
         ldo = _bits16(out, "out", rows, cols, dev)
-    st = load().tf_qk_norm_rope(x.data_ptr(), fp32, x.stride(0), B, rows // B, n_q, n_kv, n_v, wq, wk, eps, turned, rot,
+    st = load().tf_qk_norm_rope(x.data_ptr(), fp32, ldx, B, rows // B, n_q, n_kv, n_v, wq, wk, eps, turned, rot,
                                 adjacent, pos.data_ptr(), pos_offset, out.data_ptr(), ldo, _stream(stream))
     if st:
         _check(st)
@@ -608,7 +602,7 @@ def qk_norm_rope(x: torch.Tensor, n_q: int, n_kv: int, pos: torch.Tensor, turns:
 
 
 def _head_weight(w: torch.Tensor, name: str, device) -> int:
-    if w.dtype not in _BITS16 or w.numel() != HEAD_DIM or not w.is_contiguous() or w.device != device:
+    if w.dtype not in _BITS16 or w.numel() != HEAD_DIM or w.stride() != (1,) or w.device != device:
         _refuse(f"{name} must be {HEAD_DIM} contiguous bf16 values on {device}")
     return w.data_ptr()
 
