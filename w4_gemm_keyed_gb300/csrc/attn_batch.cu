@@ -46,7 +46,7 @@ constexpr int kHalfBytes = kTile * 128; // 64 elements of 128 rows
 constexpr int kTileBytes = 2 * kHalfBytes;
 constexpr int kRing = 4;                // items known ahead
 constexpr int kGroups = 256;            // entries of the table of own parts
-constexpr int kSoftmaxWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kQueryWarp = 10;
+constexpr int kSoftmaxWarps = 8, kProducerWarp = 8, kMmaWarp = 9;
 constexpr int kExpandWarp = 12, kExpandWarps = 8;
 
 // What the cache's format changes: an E4M3 tile (16 KB and 128 scale bytes) is
@@ -57,7 +57,7 @@ struct Form {
     static constexpr int stages = E4M3 ? 4 : 5;         // bf16 K and V tiles in shared memory
     static constexpr int raw = E4M3 ? 2 : 0;            // E4M3 tiles on their way
     static constexpr int threads = E4M3 ? 640 : 384;
-    static constexpr int readers = kSoftmaxWarps + 2 + (E4M3 ? kExpandWarps : 0);  // of the item ring
+    static constexpr int readers = kSoftmaxWarps + 1 + (E4M3 ? kExpandWarps : 0);  // of the item ring
     // registers a thread: the softmax warps' and the others', together no more
     // than the launch's share (96 a thread of 640, 168 of 384)
     static constexpr int regs_softmax = E4M3 ? 144 : 208, regs_other = E4M3 ? 64 : 88;
@@ -252,8 +252,8 @@ __device__ Item item_of(const KernelArgs &k, const Shared *sh, unsigned i, int g
 
 // ------------------------------------------------------------------ roles
 // One CTA per SM takes items from a common counter.
-//   warp 8      finds the next item and streams its K and V tiles by TMA
-//   warp 10     streams the items' query vectors
+//   warp 8      finds the next item and streams its query vectors and its K and V
+//               tiles by TMA
 //   warp 9      issues the products
 //   warps 12-19 expand E4M3 tiles (there alone)
 //   warps 0-7   softmax: a thread per vector.  Items of two tiles give one tile to
@@ -262,7 +262,7 @@ __device__ Item item_of(const KernelArgs &k, const Shared *sh, unsigned i, int g
 //               while this one's are being exponentiated.
 
 template <bool E4M3>
-__device__ void produce(const KernelArgs &k, Shared *sh, uint8_t *stages) {
+__device__ void produce(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint8_t *stages) {
     constexpr int kStages = E4M3 ? Form<E4M3>::raw : Form<E4M3>::stages;
     uint64_t *const full = E4M3 ? sh->raw_full : sh->kv_full, *const empty = E4M3 ? sh->raw_empty : sh->kv_empty;
     const int lane = threadIdx.x & 31, n_seq = k.a.own.n_seq;
@@ -286,7 +286,10 @@ __device__ void produce(const KernelArgs &k, Shared *sh, uint8_t *stages) {
     if (lane != 0) return;
 
     unsigned i = blockIdx.x;
-    unsigned loaded = 0;     // tiles so far
+    unsigned loaded = 0;     // K and V tiles so far
+    unsigned q_uses[2] = {0, 0};
+    int q_next = 0;          // the query tile of the next one-tile item
+    const int g = k.a.group;
     for (unsigned n = 0;; ++n) {
         const int slot = n % kRing;
         if (n >= kRing && !wait_or_abort(sh, &sh->item_empty[slot], (n / kRing - 1) & 1)) break;
@@ -299,6 +302,23 @@ __device__ void produce(const KernelArgs &k, Shared *sh, uint8_t *stages) {
         const int tiles = (it.n_keys + kTile - 1) / kTile, outer = own ? it.b * k.a.own.n_kv + it.j : it.j;
         const void *map_k = &k.map[own ? 2 : 0], *map_v = &k.map[own ? 3 : 1];
         bool ok = true;
+        // Queries first: behind the next item's K and V tiles they came 5,400 cycles late.
+        // A tile is whole rows of the KV head's query heads, one box of (64 elements,
+        // heads, rows) per half, swizzled into a K-major tile.  Rows of the box past
+        // the item's (another sequence's, or zeros past the last) fill vectors that
+        // nothing reads: rows of a product never mix.
+        const bool two = it.n_vec > k.p.tile;
+        for (int t = 0; t < (two ? 2 : 1) && ok; ++t) {
+            const int buf = two ? t : q_next;
+            if (q_uses[buf] > 0) ok = wait_or_abort(sh, &sh->q_empty[buf], (q_uses[buf] - 1) & 1);
+            if (!ok) break;
+            ++q_uses[buf];
+            const int row = (it.vec0 + t * k.p.tile) / g;
+            mbar_arrive_expect_tx(&sh->q_full[buf], 2 * uint32_t(k.p.tile) * 128u);
+            tma_load_3d(q_tiles + buf * kTileBytes, &k.map[4], 0, it.j * g, row, &sh->q_full[buf]);
+            tma_load_3d(q_tiles + buf * kTileBytes + kHalfBytes, &k.map[4], 64, it.j * g, row, &sh->q_full[buf]);
+        }
+        if (!two) q_next ^= 1;
         for (int t = 0; t < 2 * tiles && ok; ++t, ++loaded) {
             const bool is_v = order_is_v(t, tiles);
             const int row = it.key0 + order_tile(t, tiles) * kTile;
@@ -327,6 +347,8 @@ __device__ void produce(const KernelArgs &k, Shared *sh, uint8_t *stages) {
     // no copy outlives the CTA
     for (unsigned t = loaded > kStages ? loaded - kStages : 0; t < loaded; ++t)
         wait_drained(&full[t % kStages], (t / kStages) & 1);
+    for (int buf = 0; buf < 2; ++buf)
+        if (q_uses[buf] > 0) wait_drained(&sh->q_full[buf], (q_uses[buf] - 1) & 1);
 }
 
 // E4M3 tiles -> bf16 tiles, eight lanes an entry.  Rows of a V tile past the
@@ -379,42 +401,6 @@ __device__ void expand_tiles(const KernelArgs &k, Shared *sh, uint8_t *stages, c
             }
         }
     }
-}
-
-// The query vectors of a tile, whole rows of the KV head's `group` query heads,
-// as one box of (64 elements, heads, rows) per half, swizzled into a K-major tile.
-// Rows of the box past the item's (another sequence's, or zeros past the last)
-// fill vectors that nothing reads: rows of a product never mix.
-__device__ void load_queries(const KernelArgs &k, Shared *sh, uint8_t *tiles) {
-    if ((threadIdx.x & 31) != 0) return;
-    const int g = k.a.group;
-    const uint32_t half_bytes = uint32_t(k.p.tile) * 128u;
-    unsigned uses[2] = {0, 0};
-    int next = 0;
-    for (unsigned n = 0;; ++n) {
-        const int slot = n % kRing;
-        if (!wait_or_abort(sh, &sh->item_full[slot], (n / kRing) & 1)) break;
-        const Item it = sh->item[slot];
-        mbar_arrive(&sh->item_empty[slot]);
-        if (it.n_vec == 0) break;
-        const bool two = it.n_vec > k.p.tile;
-        bool ok = true;
-        for (int t = 0; t < (two ? 2 : 1) && ok; ++t) {
-            const int buf = two ? t : next;
-            if (uses[buf] > 0) ok = wait_or_abort(sh, &sh->q_empty[buf], (uses[buf] - 1) & 1);
-            if (!ok) break;
-            ++uses[buf];
-            const int row = it.vec0 / g + t * (k.p.tile / g);
-            mbar_arrive_expect_tx(&sh->q_full[buf], 2 * half_bytes);
-            tma_load_3d(tiles + buf * kTileBytes, &k.map[4], 0, it.j * g, row, &sh->q_full[buf]);
-            tma_load_3d(tiles + buf * kTileBytes + kHalfBytes, &k.map[4], 64, it.j * g, row, &sh->q_full[buf]);
-        }
-        if (!ok) break;
-        if (!two) next ^= 1;
-    }
-    // no copy outlives the CTA
-    for (int buf = 0; buf < 2; ++buf)
-        if (uses[buf] > 0) wait_drained(&sh->q_full[buf], (uses[buf] - 1) & 1);
 }
 
 // The last V tiles of an own part: rows past the sequence's last entry become
@@ -803,11 +789,9 @@ __global__ void __launch_bounds__(Form<E4M3>::threads, 1) attn_batch_kernel(cons
     } else {
         regs_lower<F::regs_other>();
         if (warp == kProducerWarp)
-            produce<E4M3>(k, sh, E4M3 ? raw : stages);
+            produce<E4M3>(k, sh, q_tiles, E4M3 ? raw : stages);
         else if (warp == kMmaWarp)
             multiply<E4M3>(k, sh, q_tiles, stages, tmem);
-        else if (warp == kQueryWarp)
-            load_queries(k, sh, q_tiles);
         else if (E4M3 && warp >= kExpandWarp)
             expand_tiles(k, sh, stages, raw);
     }
@@ -819,15 +803,15 @@ __global__ void __launch_bounds__(Form<E4M3>::threads, 1) attn_batch_kernel(cons
 }
 
 // ------------------------------------------------------------------ joining the parts
-// A CTA takes 32 query vectors (lanes) and four column quads of one KV head; its
-// 16 warps are the quads times four runs of consecutive parts.  A run's parts are
+// A CTA takes 32 query vectors (lanes) and two column quads of one KV head; its
+// eight warps are the quads times four runs of consecutive parts.  A run's parts are
 // folded in ascending order (prefix parts first) against the maximum of all the
 // vector's parts, then the runs in ascending order: an order that the number of
 // the vector's parts fixes.  520 bytes per vector and part from HBM or L2 bound it
 // where there are many vectors; where there are few, the chain of two loads does.
-constexpr int kJoinRuns = 4, kJoinQuads = 4, kJoinUnroll = 5;
+constexpr int kJoinRuns = 4, kJoinQuads = 2, kJoinUnroll = 4;
 
-__global__ void __launch_bounds__(32 * kJoinRuns * kJoinQuads, 2) attn_batch_join_kernel(
+__global__ void __launch_bounds__(32 * kJoinRuns * kJoinQuads, 4) attn_batch_join_kernel(
     AttnBatchArgs a, Plan p, const float *opart, const float2 *ml, unsigned *next) {
     __shared__ float s_top[kJoinRuns][32], s_l[kJoinRuns][32];
     __shared__ float4 s_o[kJoinRuns][kJoinQuads][32];
