@@ -109,3 +109,32 @@ def attention_batch(q, shared_k, shared_v, own_k, own_v, pos):
                 out[b, r, j] = w @ v
                 spread[b, r, j] = w @ np.abs(v)
     return out, spread
+
+
+def branch_logits(model, tokens, eps=1e-6):
+    """fp64 logits [len(tokens)][V] of the branch decoder (decode.BranchModel) for one
+    sequence of tokens at positions 0.., every row at once: per block
+    n = bf16(rms(x)); q, k, v = n Wqkv; q, k normalised and turned, all three to
+    bf16; o = bf16(causal attention); x += o Wo; then the MLP block.  ``model`` is
+    attn_decoder's dict with, per ``attn`` entry, q_norm and k_norm (bf16 bits), and
+    inv_freq, adjacent, quantise (cache vectors through E4M3)."""
+    from .decoder import block_forward, final_input
+    from .linear import bf16_to_f64, w4_linear
+    from .numerics import bf16_bits_of, bf16_round, rms_norm
+    G, n_kv, g, T = model["group"], model["n_kv"], model["attn_group"], len(tokens)
+    n_q = n_kv * g
+    x = bf16_to_f64(model["emb"][np.asarray(tokens)])
+    for blk, att in zip(model["blocks"], model["attn"]):
+        y = w4_linear(att["qkv_codes"], att["qkv_scales"], bf16_bits_of(bf16_round(rms_norm(x, eps))), G)
+        y = qk_norm_rope(y.reshape(T, n_q + 2 * n_kv, HEAD_DIM), n_q, n_kv, bf16_to_f64(att["q_norm"]),
+                         bf16_to_f64(att["k_norm"]), eps, model["inv_freq"], model["adjacent"], range(T))
+        y = bf16_round(y)
+        kv = y[:, n_q:]
+        if model["quantise"]:
+            kv = np.stack([e4m3_values(*e4m3_vector(v)) for v in kv.reshape(-1, HEAD_DIM)]).reshape(kv.shape)
+        k, v = kv[:, :n_kv].transpose(1, 0, 2), kv[:, n_kv:].transpose(1, 0, 2)
+        q = y[:, :n_q].reshape(1, T, n_kv, g, HEAD_DIM)
+        o = attention_batch(q, k[:, :0], v[:, :0], k[None], v[None], [0])[0].reshape(T, n_q * HEAD_DIM)
+        x = x + w4_linear(att["o_codes"], att["o_scales"], bf16_bits_of(bf16_round(o)), G)
+        x = block_forward(x, blk, G)
+    return w4_linear(model["lm_codes"], model["lm_scales"], final_input(x), G)

@@ -331,3 +331,166 @@ def attn_drafted_decode(dec: AttnDecoder, last_token: int, pos: int, n_tokens: i
         out.extend(t[: a + 1])
         lens.append(a)
     return out[:n_tokens], lens
+
+
+# ---------------------------------------------------------------- several replies of one prompt
+class BranchModel:
+    """The synthetic decoder with a position-aware attention sub-block before each
+    MLP block: queries and keys are RMS-normalised per head (gains q_norm[b],
+    k_norm[b], bf16 [128]) and turned by their positions (tf.rope_turns) between
+    the QKV projection and the cache.  Otherwise as AttnModel."""
+
+    def __init__(self, base: tf.Model, qkv, o, q_norm, k_norm, turns: torch.Tensor, n_kv: int, group: int,
+                 adjacent: bool = False):
+        if not len(qkv) == len(o) == len(q_norm) == len(k_norm) == len(base.gate_up):
+            raise ValueError("one qkv and one output projection, and one pair of gains, per block")
+        self.base, self.qkv, self.o = base, list(qkv), list(o)
+        self.q_norm, self.k_norm, self.turns, self.adjacent = list(q_norm), list(k_norm), turns, adjacent
+        self.n_kv, self.group, self.n_q = n_kv, group, n_kv * group
+
+
+def upload_branch_model(weights: dict, n_kv: int, group: int, theta: float = 1e6, rot_dim: int = tf.HEAD_DIM,
+                        adjacent: bool = False, rms_eps: float = 1e-6, device="cuda") -> BranchModel:
+    """``weights`` as for upload_attn_model, each ``attn`` entry with q_norm and k_norm
+    (uint16 bf16 bits [128])."""
+    am = upload_attn_model(weights, n_kv, group, 256, rms_eps, device)
+    norms = [[torch.from_numpy(np.ascontiguousarray(a[n]).view(np.int16)).to(device) for a in weights["attn"]]
+             for n in ("q_norm", "k_norm")]
+    return BranchModel(am.base, am.qkv, am.o, *norms, tf.rope_turns(rot_dim, theta, device=device), n_kv, group,
+                       adjacent)
+
+
+class BranchDecoder:
+    """Decodes up to n_branch replies of one prompt in common passes.
+
+    The prompt's cache entries (all but its last token's, which is every reply's
+    first input) are computed once and shared; each branch keeps a cache of its
+    own.  A pass of R rows feeds each branch its last committed token and R - 1
+    drafts, verifies them (keyed sampling with the branch's own seed) and commits
+    the accepted ones.  Every row's bits are those of its branch decoding alone,
+    one row a pass, so neither drafts nor the other branches change its tokens.
+    A finished branch idles until the next prompt.  ``fmt``: "bf16" or "e4m3"
+    cache entries.
+    """
+
+    def __init__(self, model: BranchModel, n_branch: int, max_prompt: int, max_reply: int, fmt: str = "bf16",
+                 max_rows: int = 8, device="cuda"):
+        b = model.base
+        n = max(n_branch * max_rows, tf.MAX_ROWS)
+        W, A = (model.n_q + 2 * model.n_kv) * tf.HEAD_DIM, model.n_q * tf.HEAD_DIM
+
+        def up(k):
+            return -(-k // 256) * 256
+
+        self.model, self.n_branch, self.max_rows = model, n_branch, max_rows
+        self.shared = [tf.KVBatch(1, model.n_kv, up(max_prompt), fmt, device) for _ in model.qkv]
+        self.own = [tf.KVBatch(n_branch, model.n_kv, up(max_reply + max_rows), fmt, device) for _ in model.qkv]
+        f32, b16 = dict(dtype=torch.float32, device=device), dict(dtype=torch.bfloat16, device=device)
+        self.x, self.qkv, self.logits = (torch.zeros((n, c), **f32) for c in (b.hidden, W, b.vocab))
+        self.n, self.qkv_b, self.att = (torch.zeros((n, c), **b16) for c in (b.hidden, W, A))
+        self.n_bits = self.n.view(torch.int16)
+        self.n_out, self.h_out = (torch.zeros((tf.MAX_ROWS, c), dtype=torch.int16, device=device)
+                                  for c in (b.hidden, b.ffn))
+        self.ws_gemm = tf.workspace(max(tf.lane_gemm_workspace_bytes(m.K, m.N, m.group)
+                                        for m in model.qkv + model.o + [b.lm_head]), device)
+        self.ws_block = tf.workspace(b.block_workspace_bytes(), device)
+        self.ws_sample = tf.workspace(tf.keyed_sample_workspace_bytes(max_rows, b.vocab), device)
+        self.ws_status = tf.workspace(256, device)
+        self.ws_attn = None
+        self.last = torch.zeros(max(n_branch, 1), dtype=torch.int32, device=device)
+        self.drafts = torch.zeros((n_branch, max(max_rows, tf.MAX_ROWS)), dtype=torch.int32, device=device)
+        self.tokens = torch.zeros((n_branch, max_rows), dtype=torch.int32, device=device)
+        self.accepted = torch.zeros(n_branch, dtype=torch.int32, device=device)
+        self.pos = torch.zeros(n_branch, dtype=torch.int64, device=device)
+        self.prompt_pos = torch.zeros(1, dtype=torch.int64, device=device)
+        self.sample_pos = torch.zeros((n_branch, max_rows), dtype=torch.int64, device=device)
+        self.prompt_len, self.at = 0, [-1] * n_branch
+
+    def _rows(self, caches, pos: torch.Tensor, R: int, offset: int, prefix=None):
+        """Rows 0..len(pos)*R-1, embedded in self.x, through every block."""
+        m, b = self.model, self.model.base
+        rows, qo, ko, vo = len(pos) * R, 0, m.n_q * tf.HEAD_DIM, (m.n_q + m.n_kv) * tf.HEAD_DIM
+        chunks = [slice(r, min(r + tf.MAX_ROWS, rows)) for r in range(0, rows, tf.MAX_ROWS)]
+        P = offset if prefix is not None else 0
+        need = caches[0].attention_workspace_bytes(m.group, R, P)
+        if self.ws_attn is None or self.ws_attn.numel() < need:
+            self.ws_attn = tf.workspace(need, self.x.device)
+        for i, own in enumerate(caches):
+            tf.rmsnorm_bf16(self.x[:rows], b.rms_eps, out=self.n_bits[:rows])
+            for c in chunks:
+                tf.lane_gemm_w4(m.qkv[i], self.n_bits[c], y=self.qkv[c], ws=self.ws_gemm)
+            tf.qk_norm_rope(self.qkv[:rows], m.n_q, m.n_kv, pos, m.turns, m.q_norm[i], m.k_norm[i], b.rms_eps,
+                            m.adjacent, pos_offset=offset, out=self.qkv_b[:rows])
+            own.store(self.qkv_b[:rows, ko:vo], self.qkv_b[:rows, vo:], pos, ws=self.ws_status)
+            own.attention(self.qkv_b[:rows, qo:ko], m.group, pos, prefix=prefix[i] if prefix is not None else None,
+                          prefix_len=P, out=self.att[:rows], ws=self.ws_attn)
+            for c in chunks:
+                tf.lane_gemm_w4_accumulate(m.o[i], self.att[c], self.x[c], ws=self.ws_gemm)
+                b.block(i, self.x[c], self.n_out, self.h_out, self.ws_block)
+
+    def start(self, prompt):
+        """A new prompt (at least one token): its entries into the shared caches, all branches at its end."""
+        toks = [int(t) for t in prompt]
+        if not toks:
+            raise ValueError("a prompt has at least one token")
+        for p in range(0, len(toks) - 1, tf.MAX_ROWS):
+            R = min(tf.MAX_ROWS, len(toks) - 1 - p)
+            self.prompt_pos.fill_(p)
+            chunk = torch.tensor(toks[p:p + R] + [0], dtype=torch.int32, device=self.x.device)
+            self.model.base.embed_rows(chunk[:1], chunk[1:], R, self.x[:R], self.ws_status)
+            self._rows(self.shared, self.prompt_pos, R, 0)
+        self.prompt_len = len(toks) - 1
+        self.last.fill_(toks[-1])
+        self.at = [0] * self.n_branch
+
+    def finish(self, branch: int):
+        self.at[branch] = -1
+
+    def step(self, R: int, drafts, temperature, top_k, top_p, seeds):
+        """One verify pass of R rows per branch; ``drafts[b]`` holds branch b's R - 1
+        proposals.  Returns per branch (a, tokens t[0..R-1]), or None where it idles."""
+        b, P, rows = self.model.base, self.prompt_len, self.n_branch * R
+        self.pos.copy_(torch.tensor(self.at, dtype=torch.int64))
+        first = torch.tensor([[P + p + 1 + r for r in range(R)] for p in self.at], dtype=torch.int64)
+        self.sample_pos[:, :R].copy_(first)
+        if R > 1:
+            d = np.zeros((self.n_branch, R - 1), np.int32)
+            for i, p in enumerate(self.at):
+                if p >= 0:
+                    d[i] = np.asarray(drafts[i][: R - 1], np.int32)
+            self.drafts[:, : R - 1].copy_(torch.from_numpy(d))
+        for i in range(self.n_branch):
+            b.embed_rows(self.last[i:i + 1], self.drafts[i], R, self.x[i * R:(i + 1) * R], self.ws_status)
+        self._rows(self.own, self.pos, R, P, self.shared if P else None)
+        tf.rmsnorm_bf16(self.x[:rows], b.rms_eps, out=self.n_bits[:rows])
+        for r in range(0, rows, tf.MAX_ROWS):
+            c = slice(r, min(r + tf.MAX_ROWS, rows))
+            tf.lane_gemm_w4(b.lm_head, self.n_bits[c], y=self.logits[c], ws=self.ws_gemm)
+        for i, p in enumerate(self.at):
+            if p < 0:
+                continue
+            tf.keyed_sample(self.logits[i * R:(i + 1) * R], temperature, top_k, top_p, seeds[i],
+                            pos=self.sample_pos[i, :R], tokens=self.tokens[i, :R], ws=self.ws_sample)
+            tf.accept(self.drafts[i], self.tokens[i, :R], accepted=self.accepted[i:i + 1], bonus=self.last[i:i + 1])
+        got, t = self.accepted.tolist(), self.tokens[:, :R].tolist()
+        out = [None if p < 0 else (got[i], t[i]) for i, p in enumerate(self.at)]
+        self.at = [p if p < 0 else p + got[i] + 1 for i, p in enumerate(self.at)]
+        return out
+
+
+def branch_decode(dec: BranchDecoder, prompt, n_tokens, R: int, temperature, top_k, top_p, seeds, draft_fn=None):
+    """One reply of n_tokens[b] tokens per branch, R rows a pass; ``draft_fn(b, k, n)``
+    gives branch b's drafts for its tokens k .. k + n - 1.  Returns the replies."""
+    dec.start(prompt)
+    out = [[] for _ in range(dec.n_branch)]
+    for b in range(dec.n_branch):
+        if n_tokens[b] == 0:
+            dec.finish(b)
+    while any(p >= 0 for p in dec.at):
+        drafts = [draft_fn(b, len(out[b]), R - 1) if R > 1 and dec.at[b] >= 0 else [] for b in range(dec.n_branch)]
+        for b, got in enumerate(dec.step(R, drafts, temperature, top_k, top_p, seeds)):
+            if got is not None:
+                out[b].extend(got[1][: got[0] + 1])
+                if len(out[b]) >= n_tokens[b]:
+                    dec.finish(b)
+    return [o[:n] for o, n in zip(out, n_tokens)]
