@@ -519,7 +519,7 @@ TF_API tf_status tf_attention_verify(const tf_kv_cache *c, int32_t group, const 
  *     value = code * 2^(s - 127), exact in bf16.  s - 127 is the smallest
  *     exponent e in [-120, 7] with max|x| <= 448 * 2^e over the entry's 128
  *     elements; code = x * 2^-e rounded to nearest even, saturating at 448.  s =
- *     255 marks an entry that held an infinity or NaN: all its elements read
+ *     255 marks an entry that held an infinity or NaN (codes 0): all its elements read
  *     as NaN.  Element d of an entry is byte
  *       16 * ((d % 64) / 8) + 8 * (d / 64) + d % 8,
  *     with the bytes of elements 4i + 1 and 4i + 2 exchanged.

@@ -375,23 +375,38 @@ __device__ void expand_tiles(const KernelArgs &k, Shared *sh, uint8_t *stages, c
             const int rs = done % kRaw, st = done % kStages;
             if (!wait_or_abort(sh, &sh->raw_full[rs], (done / kRaw) & 1)) return;
             if (done >= kStages && !wait_or_abort(sh, &sh->kv_empty[st], (done / kStages - 1) & 1)) return;
-            const uint8_t *src = raw + size_t(rs) * kRawBytes + 16 * group, *sc = scales + rs * kTile;
-            uint8_t *dst = stages + size_t(st) * kTileBytes;
-#pragma unroll 4
-            for (int row = tid >> 3; row < fill; row += 4 * kExpandWarps) {
-                uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-                const uint32_t sb = row < valid ? sc[row] : uint32_t(kScaleNan);
-                if (row < valid && !(is_v && sb == uint32_t(kScaleNan) && row >= hidden)) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(src + row * kHeadDim);
-                    const uint32_t f = e4m3_factor(sb);
-                    e4m3_expand(w.x, f, lo.x, lo.y);
-                    e4m3_expand(w.y, f, lo.z, lo.w);
-                    e4m3_expand(w.z, f, hi.x, hi.y);
-                    e4m3_expand(w.w, f, hi.z, hi.w);
+            constexpr int kRows = 4 * kExpandWarps, kSteps = kTile / kRows;    // rows all warps take at a time
+            static_assert(kRows % 8 == 0 && kTile % kRows == 0, "a thread's rows share their place in the swizzle");
+            const int row0 = tid >> 3;
+            const uint8_t *src = raw + size_t(rs) * kRawBytes + row0 * kHeadDim + 16 * group;
+            const uint8_t *sc = scales + rs * kTile + row0;
+            uint8_t *dst = stages + size_t(st) * kTileBytes + row0 * 128 + ((group ^ (row0 & 7)) << 4);
+            const bool whole = valid == kTile && !(is_v && hidden < kTile);     // nothing to leave out
+            uint4 w[kSteps];
+            uint32_t f[kSteps];
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                w[i] = *reinterpret_cast<const uint4 *>(src + i * kRows * kHeadDim);
+                f[i] = sc[i * kRows];
+            }
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int row = row0 + i * kRows;
+                if (!whole) {
+                    if (row >= fill) break;
+                    if (row >= valid || (is_v && f[i] == uint32_t(kScaleNan) && row >= hidden)) {
+                        w[i] = make_uint4(0u, 0u, 0u, 0u);
+                        f[i] = 0u;
+                    }
                 }
-                uint8_t *p = dst + row * 128 + ((group ^ (row & 7)) << 4);
-                *reinterpret_cast<uint4 *>(p) = lo;
-                *reinterpret_cast<uint4 *>(p + kHalfBytes) = hi;
+                const uint32_t factor = e4m3_factor(f[i]);
+                uint4 lo, hi;
+                e4m3_expand(w[i].x, factor, lo.x, lo.y);
+                e4m3_expand(w[i].y, factor, lo.z, lo.w);
+                e4m3_expand(w[i].z, factor, hi.x, hi.y);
+                e4m3_expand(w[i].w, factor, hi.z, hi.w);
+                *reinterpret_cast<uint4 *>(dst + i * kRows * 128) = lo;
+                *reinterpret_cast<uint4 *>(dst + i * kRows * 128 + kHalfBytes) = hi;
             }
             fence_proxy_async_smem();
             __syncwarp();

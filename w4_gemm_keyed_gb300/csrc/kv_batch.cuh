@@ -51,7 +51,7 @@ __host__ __device__ constexpr int e4m3_byte(int d) {
 }
 
 constexpr int kE4m3MinExp = -120, kE4m3MaxExp = 7;
-constexpr int kScaleNan = 255;
+constexpr int kScaleNan = 255;    // its codes are zeros
 
 // Scale byte of a vector whose largest bf16 magnitude has the bits m (sign
 // cleared).  448 = 1.75 * 2^8.
@@ -61,11 +61,9 @@ __device__ __forceinline__ int e4m3_scale_byte(uint32_t m) {
     return min(max(e, kE4m3MinExp), kE4m3MaxExp) + 127;
 }
 
-// bf16x2 factor that turns expanded codes (code * 2^-120) into values.
-__device__ __forceinline__ uint32_t e4m3_factor(uint32_t s) {
-    const uint32_t f = s == uint32_t(kScaleNan) ? 0x7FFFu : (s + 120u) << 7;
-    return f | (f << 16);
-}
+// bf16x2 factor that turns expanded codes (code * 2^-120) into values: 2^(s - 7),
+// or infinity for the NaN mark, whose codes are zeros (0 * inf = NaN).
+__device__ __forceinline__ uint32_t e4m3_factor(uint32_t s) { return min(s + 120u, 255u) * 0x00800080u; }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t d;
@@ -76,11 +74,12 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 // Four codes of one 4-byte word -> four bf16 values (lo: elements 0, 1; hi: 2, 3).
 // A code's exponent and mantissa bits, moved to bits 10..4 of a bf16, read as
 // code * 2^-120 (subnormal codes as subnormal bf16); one exact product with the
-// factor restores the value.
+// factor restores the value.  Left shifts are products, which leave the logic
+// unit (half the multiply unit's rate) to the masks.
 __device__ __forceinline__ void e4m3_expand(uint32_t w, uint32_t factor, uint32_t &lo, uint32_t &hi) {
-    const uint32_t t = w << 8;
-    lo = mul_bf16x2((t & 0x80008000u) | ((t >> 4) & 0x07F007F0u), factor);
-    hi = mul_bf16x2((w & 0x80008000u) | ((w >> 4) & 0x07F007F0u), factor);
+    constexpr uint32_t kMagnitude = 0x07F007F0u, kSign = 0x80008000u;
+    lo = mul_bf16x2(lop3_and_or(w * 256u, kSign, (w * 16u) & kMagnitude), factor);
+    hi = mul_bf16x2(lop3_and_or(w, kSign, (w >> 4) & kMagnitude), factor);
 }
 
 // Two fp32 operations in one instruction, each rounded as the single one is.
