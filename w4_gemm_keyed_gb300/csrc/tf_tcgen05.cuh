@@ -39,40 +39,33 @@ __device__ __forceinline__ uint32_t elect_one() {
     return r;
 }
 
-// The products and commits below are issued by the lane whose `leader` is not
-// zero, under a predicate and not a branch: in a converged warp the descriptors
-// then stay in uniform registers, where a branch would have each of them moved
-// there for each product (measured: about 130 cycles a product).
+// The products and commits below are issued by one thread, the elected lane of
+// its warp.
 
 // D[tmem] (+)= A * B, A and B in shared memory (lower words of their descriptors).
-__device__ __forceinline__ void tc_mma_ss(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
-                                          uint32_t accumulate) {
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "mov.b64 a, {%1, %6};\n\tmov.b64 b, {%2, %6};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(leader), "n"(kDescHigh)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
         : "memory");
 }
 
 // The same with A in tensor memory (lane = row, two 16-bit elements of K per column).
-__device__ __forceinline__ void tc_mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
-                                          uint32_t accumulate) {
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "mov.b64 b, {%2, %6};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(leader), "n"(kDescHigh)
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
         : "memory");
 }
 
 // One arrival on bar once every product issued so far by this thread is done.
-__device__ __forceinline__ void tc_commit(uint32_t leader, uint64_t *bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
-        "r"(leader)
-        : "memory");
+__device__ __forceinline__ void tc_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
 }
 
 // Allocates n columns of tensor memory (a power of two >= 32), the whole warp.
