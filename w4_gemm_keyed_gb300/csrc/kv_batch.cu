@@ -19,14 +19,15 @@ namespace {
 // fraction of a turn of a 64-bit fixed-point frequency, whatever the position, and
 // its top 32 bits go to sincospi as an fp32 in [-1, 1) half turns (off by at
 // most 2^-25 half turns).  HBM bounds it where there are many rows: 16383 bf16
-// rows of 40 heads in PROMPT_US us (PROMPT_GBS of 6.78 TB/s copy); four lanes' worth of
-// shuffles fewer and two elements an instruction took it there from 95 us.
+// rows of 40 heads take 62 us (5.4 TB/s; a copy reaches 6.8).  A lane for 4
+// elements, partners by shuffle and one element an instruction took 95 us, 68
+// without the next heads' loads under way.
 __device__ __forceinline__ void sincos_turns(unsigned long long frac, float &c, float &s) {
     const float half_turns = __int2float_rn(int(frac >> 32)) * 0x1p-31f;
     sincospif(half_turns, &s, &c);
 }
 
-constexpr int kRopeSteps = 4;   // pairs of heads a warp has in flight
+constexpr int kRopeSteps = 2;   // pairs of heads a warp turns while as many are on their way
 
 __device__ __forceinline__ uint64_t widen2(uint32_t w) {       // two bf16 -> two fp32
     return uint64_t(w << 16) | (uint64_t(w & 0xFFFF0000u) << 32);
@@ -82,22 +83,32 @@ __global__ void __launch_bounds__(256, FP32 ? 2 : 3) qk_norm_rope_kernel(QkNormR
     }
     const char *src = static_cast<const char *>(a.x) + (size_t)row * a.ldx * (FP32 ? 4 : 2);
     uint16_t *dst = a.y + (size_t)row * a.ldy;
-    for (int h = h0 + half; h < h1 + half; h += 2 * kRopeSteps) {
-        uint4 x[kRopeSteps][FP32 ? 2 : 1];
+    uint4 ahead[kRopeSteps][FP32 ? 2 : 1];      // the next heads, on their way while these are turned
+    auto load = [&](int h) {
 #pragma unroll
         for (int u = 0; u < kRopeSteps; ++u) {
             const int hu = h + 2 * u;
             if (hu >= h1) continue;
             if constexpr (FP32) {
                 const float *from = reinterpret_cast<const float *>(src) + hu * kHeadDim;
-                x[u][0] = __ldg(reinterpret_cast<const uint4 *>(from + e0));
-                x[u][1] = __ldg(reinterpret_cast<const uint4 *>(from + e1));
+                ahead[u][0] = __ldg(reinterpret_cast<const uint4 *>(from + e0));
+                ahead[u][1] = __ldg(reinterpret_cast<const uint4 *>(from + e1));
             } else {    // not the read-only path: the caller may rotate rows in place
                 const uint16_t *from = reinterpret_cast<const uint16_t *>(src) + hu * kHeadDim;
                 const uint2 lo = *reinterpret_cast<const uint2 *>(from + e0), hi = *reinterpret_cast<const uint2 *>(from + e1);
-                x[u][0] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                ahead[u][0] = make_uint4(lo.x, lo.y, hi.x, hi.y);
             }
         }
+    };
+    load(h0 + half);
+    for (int h = h0 + half; h < h1 + half; h += 2 * kRopeSteps) {
+        uint4 x[kRopeSteps][FP32 ? 2 : 1];
+#pragma unroll
+        for (int u = 0; u < kRopeSteps; ++u) {
+            x[u][0] = ahead[u][0];
+            if constexpr (FP32) x[u][1] = ahead[u][1];
+        }
+        load(h + 2 * kRopeSteps);
 #pragma unroll
         for (int u = 0; u < kRopeSteps; ++u) {
             const int hu = h + 2 * u;
@@ -148,7 +159,9 @@ __global__ void __launch_bounds__(256, FP32 ? 2 : 3) qk_norm_rope_kernel(QkNormR
 // A CTA takes some rows of one sequence, all heads; 16 lanes move a row's K and V
 // vectors of one head, 16 bytes of bf16 a lane each, two heads in flight.
 // Consecutive half warps take consecutive heads of a row (which the rows hold
-// together); a head's entries of consecutive rows are one CTA's.
+// together); a head's entries of consecutive rows are one CTA's.  HBM bounds both
+// where there are many rows: 32767 rows of 8 heads, E4M3, are written and read back
+// in 69 us (5.8 TB/s; 117 us with an integer division per vector's place).
 constexpr int kVecUnroll = 2, kVecThreads = 256, kVecHalfWarps = kVecThreads / 16;
 
 int rows_per_cta(int n_kv) { return n_kv < 64 ? 64 / n_kv : 1; }
