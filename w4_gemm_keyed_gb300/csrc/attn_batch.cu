@@ -26,10 +26,10 @@
 // What bounds it (GB300, us measured): many rows, the tensor cores and the
 // hand-over between them and the softmax: a step of two tiles and 128 keys takes
 // 2,860 cycles where its products take 2,080 (512 rows x 64 heads over 32768
-// entries 460 us, 1.19 PFLOP/s; of that the steps 320, passing from item to item 42,
-// joining 74).  Few rows, HBM: 12 rows x 20 heads over 130001 entries 53 us, 5.0
+// entries 449 us, 1.21 PFLOP/s; of that the steps 320, passing from item to item 42,
+// joining 55).  Few rows, HBM: 12 rows x 20 heads over 130001 entries 53 us, 5.0
 // TB/s.  E4M3 caches with many rows, the issue slots that expansion shares with
-// the softmax: 240 rows x 64 heads over 20000 entries 221 us.
+// the softmax: 240 rows x 64 heads over 20000 entries 216 us.
 #include <atomic>
 
 #include <cuda.h>
@@ -841,26 +841,29 @@ __global__ void __launch_bounds__(Form<E4M3>::threads, 1) attn_batch_kernel(cons
 }
 
 // ------------------------------------------------------------------ joining the parts
-// A CTA takes 32 query vectors (lanes) and two column quads of one KV head; its
-// eight warps are the quads times four runs of consecutive parts.  A run's parts are
-// folded in ascending order (prefix parts first) against the maximum of all the
-// vector's parts, then the runs in ascending order: an order that the number of
-// the vector's parts fixes.  520 bytes per vector and part from HBM or L2 bound it
-// where there are many vectors; where there are few, the chain of two loads does.
-constexpr int kJoinRuns = 4, kJoinQuads = 2, kJoinUnroll = 4;
+// A CTA takes 32 query vectors (lanes) and four column quads of one KV head; its
+// eight warps are two pairs of quads times four runs of consecutive parts.  A
+// run's parts are folded in ascending order (prefix parts first) against the
+// maximum of all the vector's parts, then the runs in ascending order: an order
+// that the number of the vector's parts fixes.  Where there are many vectors, 520
+// bytes per vector and part from HBM or L2 and the instructions that find them
+// bound it (with a quad a thread and 64-bit products for every part's place, 512
+// rows x 64 heads x 14 parts took 74 us); where there are few, the chain of
+// three loads does.
+constexpr int kJoinRuns = 4, kJoinPairs = 2, kJoinUnroll = 4, kJoinThreads = 32 * kJoinRuns * kJoinPairs;
 
-__global__ void __launch_bounds__(32 * kJoinRuns * kJoinQuads, 4) attn_batch_join_kernel(
-    AttnBatchArgs a, Plan p, const float *opart, const float2 *ml, unsigned *next) {
+__global__ void __launch_bounds__(kJoinThreads, 3) attn_batch_join_kernel(AttnBatchArgs a, Plan p, const float *opart,
+                                                                          const float2 *ml, unsigned *next) {
     __shared__ float s_top[kJoinRuns][32], s_l[kJoinRuns][32];
-    __shared__ float4 s_o[kJoinRuns][kJoinQuads][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, run = warp / kJoinQuads, col = warp % kJoinQuads;
-    const int quad = blockIdx.z * kJoinQuads + col, n_kv = a.own.n_kv, rg = a.R * a.group, j = blockIdx.y;
+    __shared__ float4 s_o[kJoinRuns][kJoinPairs][2][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, run = warp / kJoinPairs, col = warp % kJoinPairs;
+    const int quad = 2 * (blockIdx.z * kJoinPairs + col), n_kv = a.own.n_kv, rg = a.R * a.group, j = blockIdx.y;
     const int v = blockIdx.x * 32 + lane;
     int n = 0, b = 0;
     if (v < p.n_vec) {
-        b = v / rg;
+        b = idx_div(v, rg);
         const long long pos = seq_position(a.pos, b, a.R, a.own.max_len, a.err, false);
-        if (pos >= 0) n = p.n_parts + int((pos + (v - b * rg) / a.group) / kOwnPart) + 1;
+        if (pos >= 0) n = p.n_parts + int((pos + idx_div(v - b * rg, a.group)) / kOwnPart) + 1;
     }
     // Positions come from before the attention grid, which had waited for them when it
     // let this grid start; the partial results come from that grid itself.
@@ -868,22 +871,41 @@ __global__ void __launch_bounds__(32 * kJoinRuns * kJoinQuads, 4) attn_batch_joi
     grid_launch_dependents();
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *next = 0u;
     const int c_begin = n * run / kJoinRuns, c_end = n * (run + 1) / kJoinRuns;
-    // vector slot of part c
-    const int tile = v / p.tile, in0 = v - tile * p.tile, in1 = v - b * rg;
-    const long long slot0 = ((long long)j * p.tiles + tile) * p.tile, step0 = (long long)n_kv * p.tiles * p.tile;
-    const long long slot1 = p.own0 + ((long long)b * n_kv + j) * rg, step1 = (long long)a.own.n_seq * n_kv * rg;
+    // where a part's (maximum, sum) and values are: prefix parts, then own parts
+    const int tile = idx_div(v, p.tile), in0 = v - tile * p.tile, in1 = v - b * rg;
+    const size_t step0 = (size_t)n_kv * p.tiles * p.tile, step1 = (size_t)n_kv * p.n_vec;
+    const size_t slot0 = (size_t)(j * p.tiles + tile) * p.tile, slot1 = (size_t)p.own0 + (size_t)(b * n_kv + j) * rg;
+    const float4 *const values = reinterpret_cast<const float4 *>(opart);
+    struct Place {
+        const float2 *ml;
+        const float4 *x;
+    };
+    const Place own = {ml + slot1 + in1, values + slot1 * 32 + quad * rg + in1};
+    Place at;
+    if (c_begin < p.n_parts)
+        at = {ml + slot0 + c_begin * step0 + in0, values + (slot0 + c_begin * step0) * 32 + quad * p.tile + in0};
+    else
+        at = {own.ml + (c_begin - p.n_parts) * step1, own.x + (c_begin - p.n_parts) * step1 * 32};
+    auto advance = [&](Place &q, int c) {       // from part c to part c + 1
+        if (c + 1 == p.n_parts) {
+            q = own;
+        } else {
+            const size_t step = c < p.n_parts ? step0 : step1;
+            q.ml += step;
+            q.x += step * 32;
+        }
+    };
     float2 w[kJoinUnroll];
-    float4 x[kJoinUnroll];
+    float4 x[kJoinUnroll][2];
     auto load = [&](int c) {        // parts c .. c + kJoinUnroll - 1 of this run
 #pragma unroll
         for (int u = 0; u < kJoinUnroll; ++u) {
             w[u] = make_float2(-INFINITY, 0.f);
             if (c + u < c_end) {
-                const bool shared = c + u < p.n_parts;
-                const long long slot = shared ? slot0 + (c + u) * step0 : slot1 + (c + u - p.n_parts) * step1;
-                w[u] = ml[slot + (shared ? in0 : in1)];
-                x[u] = __ldcs(reinterpret_cast<const float4 *>(opart) + slot * 32 + quad * (shared ? p.tile : rg) +
-                              (shared ? in0 : in1));
+                w[u] = *at.ml;
+                x[u][0] = __ldcs(at.x);
+                x[u][1] = __ldcs(at.x + (c + u < p.n_parts ? p.tile : rg));
+                advance(at, c + u);
             }
         }
     };
@@ -891,14 +913,17 @@ __global__ void __launch_bounds__(32 * kJoinRuns * kJoinQuads, 4) attn_batch_joi
     float top = -INFINITY;
 #pragma unroll
     for (int u = 0; u < kJoinUnroll; ++u) top = fmaxf(top, w[u].x);
-    for (int c = c_begin + kJoinUnroll; c < c_end; ++c)
-        top = fmaxf(top, (c < p.n_parts ? ml[slot0 + c * step0 + in0] : ml[slot1 + (c - p.n_parts) * step1 + in1]).x);
+    Place far = at;
+    for (int c = c_begin + kJoinUnroll; c < c_end; ++c) {
+        top = fmaxf(top, far.ml->x);
+        advance(far, c);
+    }
     if (col == 0) s_top[run][lane] = top;
     __syncthreads();
     top = fmaxf(fmaxf(s_top[0][lane], s_top[1][lane]), fmaxf(s_top[2][lane], s_top[3][lane]));
     if (top == -INFINITY) top = 0.f;
     float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
     for (int c = c_begin; c < c_end; c += kJoinUnroll) {
         if (c > c_begin) load(c);
 #pragma unroll
@@ -906,31 +931,42 @@ __global__ void __launch_bounds__(32 * kJoinRuns * kJoinQuads, 4) attn_batch_joi
             if (c + u >= c_end) break;
             const float f = ex2_approx((w[u].x - top) * kScaleLog2);
             l = fmaf(w[u].y, f, l);
-            o.x = fmaf(x[u].x, f, o.x);
-            o.y = fmaf(x[u].y, f, o.y);
-            o.z = fmaf(x[u].z, f, o.z);
-            o.w = fmaf(x[u].w, f, o.w);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                o[i].x = fmaf(x[u][i].x, f, o[i].x);
+                o[i].y = fmaf(x[u][i].y, f, o[i].y);
+                o[i].z = fmaf(x[u][i].z, f, o[i].z);
+                o[i].w = fmaf(x[u][i].w, f, o[i].w);
+            }
         }
     }
-    s_o[run][col][lane] = o;
+    if (run != 0) {
+        s_o[run][col][0][lane] = o[0];
+        s_o[run][col][1][lane] = o[1];
+    }
     if (col == 0) s_l[run][lane] = l;
     __syncthreads();
     if (run != 0 || v >= p.n_vec) return;
     l = s_l[0][lane];
+    uint4 y = make_uint4(0u, 0u, 0u, 0u);       // idle
 #pragma unroll
-    for (int i = 1; i < kJoinRuns; ++i) {
-        const float4 t = s_o[i][col][lane];
-        l += s_l[i][lane];
-        o = make_float4(o.x + t.x, o.y + t.y, o.z + t.z, o.w + t.w);
+    for (int r = 1; r < kJoinRuns; ++r) {
+        l += s_l[r][lane];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 t = s_o[r][col][i][lane];
+            o[i] = make_float4(o[i].x + t.x, o[i].y + t.y, o[i].z + t.z, o[i].w + t.w);
+        }
     }
-    uint2 r = make_uint2(0u, 0u);       // idle
     if (n > 0) {
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(__fdiv_rn(o.x, l), __fdiv_rn(o.y, l));
-        const __nv_bfloat162 hi = __floats2bfloat162_rn(__fdiv_rn(o.z, l), __fdiv_rn(o.w, l));
-        r = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+        auto pair = [&](float e0, float e1) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(__fdiv_rn(e0, l), __fdiv_rn(e1, l));
+            return *reinterpret_cast<const uint32_t *>(&h);
+        };
+        y = make_uint4(pair(o[0].x, o[0].y), pair(o[0].z, o[0].w), pair(o[1].x, o[1].y), pair(o[1].z, o[1].w));
     }
-    const int row = v / a.group;
-    *(reinterpret_cast<uint2 *>(a.out + (size_t)row * a.ldo + (size_t)(j * a.group + v - row * a.group) * kHeadDim) + quad) = r;
+    const int row = idx_div(v, a.group);
+    *reinterpret_cast<uint4 *>(a.out + (size_t)row * a.ldo + (size_t)(j * a.group + v - row * a.group) * kHeadDim + 4 * quad) = y;
 }
 
 bool encode(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
@@ -1012,7 +1048,7 @@ cudaError_t launch_attn_batch(const AttnBatchArgs &a, cudaStream_t s, const char
     e = e4m3 ? launch_pdl(attn_batch_kernel<true>, grid, dim3(Form<true>::threads), kSmemBytes<true>, s, k)
              : launch_pdl(attn_batch_kernel<false>, grid, dim3(Form<false>::threads), kSmemBytes<false>, s, k);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_batch_join_kernel, dim3((k.p.n_vec + 31) / 32, a.own.n_kv, 32 / kJoinQuads), dim3(32 * kJoinRuns * kJoinQuads), 0, s, a, k.p,
+    return launch_pdl(attn_batch_join_kernel, dim3((k.p.n_vec + 31) / 32, a.own.n_kv, 16 / kJoinPairs), dim3(kJoinThreads), 0, s, a, k.p,
                       (const float *)k.opart, (const float2 *)k.ml, k.next);
 }
 
