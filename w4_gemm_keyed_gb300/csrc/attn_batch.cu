@@ -33,6 +33,7 @@
 #include <atomic>
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 
 #include "attn_batch.cuh"
 #include "tf_tcgen05.cuh"
@@ -967,6 +968,19 @@ __global__ void __launch_bounds__(kJoinThreads, 3) attn_batch_join_kernel(AttnBa
     }
     const int row = idx_div(v, a.group);
     *reinterpret_cast<uint4 *>(a.out + (size_t)row * a.ldo + (size_t)(j * a.group + v - row * a.group) * kHeadDim + 4 * quad) = y;
+}
+
+// cuTensorMapEncodeTiled, or null where the driver has none.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool there = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                               cudaSuccess &&
+                           q == cudaDriverEntryPointSuccess;
+        return there ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
+    }();
+    return fn;
 }
 
 bool encode(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],

@@ -1341,8 +1341,6 @@ cudaError_t launch_pack_nvfp4(const uint8_t *codes, const uint8_t *scales, int K
     return cudaGetLastError();
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return encode_fn(); }
-
 int device_sm_count() {
     static std::atomic<int> cached[kMaxDevices];
     int dev = 0, n = 0;

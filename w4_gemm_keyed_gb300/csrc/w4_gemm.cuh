@@ -3,7 +3,6 @@
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 namespace tfk {
@@ -201,7 +200,5 @@ cudaError_t launch_pack_w4_affine(const uint32_t *codes, const uint16_t *scales,
 cudaError_t launch_pack_w4(const uint8_t *codes, const uint16_t *scales, int K, int N, int G, void *packed,
                            bool interleave_gate_up, cudaStream_t s);
 int device_sm_count();
-// cuTensorMapEncodeTiled, or null where the driver has none.
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 }  // namespace tfk
