@@ -12,7 +12,7 @@
 
 namespace tfk {
 
-constexpr int kKvBf16 = 0, kKvE4m3 = 1;
+constexpr int kKvE4m3 = 1;  // the other format, 0, is bf16
 
 // n_seq caches of n_kv heads and max_len entries.  bf16: tf_kv_cache's layout
 // per sequence.  E4M3: 128 codes per entry, one scale byte per entry and head.
