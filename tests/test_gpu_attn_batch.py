@@ -142,6 +142,47 @@ def test_eight_bit_entries_give_the_bits_of_their_values(tf):
     assert torch.equal(own.attention(c.q_dev(), 8, dev_pos(pos), prefix=prefix, prefix_len=1111), c.run())
 
 
+@pytest.mark.parametrize("B,R,n_kv,g,P", [(40, 2, 2, 8, 1), (23, 3, 1, 8, 127), (17, 16, 2, 2, 1300), (33, 16, 1, 1, 520),
+                                          (13, 8, 3, 7, 641)])
+def test_many_vectors_over_an_eight_bit_prefix(tf, B, R, n_kv, g, P):
+    """Several pairs of query tiles a head: the bits are those of each sequence alone and
+    of a bf16 cache of the same values."""
+    pos = [(97 * b) % 600 for b in range(B)]
+    pos[B // 2] = -1
+    c = Case(tf, 31, B, R, n_kv, g, P, pos, "e4m3")
+    ws = tf.workspace(c.cache.attention_workspace_bytes(g, R, P))
+    whole = c.run(ws=ws).clone()
+    c.check(whole)
+    assert torch.equal(c.run(ws=ws), whole)
+    own, prefix = tf.KVBatch(B, n_kv, c.L), tf.KVBatch(1, n_kv, c.prefix.max_len)
+    own.store(*c.cache.load(dev_pos([0] * B), c.L), dev_pos([0] * B))
+    prefix.store(*c.prefix.load(dev_pos([0]), P), dev_pos([0]))
+    assert torch.equal(own.attention(c.q_dev(), g, dev_pos(pos), prefix=prefix, prefix_len=P), whole)
+    q = c.q_dev()
+    for b in (0, B // 2, B - 1):
+        one = tf.KVBatch(1, n_kv, c.L, "e4m3")
+        for name in ("k", "v", "k_scale", "v_scale"):
+            getattr(one, name).copy_(getattr(c.cache, name)[b:b + 1])
+        got = one.attention(q[b * R:(b + 1) * R], g, dev_pos([pos[b]]), prefix=c.prefix, prefix_len=P, ws=ws)
+        assert torch.equal(got, whole[b * R:(b + 1) * R]), b
+    assert torch.equal(c.run(ws=ws), whole)     # the workspace served the smaller calls in between
+
+
+def test_many_vectors_over_a_prefix_with_nonfinite_entries(tf):
+    """A NaN vector of the prefix reaches its head's rows and no other head's; what lies
+    behind the prefix's last entry reaches none."""
+    B, R, g, P = 40, 2, 8, 700
+    c = Case(tf, 32, B, R, 2, g, P, [b % 5 for b in range(B)], "e4m3")
+    want = c.run().clone().reshape(B * R, 2, g * D)
+    c.prefix.k_scale[:, :, P:] = 255
+    c.prefix.v_scale[:, :, P:] = 255
+    assert torch.equal(c.run().reshape(B * R, 2, g * D), want)
+    c.prefix.v_scale[0, 1, 600] = 255
+    c.prefix.v[0, 1, 600] = 0
+    got = c.run().reshape(B * R, 2, g * D)
+    assert torch.equal(got[:, 0], want[:, 0]) and bool(got[:, 1].isnan().all())
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 def test_entries_no_row_sees_may_hold_anything(tf, fmt):
     """NaN, infinities and garbage past every sequence's last row and past the prefix."""
