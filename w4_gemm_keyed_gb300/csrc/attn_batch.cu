@@ -29,7 +29,7 @@
 // entries 449 us, 1.21 PFLOP/s; of that the steps 320, passing from item to item 42,
 // joining 55).  Few rows, HBM: 12 rows x 20 heads over 130001 entries 53 us, 5.0
 // TB/s.  E4M3 caches with many rows, the issue slots that expansion shares with
-// the softmax: 240 rows x 64 heads over 20000 entries 216 us.
+// the softmax: 240 rows x 64 heads over 20000 entries 213 us.
 #include <atomic>
 
 #include <cuda.h>
@@ -64,8 +64,10 @@ constexpr int kExpandWarp = 12, kExpandWarps = 8;
 // the products are those of a bf16 cache holding the same values.
 template <bool E4M3>
 struct Form {
-    static constexpr int stages = E4M3 ? 4 : 5;         // bf16 K and V tiles in shared memory
-    static constexpr int raw = E4M3 ? 2 : 0;            // E4M3 tiles on their way
+    static constexpr int stages = E4M3 ? 3 : 5;         // bf16 K and V tiles in shared memory
+    // E4M3 tiles on their way (3 + 3: 213 us and 71.9 us at 240 rows over 20000 entries and
+    // 12 rows over 130001; 4 + 2: 214.6 and 73.5, 3 + 4 as 3 + 3)
+    static constexpr int raw = E4M3 ? 3 : 0;
     static constexpr int threads = E4M3 ? 640 : 384;
     static constexpr int readers = kSoftmaxWarps + 1 + (E4M3 ? kExpandWarps : 0);  // of the item ring
     // registers a thread: the softmax warps' and the others', together no more
@@ -139,7 +141,7 @@ struct KernelArgs {
 // S0 and S1 of one-tile items and S0 of two-tile items are read by the first
 // softmax group (0, 1, 0), S1 of two-tile items by the second (2).
 struct __align__(16) Shared {
-    uint64_t kv_full[5], kv_empty[5], raw_full[4], raw_empty[4];
+    uint64_t kv_full[5], kv_empty[5], raw_full[3], raw_empty[3];
     uint64_t q_full[2], q_empty[2], s_full[3], p_full[2][2], o_done[2];
     uint64_t item_full[kRing], item_empty[kRing], drain;
     Item item[kRing];
