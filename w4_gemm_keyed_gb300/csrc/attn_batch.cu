@@ -25,11 +25,11 @@
 //
 // What bounds it (GB300, us measured): many rows, the tensor cores and the
 // hand-over between them and the softmax: a step of two tiles and 128 keys takes
-// 2,860 cycles where its products take 2,080 (512 rows x 64 heads over 32768
-// entries 449 us, 1.21 PFLOP/s; of that the steps 320, passing from item to item 42,
+// 2,700 cycles where its products take 2,080 (512 rows x 64 heads over 32768
+// entries 430 us, 1.26 PFLOP/s; of that the steps 300, passing from item to item 42,
 // joining 55).  Few rows, HBM: 12 rows x 20 heads over 130001 entries 53 us, 5.0
 // TB/s.  E4M3 caches with many rows, the issue slots that expansion shares with
-// the softmax: 240 rows x 64 heads over 20000 entries 213 us.
+// the softmax: 240 rows x 64 heads over 20000 entries 212 us.
 #include <atomic>
 
 #include <cuda.h>
@@ -638,13 +638,18 @@ __device__ void softmax(const KernelArgs &k, Shared *sh, uint32_t tmem) {
     for (unsigned n = 0;; ++n) {
         const int slot = n % kRing;
         if (!wait_or_abort(sh, &sh->item_full[slot], (n / kRing) & 1)) return;
-        const Item it = sh->item[slot];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
+        const Item &it = sh->item[slot];        // read where it is needed: registers are short
         if (it.n_vec == 0) return;
+        auto release = [&] {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
+        };
         const bool two = it.n_vec > k.p.tile;
         const int tiles = (it.n_keys + kTile - 1) / kTile;
-        if (wg == 1 && !two) continue;
+        if (wg == 1 && !two) {
+            release();
+            continue;
+        }
         const int v = 32 * (warp & 3) + lane;               // vector within the tile
         const int n_here = min(k.p.tile, it.n_vec - wg * k.p.tile);     // of this tile
         const bool active = 32 * (warp & 3) < n_here;
@@ -659,29 +664,46 @@ __device__ void softmax(const KernelArgs &k, Shared *sh, uint32_t tmem) {
                 const uint32_t t_s = tmem + kTmemS + buf * kTile + my_lanes;
                 const int last = lim - i * kTile;
                 const bool part_seen = __any_sync(0xFFFFFFFFu, last < kTile - 1);
-                // 64 scores at a time in registers: the upper half for its maximum
-                // first, and once more after the lower half's weights have been stored
-                uint32_t x[64];
+                // bf16 caches: all scores in registers (512 rows over 32768 entries: 430 us; with
+                // the upper half read again for its weights, as below, 449).  The softmax of
+                // E4M3 caches has fewer: 64 scores at a time, the upper half for its maximum
+                // first, and once more after the lower half's weights have been stored; its
+                // loops stay rolled, as instructions are fetched anew for every role between.
+                uint32_t x[64], y[E4M3 ? 1 : 64];
                 float mt[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                auto load = [&](int c0) {
-                    tc_ld32(t_s + c0, x);
-                    tc_ld32(t_s + c0 + 32, x + 32);
-                    tc_wait_ld();
-                    tc_pin32(x);
-                    tc_pin32(x + 32);
+                auto fetch = [&](int c0, uint32_t *s) {
+                    tc_ld32(t_s + c0, s);
+                    tc_ld32(t_s + c0 + 32, s + 32);
+                };
+                auto settle = [&](int c0, uint32_t *s) {    // after tc_wait_ld
+                    tc_pin32(s);
+                    tc_pin32(s + 32);
                     if (part_seen) {
 #pragma unroll
-                        for (int c = 0; c < 64; ++c) x[c] = c0 + c <= last ? x[c] : 0xFF800000u;
+                        for (int c = 0; c < 64; ++c) s[c] = c0 + c <= last ? s[c] : 0xFF800000u;
                     }
                 };
-                // rolled, here and below: the loop bodies are long, and instructions are
-                // fetched anew for every role that runs between
-#pragma unroll 1
-                for (int c0 = 64; c0 >= 0; c0 -= 64) {
-                    load(c0);
+                auto tops = [&](const uint32_t *s) {
 #pragma unroll
                     for (int c = 0; c < 64; c += 2)
-                        mt[(c >> 1) & 3] = max3(mt[(c >> 1) & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+                        mt[(c >> 1) & 3] = max3(mt[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+                };
+                if constexpr (E4M3) {
+#pragma unroll 1
+                    for (int c0 = 64; c0 >= 0; c0 -= 64) {
+                        fetch(c0, x);
+                        tc_wait_ld();
+                        settle(c0, x);
+                        tops(x);
+                    }
+                } else {
+                    fetch(0, x);
+                    fetch(64, y);
+                    tc_wait_ld();
+                    settle(0, x);
+                    settle(64, y);
+                    tops(x);
+                    tops(y);
                 }
                 const float top = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
                 const bool moved = top > m + kMaxSlack;     // true for the first visible scores (m = -inf)
@@ -711,28 +733,40 @@ __device__ void softmax(const KernelArgs &k, Shared *sh, uint32_t tmem) {
                 const float mc = m == -INFINITY ? 0.f : m * kScaleLog2;
                 const uint64_t scale2 = pack2(kScaleLog2, kScaleLog2), shift2 = pack2(-mc, -mc);
                 uint64_t sum2[2] = {0ull, 0ull};
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    if (h == 1) load(64);
+                auto weigh = [&](uint32_t *s, int h) {
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
                         float a, b;
-                        unpack2(fma2(pack2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), scale2, shift2), a, b);
+                        unpack2(fma2(pack2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), scale2, shift2), a, b);
                         a = ex2_approx(a);
                         b = ex2_approx(b);
                         sum2[c & 1] = add2(sum2[c & 1], pack2(a, b));
                         // weights meet V as bf16 (off by at most 2^-8 of each, half a step);
                         // the sum keeps them whole
                         const __nv_bfloat162 pk = __floats2bfloat162_rn(a, b);
-                        x[c] = *reinterpret_cast<const uint32_t *>(&pk);
+                        s[c] = *reinterpret_cast<const uint32_t *>(&pk);
                     }
-                    tc_st32(t_s + 32 * h, x);
+                    tc_st32(t_s + 32 * h, s);
                     if (h == 0) {       // the product with the first 64 keys may start
                         tc_wait_st();
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&sh->p_full[buf][0]);
                     }
+                };
+                if constexpr (E4M3) {
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        if (h == 1) {
+                            fetch(64, x);
+                            tc_wait_ld();
+                            settle(64, x);
+                        }
+                        weigh(x, h);
+                    }
+                } else {
+                    weigh(x, 0);
+                    weigh(y, 1);
                 }
                 float s0, s1, s2, s3;
                 unpack2(sum2[0], s0, s1);
@@ -753,7 +787,10 @@ __device__ void softmax(const KernelArgs &k, Shared *sh, uint32_t tmem) {
         const int first = max(0, it.lim0 + 1), end = it.n_keys - 1;
         const bool bad = active && it.b >= 0 && first <= end && any_nonfinite<E4M3>(k, it, first, end, lane);
         if (!wait_or_abort(sh, &sh->o_done[wg], (o_uses - 1) & 1)) return;
-        if (!active) continue;
+        if (!active) {
+            release();
+            continue;
+        }
         tc_fence_after();
         const bool store = v < n_here;
         const long long part = it.part + (wg ? k.p.tile : 0);
@@ -780,6 +817,7 @@ __device__ void softmax(const KernelArgs &k, Shared *sh, uint32_t tmem) {
             }
         }
         tc_fence_before();      // the reads of O precede this warp's next arrival on p_full
+        release();
     }
 }
 
