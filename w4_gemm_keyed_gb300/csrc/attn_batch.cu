@@ -25,11 +25,11 @@
 //
 // What bounds it (GB300, us measured): many rows, the tensor cores and the
 // hand-over between them and the softmax: a step of two tiles and 128 keys takes
-// 2,700 cycles where its products take 2,080 (512 rows x 64 heads over 32768
-// entries 430 us, 1.26 PFLOP/s; of that the steps 300, passing from item to item 42,
-// joining 55).  Few rows, HBM: 12 rows x 20 heads over 130001 entries 53 us, 5.0
+// about 2,700 cycles where its products take 2,080 (512 rows x 64 heads over 32768
+// entries 428 us, 1.27 PFLOP/s; of that the steps about 300, passing from item to item 42,
+// joining 55).  Few rows, HBM: 12 rows x 20 heads over 130001 entries 51 us, 5.2
 // TB/s.  E4M3 caches with many rows, the issue slots that expansion shares with
-// the softmax: 240 rows x 64 heads over 20000 entries 212 us.
+// the softmax: 240 rows x 64 heads over 20000 entries 211 us.
 #include <atomic>
 
 #include <cuda.h>
@@ -71,8 +71,10 @@ struct Form {
     static constexpr int threads = E4M3 ? 640 : 384;
     static constexpr int readers = kSoftmaxWarps + 1 + (E4M3 ? kExpandWarps : 0);  // of the item ring
     // registers a thread: the softmax warps' and the others', together no more
-    // than the launch's share (96 a thread of 640, 168 of 384)
-    static constexpr int regs_softmax = E4M3 ? 144 : 208, regs_other = E4M3 ? 64 : 88;
+    // than the launch's share (96 a thread of 640, 168 of 384).  With 144 and 64, 208
+    // and 88, 240 rows (E4M3) and 512 rows (bf16) took 212 and 432 us; with these 211
+    // and 428.
+    static constexpr int regs_softmax = E4M3 ? 168 : 216, regs_other = E4M3 ? 48 : 72;
     static_assert(256 * regs_softmax + (threads - 256) * regs_other <= threads * (E4M3 ? 96 : 168), "register split");
 };
 constexpr int kRawBytes = kTile * kHeadDim;
@@ -664,7 +666,7 @@ __device__ void softmax(const KernelArgs &k, Shared *sh, uint32_t tmem) {
                 const uint32_t t_s = tmem + kTmemS + buf * kTile + my_lanes;
                 const int last = lim - i * kTile;
                 const bool part_seen = __any_sync(0xFFFFFFFFu, last < kTile - 1);
-                // bf16 caches: all scores in registers (512 rows over 32768 entries: 430 us; with
+                // bf16 caches: all scores in registers (512 rows over 32768 entries: 428 us; with
                 // the upper half read again for its weights, as below, 449).  The softmax of
                 // E4M3 caches has fewer: 64 scores at a time, the upper half for its maximum
                 // first, and once more after the lower half's weights have been stored; its
