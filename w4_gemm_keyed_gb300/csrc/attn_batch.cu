@@ -26,10 +26,10 @@
 // What bounds it (GB300, us measured): many rows, the tensor cores and the
 // hand-over between them and the softmax: a step of two tiles and 128 keys takes
 // about 2,700 cycles where its products take 2,080 (512 rows x 64 heads over 32768
-// entries 428 us, 1.27 PFLOP/s; of that the steps about 300, passing from item to item 42,
-// joining 55).  Few rows, HBM: 12 rows x 20 heads over 130001 entries 51 us, 5.2
+// entries 420 us, 1.29 PFLOP/s; of that the steps about 300, passing from item to item 42,
+// joining about 47).  Few rows, HBM: 12 rows x 20 heads over 130001 entries 51 us, 5.2
 // TB/s.  E4M3 caches with many rows, the issue slots that expansion shares with
-// the softmax: 240 rows x 64 heads over 20000 entries 211 us.
+// the softmax: 240 rows x 64 heads over 20000 entries 208 us.
 #include <atomic>
 
 #include <cuda.h>
@@ -884,23 +884,23 @@ __global__ void __launch_bounds__(Form<E4M3>::threads, 1) attn_batch_kernel(cons
 }
 
 // ------------------------------------------------------------------ joining the parts
-// A CTA takes 32 query vectors (lanes) and four column quads of one KV head; its
-// eight warps are two pairs of quads times four runs of consecutive parts.  A
-// run's parts are folded in ascending order (prefix parts first) against the
-// maximum of all the vector's parts, then the runs in ascending order: an order
-// that the number of the vector's parts fixes.  Where there are many vectors, 520
-// bytes per vector and part from HBM or L2 and the instructions that find them
-// bound it (with a quad a thread and 64-bit products for every part's place, 512
-// rows x 64 heads x 14 parts took 74 us); where there are few, the chain of
-// three loads does.
-constexpr int kJoinRuns = 4, kJoinPairs = 2, kJoinUnroll = 4, kJoinThreads = 32 * kJoinRuns * kJoinPairs;
+// A CTA takes 32 query vectors (lanes) and two column quads of one KV head; its
+// four warps are four runs of consecutive parts.  A run's parts are folded in
+// ascending order (prefix parts first) against the maximum of all the vector's
+// parts, then the runs in ascending order: an order that the number of the vector's
+// parts fixes.  Where there are many vectors, 520 bytes per vector and part from HBM
+// or L2 and the instructions that find them bound it (with a quad a thread and 64-bit
+// products for every part's place, 512 rows x 64 heads x 14 parts took 74 us, with
+// two quads 55; CTAs of four quads, 256 threads, made the whole call 424 us, these
+// 416); where there are few, the chain of three loads does.
+constexpr int kJoinRuns = 4, kJoinUnroll = 4, kJoinThreads = 32 * kJoinRuns;
 
-__global__ void __launch_bounds__(kJoinThreads, 3) attn_batch_join_kernel(AttnBatchArgs a, Plan p, const float *opart,
+__global__ void __launch_bounds__(kJoinThreads, 6) attn_batch_join_kernel(AttnBatchArgs a, Plan p, const float *opart,
                                                                           const float2 *ml, unsigned *next) {
     __shared__ float s_top[kJoinRuns][32], s_l[kJoinRuns][32];
-    __shared__ float4 s_o[kJoinRuns][kJoinPairs][2][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, run = warp / kJoinPairs, col = warp % kJoinPairs;
-    const int quad = 2 * (blockIdx.z * kJoinPairs + col), n_kv = a.own.n_kv, rg = a.R * a.group, j = blockIdx.y;
+    __shared__ float4 s_o[kJoinRuns][2][32];
+    const int lane = threadIdx.x & 31, run = threadIdx.x >> 5, quad = 2 * blockIdx.z;
+    const int n_kv = a.own.n_kv, rg = a.R * a.group, j = blockIdx.y;
     const int v = blockIdx.x * 32 + lane;
     int n = 0, b = 0;
     if (v < p.n_vec) {
@@ -961,7 +961,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) attn_batch_join_kernel(AttnBa
         top = fmaxf(top, far.ml->x);
         advance(far, c);
     }
-    if (col == 0) s_top[run][lane] = top;
+    s_top[run][lane] = top;
     __syncthreads();
     top = fmaxf(fmaxf(s_top[0][lane], s_top[1][lane]), fmaxf(s_top[2][lane], s_top[3][lane]));
     if (top == -INFINITY) top = 0.f;
@@ -984,10 +984,10 @@ __global__ void __launch_bounds__(kJoinThreads, 3) attn_batch_join_kernel(AttnBa
         }
     }
     if (run != 0) {
-        s_o[run][col][0][lane] = o[0];
-        s_o[run][col][1][lane] = o[1];
+        s_o[run][0][lane] = o[0];
+        s_o[run][1][lane] = o[1];
     }
-    if (col == 0) s_l[run][lane] = l;
+    s_l[run][lane] = l;
     __syncthreads();
     if (run != 0 || v >= p.n_vec) return;
     l = s_l[0][lane];
@@ -997,7 +997,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) attn_batch_join_kernel(AttnBa
         l += s_l[r][lane];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const float4 t = s_o[r][col][i][lane];
+            const float4 t = s_o[r][i][lane];
             o[i] = make_float4(o[i].x + t.x, o[i].y + t.y, o[i].z + t.z, o[i].w + t.w);
         }
     }
@@ -1104,7 +1104,7 @@ cudaError_t launch_attn_batch(const AttnBatchArgs &a, cudaStream_t s, const char
     e = e4m3 ? launch_pdl(attn_batch_kernel<true>, grid, dim3(Form<true>::threads), kSmemBytes<true>, s, k)
              : launch_pdl(attn_batch_kernel<false>, grid, dim3(Form<false>::threads), kSmemBytes<false>, s, k);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_batch_join_kernel, dim3((k.p.n_vec + 31) / 32, a.own.n_kv, 16 / kJoinPairs), dim3(kJoinThreads), 0, s, a, k.p,
+    return launch_pdl(attn_batch_join_kernel, dim3((k.p.n_vec + 31) / 32, a.own.n_kv, 16), dim3(kJoinThreads), 0, s, a, k.p,
                       (const float *)k.opart, (const float2 *)k.ml, k.next);
 }
 
