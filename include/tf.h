@@ -26,8 +26,13 @@
  *   the matching *_workspace_bytes() query returns, 256-byte aligned, and
  *   zero-filled before its first use (the kernels leave the parts they
  *   need zeroed when they finish, so a workspace can be reused by later calls
- *   on the same stream without clearing it again).  Calls that overlap in time
- *   must not share a workspace.
+ *   of the same entry point for the same matrix, layer, model or cache on the
+ *   same stream without clearing it again).  The lane GEMMs, tf_decoder_block,
+ *   tf_embed_rows, tf_kv_append, tf_kv_store, tf_kv_load and tf_attention_batch
+ *   may use one workspace in turn, for any matrices and caches, and tf_attention_batch
+ *   any that was zero-filled once; otherwise a workspace is cleared before
+ *   another entry point uses it.  Its first 256 bytes hold no operator's
+ *   scratch.  Calls that overlap in time must not share a workspace.
  * - Host-side argument errors return TF_ERR_INVALID_ARG / TF_ERR_UNSUPPORTED
  *   before anything is enqueued; tf_last_error() then describes the problem.
  *   Errors that only the device can see (a non-finite logit, an out-of-range

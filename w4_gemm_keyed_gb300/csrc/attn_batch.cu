@@ -1060,9 +1060,15 @@ bool encode_queries(CUtensorMap *m, const AttnBatchArgs &a, const char **why) {
 
 }  // namespace
 
+// Workspace: the status block, whose byte 128 is the item counter, then the lane
+// GEMM's split-K counters, not used here, then the parts' results.  No operator
+// has scratch in the status block, so the counter is zero whatever a workspace
+// was used for before, and a GEMM that uses it next finds its counters as it left them.
+constexpr size_t kCounterAt = 128, kResultsAt = 256 + kCounterBytes;
+
 size_t attn_batch_bytes(const KvBatch &own, int prefix_len, int group, int R) {
     const Plan p = plan_of(own, prefix_len, group, R);
-    return 512 + size_t(p.slots) * (kHeadDim * sizeof(float) + sizeof(float2));
+    return kResultsAt + size_t(p.slots) * (kHeadDim * sizeof(float) + sizeof(float2));
 }
 
 cudaError_t launch_attn_batch(const AttnBatchArgs &a, cudaStream_t s, const char **why) {
@@ -1083,9 +1089,9 @@ cudaError_t launch_attn_batch(const AttnBatchArgs &a, cudaStream_t s, const char
     k.a = a;
     k.p = plan_of(a.own, a.prefix_len, a.group, a.R);
     char *base = static_cast<char *>(a.ws);
-    k.next = reinterpret_cast<unsigned *>(base + 256);
-    k.opart = reinterpret_cast<float *>(base + 512);
-    k.ml = reinterpret_cast<float2 *>(base + 512 + size_t(k.p.slots) * kHeadDim * sizeof(float));
+    k.next = reinterpret_cast<unsigned *>(base + kCounterAt);
+    k.opart = reinterpret_cast<float *>(base + kResultsAt);
+    k.ml = reinterpret_cast<float2 *>(base + kResultsAt + size_t(k.p.slots) * kHeadDim * sizeof(float));
     const bool e4m3 = a.own.format == kKvE4m3;
     if (!encode_queries(&k.map[4], a, why)) return cudaErrorInvalidValue;
     if (!e4m3) {

@@ -15,7 +15,7 @@ struct AttnBatchArgs {
     uint16_t *out;          // bf16 [n_seq * R][ldo]
     int ldo;
     int *err;
-    void *ws;               // attn_batch_bytes() of scratch, its first 256 bytes the status word
+    void *ws;               // attn_batch_bytes(): the status block (256 bytes), then scratch
 };
 
 size_t attn_batch_bytes(const KvBatch &own, int prefix_len, int group, int R);
