@@ -89,6 +89,24 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
     return false;
 }
 
+// A wait among the roles of one CTA: gives up after kWaitLimit polls, then sets
+// *abort (shared memory), or once another wait has set it.
+__device__ __forceinline__ bool mbar_wait_or_abort(int *abort, uint64_t *bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity) || mbar_try_wait(bar, parity)) return true;
+    for (uint32_t i = 0; !mbar_try_wait(bar, parity); ++i) {
+        if (i == kWaitLimit) *reinterpret_cast<volatile int *>(abort) = 1;
+        if (*reinterpret_cast<volatile int *>(abort)) return false;
+    }
+    return true;
+}
+
+// The same for a converged warp, with one answer: lanes may see the phase end and
+// *abort in either order, and one that left alone would be missed by the warp's next
+// collective instruction.
+__device__ __forceinline__ bool mbar_warp_wait_or_abort(int *abort, uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(abort, bar, parity));
+}
+
 __device__ __forceinline__ uint64_t l2_policy_evict_first() {
     uint64_t pol;
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
