@@ -177,9 +177,25 @@ def _stream(stream=None):
     return stream.cuda_stream if stream is not None else _current_raw_stream()
 
 
-def workspace(nbytes: int, device="cuda") -> torch.Tensor:
-    """Zero-filled device scratch (the caching allocator aligns to >= 256 B)."""
-    return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+def workspace(nbytes: int, device="cuda", stream=None) -> torch.Tensor:
+    """Zero-filled device scratch (the caching allocator aligns to >= 256 B), for calls on
+    `stream` (default: the current one)."""
+    if stream is None:
+        return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    # filled, and handed out again once freed, in the order of the stream that uses it
+    with torch.cuda.stream(stream):
+        return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+
+
+def _empty(shape, dtype, device, stream=None) -> torch.Tensor:
+    """A call's own output: memory of the stream that the call runs on, so that nothing
+    still queued elsewhere uses it, marked as used on the caller's stream too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 def workspace_status(ws: torch.Tensor, stream=None) -> int:
@@ -591,7 +607,7 @@ def qk_norm_rope(x: torch.Tensor, n_q: int, n_kv: int, pos: torch.Tensor, turns:
             _refuse(f"turns must be a contiguous 1-D int64 tensor on {dev}")
         rot, turned = 2 * turns.numel(), turns.data_ptr()
     if out is None:
-        out, ldo = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev), cols
+        out, ldo = _empty((rows, cols), torch.bfloat16, dev, stream), cols
     else:
         ldo = _bits16(out, "out", rows, cols, dev)
     st = load().tf_qk_norm_rope(x.data_ptr(), fp32, ldx, B, rows // B, n_q, n_kv, n_v, wq, wk, eps, turned, rot,
@@ -656,7 +672,9 @@ class KVBatch:
             _refuse("k_new and v_new must have the same rows and row stride")
         R, at = self._rows(n), self._pos(pos)
         if ws is None:
-            ws = workspace(256, device=dev)
+            ws = workspace(256, dev, stream)
+            if stream is not None:
+                ws.record_stream(torch.cuda.current_stream(dev))
         st = load().tf_kv_store(self._c, k_new.data_ptr(), v_new.data_ptr(), ld, R, at, _ptr(ws), ws.numel(),
                                 _stream(stream))
         if st:
@@ -671,16 +689,15 @@ class KVBatch:
         if not 0 < R <= self.max_len:
             _refuse(f"R={R} outside [1, max_len={self.max_len}]")
         if k is None and v is None:
-            k = torch.empty((n, cols), dtype=torch.bfloat16, device=dev)
-            v, ld = torch.empty_like(k), cols
+            k, v, ld = *(_empty((n, cols), torch.bfloat16, dev, stream) for _ in range(2)), cols
         else:
-            k = torch.empty_like(v) if k is None else k
-            v = torch.empty_like(k) if v is None else v
+            k = _empty(v.shape, v.dtype, dev, stream) if k is None else k
+            v = _empty(k.shape, k.dtype, dev, stream) if v is None else v
             ld = _bits16(k, "k", n, cols, dev)
             if _bits16(v, "v", n, cols, dev) != ld:
                 _refuse("k and v must have the same row stride")
         if ws is None:
-            ws = workspace(256, device=dev)
+            ws = workspace(256, dev, stream)
         st = load().tf_kv_load(self._c, at, R, k.data_ptr(), v.data_ptr(), ld, _ptr(ws), ws.numel(), _stream(stream))
         if st:
             _check(st)
@@ -698,11 +715,11 @@ class KVBatch:
         ldq = _bits16(q, "q", 1, cols, dev)
         R, at = self._rows(n), self._pos(pos)
         if out is None:
-            out, ldo = torch.empty((n, cols), dtype=torch.bfloat16, device=dev), cols
+            out, ldo = _empty((n, cols), torch.bfloat16, dev, stream), cols
         else:
             ldo = _bits16(out, "out", n, cols, dev)
         if ws is None:
-            ws = workspace(self.attention_workspace_bytes(group, R, prefix_len), device=dev)
+            ws = workspace(self.attention_workspace_bytes(group, R, prefix_len), dev, stream)
         st = load().tf_attention_batch(self._c, prefix._c if prefix is not None else None, prefix_len, group,
                                        q.data_ptr(), ldq, R, at, out.data_ptr(), ldo, _ptr(ws), ws.numel(),
                                        _stream(stream))
