@@ -49,6 +49,7 @@ def rec(monkeypatch):
     lib.tf_attention_batch_workspace_bytes = lambda *a: 1024
     monkeypatch.setattr(tf, "load", lambda *a: lib)
     monkeypatch.setattr(tf, "_ptr", lambda t: None if t is None else t.data_ptr())
+    monkeypatch.setattr(tf, "_check_rows_out", lambda *a: None)      # wants CUDA tensors
     monkeypatch.setattr(torch.cuda, "stream", r.stream)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: "current")
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: r.marked.append((t, s)), raising=False)
@@ -114,3 +115,72 @@ def test_rotation(rec, monkeypatch):
     x = torch.ones((4, 6 * D)).as_subclass(OnDevice)
     out = tf.qk_norm_rope(x, 2, 2, pos(2), stream=SIDE)
     assert rec.made and all(side for _, side in rec.made) and marked(rec, out)
+
+
+def w4(K=128, N=64):
+    return tf.W4Matrix(int_(torch.uint8, 256), K, N, 64)
+
+
+def f32(*shape):
+    return torch.ones(shape, dtype=torch.float32)
+
+
+def int_(dt, *shape):
+    return torch.ones(shape, dtype=dt)
+
+
+def moe():
+    return tf.MoeLayer(int_(torch.uint8, 8), int_(torch.uint8, 8), 64, 64, 4, 2, 32)
+
+
+def kv_cache():
+    return tf.KVCache(2, 256, device="cpu")
+
+
+OTHER_CALLS = dict(
+    lane_gemm_w4=lambda: tf.lane_gemm_w4(w4(), bf16(2, 128), stream=SIDE),
+    lane_gemm_w4_accumulate=lambda: tf.lane_gemm_w4_accumulate(w4(), bf16(2, 128), f32(2, 64), stream=SIDE),
+    lane_gemm_nvfp4=lambda: tf.lane_gemm_nvfp4(tf.Nvfp4Matrix(int_(torch.uint8, 8), 128, 64, 1.0), bf16(2, 128),
+                                               stream=SIDE),
+    cast_bf16=lambda: tf.cast_bf16(f32(2, 64), stream=SIDE),
+    rmsnorm_bf16=lambda: tf.rmsnorm_bf16(f32(2, 64), 1e-6, stream=SIDE),
+    keyed_sample=lambda: tf.keyed_sample(f32(2, 100), 0.7, 20, 0.9, 1, stream=SIDE),
+    lmhead_sample=lambda: tf.lmhead_sample(w4(), bf16(2, 128), 0.7, 20, 0.9, 1, stream=SIDE),
+    keyed_hash=lambda: tf.keyed_hash(pos(3), pos(3), int_(torch.int32, 3), stream=SIDE),
+    accept=lambda: tf.accept(int_(torch.int32, 2), int_(torch.int32, 3), stream=SIDE),
+    selfcheck=lambda: tf.selfcheck_row_invariance(w4(), bf16(16, 128), stream=SIDE),
+    kv_append=lambda: kv_cache().append(bf16(2, 256), bf16(2, 256), pos(1), stream=SIDE),
+    kv_attention=lambda: kv_cache().attention(bf16(2, 256), 1, pos(1), stream=SIDE),
+    moe_w4=lambda: tf.moe_w4(moe(), bf16(2, 64), f32(2, 4), stream=SIDE),
+    pack_w4=lambda: tf.pack_w4(int_(torch.uint8, 64, 64), int_(torch.int16, 64, 2), 64, stream=SIDE).packed,
+    pack_w4_affine=lambda: tf.pack_w4_affine(int_(torch.int32, 64, 16), bf16(64, 2), bf16(64, 2), 64,
+                                             stream=SIDE).packed,
+    pack_nvfp4=lambda: tf.pack_nvfp4(int_(torch.uint8, 64, 64), int_(torch.uint8, 64, 8), 1.0, stream=SIDE).packed,
+)
+
+
+@pytest.mark.parametrize("name", OTHER_CALLS)
+def test_every_other_call(rec, monkeypatch, name):
+    for query in [n for n, _, _ in tf.SIGNATURES if n.endswith("_bytes")]:
+        setattr(tf.load(), query, lambda *a: 512)
+    if name.startswith("kv_"):
+        made = kv_cache()           # the caches themselves are the caller's, made on the current stream
+        monkeypatch.setitem(globals(), "kv_cache", lambda: made)
+        rec.made.clear()
+    got = OTHER_CALLS[name]()
+    assert rec.made and all(side for _, side in rec.made), name
+    for t in got if isinstance(got, tuple) else [got]:
+        if isinstance(t, torch.Tensor) and name != "lane_gemm_w4_accumulate":
+            assert marked(rec, t), name
+
+
+def test_copies_for_the_packers(rec, monkeypatch):
+    inside, real = [], torch.Tensor.contiguous
+
+    def contiguous(t):
+        inside.append(rec.inside > 0)
+        return real(t)
+    monkeypatch.setattr(torch.Tensor, "contiguous", contiguous)
+    tf.load().tf_w4_packed_bytes = lambda *a: 512
+    tf.pack_w4(int_(torch.uint8, 64, 64), int_(torch.int16, 64, 2), 64, stream=SIDE)
+    assert inside == [True, True]

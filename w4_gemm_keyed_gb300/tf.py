@@ -198,6 +198,22 @@ def _empty(shape, dtype, device, stream=None) -> torch.Tensor:
     return t
 
 
+def _contiguous(stream, *tensors):
+    """Contiguous tensors, what has to be copied copied on `stream`."""
+    if stream is None:
+        return [t.contiguous() for t in tensors]
+    with torch.cuda.stream(stream):
+        return [t.contiguous() for t in tensors]
+
+
+def _status_block(device, stream=None) -> torch.Tensor:
+    """The workspace of a call that returns it for its status alone."""
+    ws = workspace(256, device, stream)
+    if stream is not None:
+        ws.record_stream(torch.cuda.current_stream(device))
+    return ws
+
+
 def workspace_status(ws: torch.Tensor, stream=None) -> int:
     code = I32(0)
     _check(load().tf_workspace_status(_ptr(ws), _stream(stream), ctypes.byref(code)))
@@ -231,9 +247,8 @@ def pack_w4(codes: torch.Tensor, scales: torch.Tensor, group: int, gate_up: bool
     if nbytes == 0:
         raise TFError(TF_ERR_UNSUPPORTED, f"unsupported shape K={K} N={N} group={group}")
     if out is None:
-        out = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
-    codes = codes.contiguous()
-    scales = scales.contiguous()
+        out = _empty((nbytes,), torch.uint8, codes.device, stream)
+    codes, scales = _contiguous(stream, codes, scales)
     if gate_up:
         _check(lib.tf_pack_w4_gate_up(_ptr(codes), _ptr(scales), K, N // 2, group, _ptr(out), nbytes, _stream(stream)))
     else:
@@ -252,8 +267,8 @@ def pack_w4_affine(codes: torch.Tensor, scales: torch.Tensor, biases: torch.Tens
     if nbytes == 0:
         raise TFError(TF_ERR_UNSUPPORTED, f"unsupported shape K={K} N={N} group={group}")
     if out is None:
-        out = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
-    codes, scales, biases = codes.contiguous(), scales.contiguous(), biases.contiguous()
+        out = _empty((nbytes,), torch.uint8, codes.device, stream)
+    codes, scales, biases = _contiguous(stream, codes, scales, biases)
     _check(lib.tf_pack_w4_affine(_ptr(codes), _ptr(scales), _ptr(biases), K, N, group, _ptr(out), nbytes,
                                  _stream(stream)))
     return W4Matrix(out, K, N, group, affine=True)
@@ -289,10 +304,10 @@ def lane_gemm_w4(W: W4Matrix, x: torch.Tensor, y: torch.Tensor = None, ws: torch
     _check_rows_in(x, W.K)
     R = x.shape[0]
     if y is None:
-        y = torch.empty((R, W.N), dtype=torch.float32, device=x.device)
+        y = _empty((R, W.N), torch.float32, x.device, stream)
     _check_rows_out(y, R, W.N, x.device)
     if ws is None:
-        ws = workspace(lane_gemm_workspace_bytes(W.K, W.N, W.group), x.device)
+        ws = workspace(lane_gemm_workspace_bytes(W.K, W.N, W.group), x.device, stream)
     wc = W.c()
     _check(lib.tf_lane_gemm_w4(ctypes.byref(wc), _ptr(x), x.stride(0), R, _ptr(y), y.stride(0), _ptr(ws),
                                ws.numel(), _stream(stream)))
@@ -343,8 +358,8 @@ def pack_nvfp4(codes: torch.Tensor, scales: torch.Tensor, global_scale: float, o
     if tuple(scales.shape) != (N, K // 16) or codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
         raise TFError(TF_ERR_INVALID_ARG, "codes must be uint8 [N][K/2] and scales uint8 [N][K/16]")
     if out is None:
-        out = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
-    codes, scales = codes.contiguous(), scales.contiguous()
+        out = _empty((nbytes,), torch.uint8, codes.device, stream)
+    codes, scales = _contiguous(stream, codes, scales)
     _check(load().tf_pack_nvfp4(_ptr(codes), _ptr(scales), K, N, _ptr(out), nbytes, _stream(stream)))
     return Nvfp4Matrix(out, K, N, global_scale)
 
@@ -356,10 +371,10 @@ def lane_gemm_nvfp4(W: Nvfp4Matrix, x: torch.Tensor, y: torch.Tensor = None, ws:
     _check_rows_in(x, W.K)
     R = x.shape[0]
     if y is None:
-        y = torch.empty((R, W.N), dtype=torch.float32, device=x.device)
+        y = _empty((R, W.N), torch.float32, x.device, stream)
     _check_rows_out(y, R, W.N, x.device)
     if ws is None:
-        ws = workspace(int(lib.tf_lane_gemm_nvfp4_workspace_bytes(W.K, W.N)), x.device)
+        ws = workspace(int(lib.tf_lane_gemm_nvfp4_workspace_bytes(W.K, W.N)), x.device, stream)
     _check(lib.tf_lane_gemm_nvfp4(ctypes.byref(W.c()), _ptr(x), x.stride(0), R, _ptr(y), y.stride(0), _ptr(ws),
                                   ws.numel(), _stream(stream)))
     return y
@@ -371,7 +386,7 @@ def lane_gemm_w4_accumulate(W: W4Matrix, x: torch.Tensor, y: torch.Tensor, ws: t
     """y[R][N] (fp32, in place) += W4 linear of bf16 rows x[R][K]."""
     lib = load()
     if ws is None:
-        ws = workspace(lane_gemm_workspace_bytes(W.K, W.N, W.group), x.device)
+        ws = workspace(lane_gemm_workspace_bytes(W.K, W.N, W.group), x.device, stream)
     _check(lib.tf_lane_gemm_w4_accumulate(ctypes.byref(W.c()), _ptr(x), x.stride(0), x.shape[0], _ptr(y), y.stride(0),
                                           _ptr(ws), ws.numel(), _stream(stream)))
     return y
@@ -381,7 +396,7 @@ def cast_bf16(x: torch.Tensor, out: torch.Tensor = None, stream=None) -> torch.T
     """bf16 bits (int16 tensor) of the fp32 rows x [R][N], nearest-even."""
     R, N = x.shape
     if out is None:
-        out = torch.empty((R, N), dtype=torch.int16, device=x.device)
+        out = _empty((R, N), torch.int16, x.device, stream)
     _check(load().tf_cast_bf16(_ptr(x), R, N, x.stride(0), _ptr(out), out.stride(0), _stream(stream)))
     return out
 
@@ -396,9 +411,9 @@ def keyed_sample(logits: torch.Tensor, temperature: float, top_k: int, top_p: fl
     lib = load()
     R, V = logits.shape
     if tokens is None:
-        tokens = torch.empty(R, dtype=torch.int32, device=logits.device)
+        tokens = _empty((R,), torch.int32, logits.device, stream)
     if ws is None:
-        ws = workspace(keyed_sample_workspace_bytes(R, V), logits.device)
+        ws = workspace(keyed_sample_workspace_bytes(R, V), logits.device, stream)
     sp = SamplingC(temperature, top_k, top_p)
     _check(lib.tf_keyed_sample(_ptr(logits), logits.stride(0), R, V, ctypes.byref(sp), ctypes.c_uint64(seed & (2**64 - 1)),
                                _ptr(pos), _ptr(tokens), _ptr(ws), ws.numel(), _stream(stream)))
@@ -421,13 +436,13 @@ def lmhead_sample(W: W4Matrix, x: torch.Tensor, temperature: float, top_k: int, 
     _check_rows_in(x, W.K)
     R = x.shape[0]
     if tokens is None:
-        tokens = torch.empty(R, dtype=torch.int32, device=x.device)
+        tokens = _empty((R,), torch.int32, x.device, stream)
     if tokens.dtype != torch.int32 or tokens.numel() < R or not tokens.is_contiguous():
         raise TFError(TF_ERR_INVALID_ARG, "tokens must be a contiguous int32 tensor of >= R entries")
     if logits is not None:
         _check_rows_out(logits, R, W.N, x.device)
     if ws is None:
-        ws = workspace(lmhead_sample_workspace_bytes(W, R), x.device)
+        ws = workspace(lmhead_sample_workspace_bytes(W, R), x.device, stream)
     wc = W.c()
     sp = SamplingC(temperature, top_k, top_p)
     _check(lib.tf_lmhead_sample(ctypes.byref(wc), _ptr(x), x.stride(0), R, ctypes.byref(sp),
@@ -446,8 +461,8 @@ def keyed_hash(seed: torch.Tensor, pos: torch.Tensor, token: torch.Tensor, strea
     for t, dt in ((seed, torch.int64), (pos, torch.int64), (token, torch.int32)):
         if t.dtype != dt or not t.is_contiguous():
             raise TFError(TF_ERR_INVALID_ARG, f"expected a contiguous {dt} tensor, got {t.dtype}")
-    h = torch.empty(n, dtype=torch.int64, device=seed.device)
-    g = torch.empty(n, dtype=torch.float64, device=seed.device)
+    h = _empty((n,), torch.int64, seed.device, stream)
+    g = _empty((n,), torch.float64, seed.device, stream)
     _check(load().tf_keyed_hash(_ptr(seed), _ptr(pos), _ptr(token), n, _ptr(h), _ptr(g), _stream(stream)))
     return h, g
 
@@ -458,9 +473,9 @@ def accept(drafts: torch.Tensor, sampled: torch.Tensor, accepted: torch.Tensor =
     R = sampled.shape[0]
     dev = sampled.device
     if accepted is None:
-        accepted = torch.empty(1, dtype=torch.int32, device=dev)
+        accepted = _empty((1,), torch.int32, dev, stream)
     if bonus is None:
-        bonus = torch.empty(1, dtype=torch.int32, device=dev)
+        bonus = _empty((1,), torch.int32, dev, stream)
     _check(lib.tf_accept(_ptr(drafts) if R > 1 else None, _ptr(sampled), R, _ptr(accepted), _ptr(bonus),
                          _stream(stream)))
     return accepted, bonus
@@ -483,8 +498,8 @@ def selfcheck_row_invariance(W: W4Matrix, x: torch.Tensor, stream=None) -> int:
     """0 if every row of every R in 1..16 matches its one-row launch bit for bit,
     else R * 256 + row of the first mismatch.  x: bf16 [16][K] on the device."""
     lib = load()
-    scratch = workspace(int(lib.tf_selfcheck_scratch_bytes(W.N)), device=x.device)
-    ws = workspace(lane_gemm_workspace_bytes(W.K, W.N, W.group), device=x.device)
+    scratch = workspace(int(lib.tf_selfcheck_scratch_bytes(W.N)), x.device, stream)
+    ws = workspace(lane_gemm_workspace_bytes(W.K, W.N, W.group), x.device, stream)
     res = I32(-1)
     _check(lib.tf_selfcheck_row_invariance(ctypes.byref(W.c()), _ptr(x), x.stride(0), _ptr(scratch), scratch.numel(),
                                            _ptr(ws), ws.numel(), _stream(stream), ctypes.byref(res)))
@@ -511,7 +526,7 @@ class KVCache:
                stream=None):
         """Entries at positions pos .. pos + R - 1 from k_new, v_new bf16 [R][n_kv*128]."""
         if ws is None:
-            ws = workspace(256, device=k_new.device)
+            ws = _status_block(k_new.device, stream)
         R = k_new.shape[0]
         _check(load().tf_kv_append(ctypes.byref(self._c), _ptr(k_new), _ptr(v_new), k_new.stride(0), R, _ptr(pos),
                                    _ptr(ws), ws.numel(), _stream(stream)))
@@ -526,9 +541,9 @@ class KVCache:
         R = q.shape[0]
         n_q = self.n_kv * group
         if out is None:
-            out = torch.empty((R, n_q * HEAD_DIM), dtype=torch.float32, device=q.device)
+            out = _empty((R, n_q * HEAD_DIM), torch.float32, q.device, stream)
         if ws is None:
-            ws = workspace(self.workspace_bytes(group, R), device=q.device)
+            ws = workspace(self.workspace_bytes(group, R), q.device, stream)
         _check(load().tf_attention_verify(ctypes.byref(self._c), group, _ptr(q), q.stride(0), R, _ptr(pos), _ptr(out),
                                           out.stride(0), _ptr(ws), ws.numel(), _stream(stream)))
         return out
@@ -672,9 +687,7 @@ class KVBatch:
             _refuse("k_new and v_new must have the same rows and row stride")
         R, at = self._rows(n), self._pos(pos)
         if ws is None:
-            ws = workspace(256, dev, stream)
-            if stream is not None:
-                ws.record_stream(torch.cuda.current_stream(dev))
+            ws = _status_block(dev, stream)
         st = load().tf_kv_store(self._c, k_new.data_ptr(), v_new.data_ptr(), ld, R, at, _ptr(ws), ws.numel(),
                                 _stream(stream))
         if st:
@@ -732,7 +745,7 @@ def rmsnorm_bf16(x: torch.Tensor, eps: float, out: torch.Tensor = None, stream=N
     """bf16 bits (int16 tensor) of x / sqrt(mean(x^2) + eps), per row of fp32 x [R][H]."""
     R, H = x.shape
     if out is None:
-        out = torch.empty((R, H), dtype=torch.int16, device=x.device)
+        out = _empty((R, H), torch.int16, x.device, stream)
     _check(load().tf_rmsnorm_bf16(_ptr(x), R, H, eps, _ptr(out), _stream(stream)))
     return out
 
@@ -759,9 +772,9 @@ def moe_w4(layer: MoeLayer, x: torch.Tensor, router: torch.Tensor, out: torch.Te
     lib = load()
     R = x.shape[0]
     if out is None:
-        out = torch.empty((R, layer.hidden), dtype=torch.float32, device=x.device)
+        out = _empty((R, layer.hidden), torch.float32, x.device, stream)
     if ws is None:
-        ws = workspace(moe_workspace_bytes(layer, R), x.device)
+        ws = workspace(moe_workspace_bytes(layer, R), x.device, stream)
     lc = layer.c()
     _check(lib.tf_moe_w4(ctypes.byref(lc), _ptr(x), _ptr(router), R, _ptr(out), _ptr(ws), ws.numel(),
                          _stream(stream)))
