@@ -1,0 +1,60 @@
+"""The edges of decode.BranchDecoder on the GPU: a model may have as many query heads
+per KV head as the attention takes.
+
+Tolerance of the logits: that of tests/test_gpu_branch_decoder.py, 2^-5 of the row's
+rms, for the same number of roundings per block.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import batch as obat
+from w4_gemm_keyed_gb300 import inputs
+
+pytestmark = pytest.mark.gpu
+
+V, H, F, G, ROT, THETA = 512, 256, 256, 64, 64, 1e4
+SAMPLING = (0.7, 20, 0.95)
+
+
+def weights_of(n_kv, group):
+    rng = inputs.rng_for(95, n_kv, group)
+    n_q, blocks, attn = n_kv * group, [], []
+    for _ in range(2):
+        (gc, gs), (uc, us), (dc, ds) = (inputs.w4_weights(rng, a, b, G) for a, b in ((H, F), (H, F), (F, H)))
+        blocks.append(dict(gate_codes=gc, gate_scales=gs, up_codes=uc, up_scales=us, down_codes=dc, down_scales=ds))
+        qc, qs = inputs.w4_weights(rng, H, (n_q + 2 * n_kv) * 128, G)
+        oc, os_ = inputs.w4_weights(rng, n_q * 128, H, G)
+        gains = inputs.bf16_bits_from_f32((1 + 0.2 * rng.normal(size=(2, 128))).astype(np.float32))
+        attn.append(dict(qkv_codes=qc, qkv_scales=qs, o_codes=oc, o_scales=os_, q_norm=gains[0], k_norm=gains[1]))
+    lc, ls = inputs.w4_weights(rng, H, V, G)
+    return dict(emb=inputs.bf16_normal(rng, (V, H), 0.5), blocks=blocks, attn=attn, lm_codes=lc, lm_scales=ls, group=G)
+
+
+# ---------------------------------------------------------------- head layouts
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n_kv,group", [(1, 16), (2, 11)])
+def test_many_query_heads_per_kv_head(tf, fmt, n_kv, group):
+    """Prompts longer than one pass of rows x group = 128 query vectors: the logits are
+    the oracle's, the replies those of each branch alone."""
+    from w4_gemm_keyed_gb300 import decode
+    weights = weights_of(n_kv, group)
+    m = decode.upload_branch_model(weights, n_kv, group, THETA, ROT)
+    rng = inputs.rng_for(96, group)
+    prompt = rng.integers(0, V, 45).tolist()
+    replies = [rng.integers(0, V, 3).tolist() for _ in range(2)]
+    dec = decode.BranchDecoder(m, 2, 256, 64, fmt)
+    dec.start(prompt)
+    dec.step(4, replies, *SAMPLING, [1, 2])
+    oracle_model = dict(weights, n_kv=n_kv, attn_group=group, adjacent=False, quantise=fmt == "e4m3",
+                        inv_freq=[THETA ** (-2 * d / ROT) for d in range(ROT // 2)])
+    for b, reply in enumerate(replies):
+        ref = obat.branch_logits(oracle_model, prompt + reply)[len(prompt) - 1:]
+        got = dec.logits[4 * b:4 * b + 4].double().cpu().numpy()
+        rms = np.sqrt(np.mean(ref ** 2, axis=1, keepdims=True))
+        worst = np.max(np.abs(got - ref) / rms)
+        assert worst <= 2.0 ** -5, worst
+    one = decode.BranchDecoder(m, 1, 256, 64, fmt)
+    alone = [decode.branch_decode(one, prompt, [12], 1, *SAMPLING, [s])[0] for s in (1234, 1235)]
+    assert decode.branch_decode(dec, prompt, [12, 12], 1, *SAMPLING, [1234, 1235]) == alone

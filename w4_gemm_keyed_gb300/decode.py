@@ -433,8 +433,9 @@ class BranchDecoder:
         toks = [int(t) for t in prompt]
         if not toks:
             raise ValueError("a prompt has at least one token")
-        for p in range(0, len(toks) - 1, tf.MAX_ROWS):
-            R = min(tf.MAX_ROWS, len(toks) - 1 - p)
+        rows = max(1, min(tf.MAX_ROWS, tf.MAX_QUERIES // self.model.group))     # no row's bits depend on it
+        for p in range(0, len(toks) - 1, rows):
+            R = min(rows, len(toks) - 1 - p)
             self.prompt_pos.fill_(p)
             chunk = torch.tensor(toks[p:p + R] + [0], dtype=torch.int32, device=self.x.device)
             self.model.base.embed_rows(chunk[:1], chunk[1:], R, self.x[:R], self.ws_status)

@@ -23,6 +23,7 @@ TF_DEV_OK, TF_DEV_TIMEOUT, TF_DEV_NONFINITE_LOGIT, TF_DEV_BAD_TOKEN, TF_DEV_BAD_
 HEAD_DIM = 128
 TF_OP_LANE_GEMM, TF_OP_KEYED_SAMPLE, TF_OP_ATTENTION = 1, 2, 3
 MAX_ROWS = 16
+MAX_QUERIES = 128       # rows x query heads per KV head of one sequence in KVBatch.attention
 MAX_TOP_K = 64
 KV_FORMATS = {"bf16": 0, "e4m3": 1}
 
