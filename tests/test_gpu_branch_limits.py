@@ -1,5 +1,6 @@
-"""The edges of decode.BranchDecoder on the GPU: a model may have as many query heads
-per KV head as the attention takes.
+"""The edges of decode.BranchDecoder on the GPU: a reply or a prompt past the capacity
+given at construction is refused, and a model may have as many query heads per KV head
+as the attention takes.
 
 Tolerance of the logits: that of tests/test_gpu_branch_decoder.py, 2^-5 of the row's
 rms, for the same number of roundings per block.
@@ -30,6 +31,57 @@ def weights_of(n_kv, group):
         attn.append(dict(qkv_codes=qc, qkv_scales=qs, o_codes=oc, o_scales=os_, q_norm=gains[0], k_norm=gains[1]))
     lc, ls = inputs.w4_weights(rng, H, V, G)
     return dict(emb=inputs.bf16_normal(rng, (V, H), 0.5), blocks=blocks, attn=attn, lm_codes=lc, lm_scales=ls, group=G)
+
+
+@pytest.fixture(scope="module")
+def model(tf):
+    from w4_gemm_keyed_gb300 import decode
+    return decode.upload_branch_model(weights_of(1, 2), 1, 2, THETA, ROT)
+
+
+def decoder(model, n_branch=2):
+    from w4_gemm_keyed_gb300 import decode
+    return decode.BranchDecoder(model, n_branch, 256, 200, max_rows=4)      # 256 own entries a branch
+
+
+# ---------------------------------------------------------------- capacity
+def test_a_pass_past_the_own_caches_is_refused(tf, model):
+    dec = decoder(model)
+    dec.start([1, 2, 3])
+    dec.at = [10, 252]
+    assert len(dec.step(4, [[4, 5, 6]] * 2, *SAMPLING, [1, 2])) == 2        # entries 252 .. 255: the last ones
+    dec.at = [10, 253]
+    with pytest.raises(ValueError):
+        dec.step(4, [[4, 5, 6]] * 2, *SAMPLING, [1, 2])
+    assert dec.at == [10, 253]
+    dec.finish(1)                                                           # a finished branch needs no room
+    assert dec.step(4, [[4, 5, 6]] * 2, *SAMPLING, [1, 2])[1] is None
+
+
+def test_a_reply_longer_than_its_cache_is_refused(tf, model):
+    from w4_gemm_keyed_gb300 import decode
+    dec = decoder(model)
+    with pytest.raises(ValueError):
+        decode.branch_decode(dec, [1, 2, 3], [5, 300], 1, *SAMPLING, [1, 2])
+    out = decode.branch_decode(dec, [1, 2, 3], [5, 256], 1, *SAMPLING, [1, 2])
+    assert [len(o) for o in out] == [5, 256]
+
+
+def test_a_prompt_longer_than_its_cache_is_refused(tf, model):
+    dec = decoder(model)
+    dec.start([7] * 257)            # 256 entries and the replies' first input
+    assert dec.prompt_len == 256
+    with pytest.raises(ValueError):
+        dec.start([7] * 258)
+    assert dec.prompt_len == 256
+
+
+def test_rows_outside_the_decoder_are_refused(tf, model):
+    dec = decoder(model)
+    dec.start([1])
+    for R in (0, 5):
+        with pytest.raises(ValueError):
+            dec.step(R, [[1] * 8] * 2, *SAMPLING, [1, 2])
 
 
 # ---------------------------------------------------------------- head layouts

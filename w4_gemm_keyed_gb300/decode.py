@@ -383,8 +383,9 @@ class BranchDecoder:
             return -(-k // 256) * 256
 
         self.model, self.n_branch, self.max_rows = model, n_branch, max_rows
-        self.shared = [tf.KVBatch(1, model.n_kv, up(max_prompt), fmt, device) for _ in model.qkv]
-        self.own = [tf.KVBatch(n_branch, model.n_kv, up(max_reply + max_rows), fmt, device) for _ in model.qkv]
+        self.max_prompt, self.max_own = up(max_prompt), up(max_reply + max_rows)    # entries the caches hold
+        self.shared = [tf.KVBatch(1, model.n_kv, self.max_prompt, fmt, device) for _ in model.qkv]
+        self.own = [tf.KVBatch(n_branch, model.n_kv, self.max_own, fmt, device) for _ in model.qkv]
         f32, b16 = dict(dtype=torch.float32, device=device), dict(dtype=torch.bfloat16, device=device)
         self.x, self.qkv, self.logits = (torch.zeros((n, c), **f32) for c in (b.hidden, W, b.vocab))
         self.n, self.qkv_b, self.att = (torch.zeros((n, c), **b16) for c in (b.hidden, W, A))
@@ -433,6 +434,8 @@ class BranchDecoder:
         toks = [int(t) for t in prompt]
         if not toks:
             raise ValueError("a prompt has at least one token")
+        if len(toks) - 1 > self.max_prompt:
+            raise ValueError(f"a prompt of {len(toks)} tokens: the shared caches hold {self.max_prompt} entries")
         rows = max(1, min(tf.MAX_ROWS, tf.MAX_QUERIES // self.model.group))     # no row's bits depend on it
         for p in range(0, len(toks) - 1, rows):
             R = min(rows, len(toks) - 1 - p)
@@ -450,6 +453,11 @@ class BranchDecoder:
     def step(self, R: int, drafts, temperature, top_k, top_p, seeds):
         """One verify pass of R rows per branch; ``drafts[b]`` holds branch b's R - 1
         proposals.  Returns per branch (a, tokens t[0..R-1]), or None where it idles."""
+        if not 1 <= R <= self.max_rows:
+            raise ValueError(f"R={R} outside [1, max_rows={self.max_rows}]")
+        for i, p in enumerate(self.at):     # past its cache the device would take the branch for idle
+            if p + R > self.max_own:
+                raise ValueError(f"branch {i}: {R} rows after {p} entries, its caches hold {self.max_own}")
         b, P, rows = self.model.base, self.prompt_len, self.n_branch * R
         self.pos.copy_(torch.tensor(self.at, dtype=torch.int64))
         first = torch.tensor([[P + p + 1 + r for r in range(R)] for p in self.at], dtype=torch.int64)
@@ -482,6 +490,9 @@ class BranchDecoder:
 def branch_decode(dec: BranchDecoder, prompt, n_tokens, R: int, temperature, top_k, top_p, seeds, draft_fn=None):
     """One reply of n_tokens[b] tokens per branch, R rows a pass; ``draft_fn(b, k, n)``
     gives branch b's drafts for its tokens k .. k + n - 1.  Returns the replies."""
+    longest = max(n_tokens)
+    if longest - 1 + R > dec.max_own:       # the last pass may start at its last token
+        raise ValueError(f"a reply of {longest} tokens in passes of {R} rows: the caches hold {dec.max_own} entries")
     dec.start(prompt)
     out = [[] for _ in range(dec.n_branch)]
     for b in range(dec.n_branch):
