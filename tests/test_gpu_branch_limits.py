@@ -1,6 +1,6 @@
 """The edges of decode.BranchDecoder on the GPU: a reply or a prompt past the capacity
-given at construction is refused, and a model may have as many query heads per KV head
-as the attention takes.
+given at construction is refused, what the device reports is raised, and a model may
+have as many query heads per KV head as the attention takes.
 
 Tolerance of the logits: that of tests/test_gpu_branch_decoder.py, 2^-5 of the row's
 rms, for the same number of roundings per block.
@@ -82,6 +82,70 @@ def test_rows_outside_the_decoder_are_refused(tf, model):
     for R in (0, 5):
         with pytest.raises(ValueError):
             dec.step(R, [[1] * 8] * 2, *SAMPLING, [1, 2])
+
+
+# ---------------------------------------------------------------- what the device reports
+def test_a_prompt_token_outside_the_vocabulary_is_refused(tf, model):
+    dec = decoder(model)
+    dec.start([1, 2, 3])
+    want = dec.step(1, [], *SAMPLING, [1, 2])
+    dec.start([1, 2, 3])
+    for bad in ([1, V, 3], [1, 2, V], [-1]):
+        with pytest.raises(ValueError):
+            dec.start(bad)
+    assert dec.step(1, [], *SAMPLING, [1, 2]) == want       # the prompt before is still there
+
+
+def test_a_draft_outside_the_vocabulary_is_only_rejected(tf, model):
+    dec = decoder(model)
+    dec.start([1, 2, 3])
+    want = dec.step(1, [], *SAMPLING, [1, 2])
+    for bad in (V, -1):
+        dec.start([1, 2, 3])
+        got = dec.step(2, [[bad], [bad]], *SAMPLING, [1, 2])
+        assert [(a, t[:1]) for a, t in got] == want
+
+
+def test_nonfinite_logits_are_raised_where_they_are_committed(tf, model):
+    dec = decoder(model)
+    dec.start([1, 2, 3])
+    want = dec.step(1, [], *SAMPLING, [1, 2])
+    spoilt = next(t for t in range(10, V) if all(t != w[1][0] for w in want))
+    kept = model.base.embedding[spoilt].clone()
+    try:
+        model.base.embedding[spoilt] = 0x7FC0           # NaN
+        dec.start([1, 2, 3])
+        got = dec.step(2, [[spoilt], [spoilt]], *SAMPLING, [1, 2])      # rejected: no harm done
+        assert [(a, t[:1]) for a, t in got] == want
+        dec.start([1, 2, spoilt])
+        with pytest.raises(tf.TFError):
+            dec.step(1, [], *SAMPLING, [1, 2])
+    finally:
+        model.base.embedding[spoilt] = kept
+    dec.start([1, 2, 3])
+    assert dec.step(1, [], *SAMPLING, [1, 2]) == want
+
+
+@pytest.mark.parametrize("name", ["ws_attn", "ws_gemm", "ws_block"])
+def test_a_reported_timeout_is_raised(tf, model, name):
+    dec = decoder(model)
+    dec.start([1, 2, 3])
+    want = dec.step(1, [], *SAMPLING, [1, 2])
+
+    def report():
+        getattr(dec, name)[:4].view(torch.int32).fill_(tf.TF_DEV_TIMEOUT)
+
+    dec.start([1, 2, 3])
+    report()
+    with pytest.raises(tf.TFError):
+        dec.step(1, [], *SAMPLING, [1, 2])
+    dec.start([1, 2, 3])                # the report was taken away with it
+    assert dec.step(1, [], *SAMPLING, [1, 2]) == want
+    report()
+    with pytest.raises(tf.TFError):
+        dec.start([1, 2, 3])
+    dec.start([1, 2, 3])
+    assert dec.step(1, [], *SAMPLING, [1, 2]) == want
 
 
 # ---------------------------------------------------------------- head layouts

@@ -370,7 +370,9 @@ class BranchDecoder:
     the accepted ones.  Every row's bits are those of its branch decoding alone,
     one row a pass, so neither drafts nor the other branches change its tokens.
     A finished branch idles until the next prompt.  ``fmt``: "bf16" or "e4m3"
-    cache entries.
+    cache entries.  A kernel that reports a timeout, and a committed row whose logits
+    are not finite, raise tf.TFError; the branches' state is then lost until the next
+    ``start``.
     """
 
     def __init__(self, model: BranchModel, n_branch: int, max_prompt: int, max_reply: int, fmt: str = "bf16",
@@ -429,6 +431,17 @@ class BranchDecoder:
                 tf.lane_gemm_w4_accumulate(m.o[i], self.att[c], self.x[c], ws=self.ws_gemm)
                 b.block(i, self.x[c], self.n_out, self.h_out, self.ws_block)
 
+    def _results(self, *values: torch.Tensor) -> list:
+        """The int32 values on the host, or TFError for what a kernel reported."""
+        watched = [w[:4].view(torch.int32) for w in (self.ws_gemm, self.ws_block, self.ws_attn) if w is not None]
+        got = torch.cat([*(v.reshape(-1) for v in values), *watched]).tolist()
+        status = max(got[-len(watched):])
+        if status:
+            for w in watched:
+                w.zero_()
+            raise tf.TFError(tf.TF_ERR_TIMEOUT, f"a kernel reported device status {status}")
+        return got[:-len(watched)]
+
     def start(self, prompt):
         """A new prompt (at least one token): its entries into the shared caches, all branches at its end."""
         toks = [int(t) for t in prompt]
@@ -436,6 +449,9 @@ class BranchDecoder:
             raise ValueError("a prompt has at least one token")
         if len(toks) - 1 > self.max_prompt:
             raise ValueError(f"a prompt of {len(toks)} tokens: the shared caches hold {self.max_prompt} entries")
+        if not all(0 <= t < self.model.base.vocab for t in toks):
+            raise ValueError(f"a prompt token is outside [0, {self.model.base.vocab})")
+        self.prompt_len, self.at = 0, [-1] * self.n_branch
         rows = max(1, min(tf.MAX_ROWS, tf.MAX_QUERIES // self.model.group))     # no row's bits depend on it
         for p in range(0, len(toks) - 1, rows):
             R = min(rows, len(toks) - 1 - p)
@@ -443,6 +459,7 @@ class BranchDecoder:
             chunk = torch.tensor(toks[p:p + R] + [0], dtype=torch.int32, device=self.x.device)
             self.model.base.embed_rows(chunk[:1], chunk[1:], R, self.x[:R], self.ws_status)
             self._rows(self.shared, self.prompt_pos, R, 0)
+        self._results()
         self.prompt_len = len(toks) - 1
         self.last.fill_(toks[-1])
         self.at = [0] * self.n_branch
@@ -481,7 +498,11 @@ class BranchDecoder:
             tf.keyed_sample(self.logits[i * R:(i + 1) * R], temperature, top_k, top_p, seeds[i],
                             pos=self.sample_pos[i, :R], tokens=self.tokens[i, :R], ws=self.ws_sample)
             tf.accept(self.drafts[i], self.tokens[i, :R], accepted=self.accepted[i:i + 1], bonus=self.last[i:i + 1])
-        got, t = self.accepted.tolist(), self.tokens[:, :R].tolist()
+        got = self._results(self.accepted, self.tokens[:, :R])
+        t = [got[self.n_branch + i * R:self.n_branch + (i + 1) * R] for i in range(self.n_branch)]
+        for i, p in enumerate(self.at):     # a row whose logits are not finite has token -1; rejected rows may
+            if p >= 0 and min(t[i][: got[i] + 1]) < 0:
+                raise tf.TFError(tf.TF_ERR_INVALID_ARG, f"branch {i}: logits of a committed row are not finite")
         out = [None if p < 0 else (got[i], t[i]) for i, p in enumerate(self.at)]
         self.at = [p if p < 0 else p + got[i] + 1 for i, p in enumerate(self.at)]
         return out
