@@ -174,3 +174,9 @@ def test_many_query_heads_per_kv_head(tf, fmt, n_kv, group):
     one = decode.BranchDecoder(m, 1, 256, 64, fmt)
     alone = [decode.branch_decode(one, prompt, [12], 1, *SAMPLING, [s])[0] for s in (1234, 1235)]
     assert decode.branch_decode(dec, prompt, [12, 12], 1, *SAMPLING, [1234, 1235]) == alone
+
+
+def test_drafted_rows_need_drafts(tf, model):
+    from w4_gemm_keyed_gb300 import decode
+    with pytest.raises(ValueError):
+        decode.branch_decode(decoder(model), [1, 2], [4, 4], 2, *SAMPLING, [1, 2])

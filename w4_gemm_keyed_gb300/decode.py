@@ -511,6 +511,8 @@ class BranchDecoder:
 def branch_decode(dec: BranchDecoder, prompt, n_tokens, R: int, temperature, top_k, top_p, seeds, draft_fn=None):
     """One reply of n_tokens[b] tokens per branch, R rows a pass; ``draft_fn(b, k, n)``
     gives branch b's drafts for its tokens k .. k + n - 1.  Returns the replies."""
+    if R > 1 and draft_fn is None:
+        raise ValueError("a drafted run needs a draft_fn")
     longest = max(n_tokens)
     if longest - 1 + R > dec.max_own:       # the last pass may start at its last token
         raise ValueError(f"a reply of {longest} tokens in passes of {R} rows: the caches hold {dec.max_own} entries")
