@@ -53,3 +53,16 @@ def test_own_buffers_on_another_stream(tf, fmt):
         assert tf.workspace_status(ws, stream=side) == tf.TF_DEV_OK
         del got, again
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_load_into_one_given_strided_buffer(tf, fmt):
+    c = tf.KVBatch(2, 2, 256, fmt)
+    pos = dev_pos([3, 100])
+    c.store(rows(1, 10, 2 * D), rows(2, 10, 2 * D), pos)
+    want_k, want_v = c.load(pos, 5)
+    for name in ("k", "v"):
+        wide = torch.zeros((10, 3 * D), dtype=torch.bfloat16, device="cuda")
+        k, v = c.load(pos, 5, **{name: wide[:, :2 * D]})
+        assert (k if name == "k" else v).data_ptr() == wide.data_ptr()
+        assert torch.equal(k, want_k) and torch.equal(v, want_v) and not wide[:, 2 * D:].any()

@@ -705,10 +705,12 @@ class KVBatch:
         if k is None and v is None:
             k, v, ld = *(_empty((n, cols), torch.bfloat16, dev, stream) for _ in range(2)), cols
         else:
-            k = _empty(v.shape, v.dtype, dev, stream) if k is None else k
-            v = _empty(k.shape, k.dtype, dev, stream) if v is None else v
-            ld = _bits16(k, "k", n, cols, dev)
-            if _bits16(v, "v", n, cols, dev) != ld:
+            ld = _bits16(v if k is None else k, "v" if k is None else "k", n, cols, dev)
+            if k is None:
+                k = _empty((v.shape[0], ld), v.dtype, dev, stream)[:, :v.shape[1]]
+            elif v is None:
+                v = _empty((k.shape[0], ld), k.dtype, dev, stream)[:, :k.shape[1]]
+            elif _bits16(v, "v", n, cols, dev) != ld:
                 _refuse("k and v must have the same row stride")
         if ws is None:
             ws = workspace(256, dev, stream)
