@@ -576,6 +576,12 @@ def _positions(pos: torch.Tensor, device) -> int:
     return pos.numel()
 
 
+def _bytes(ws: torch.Tensor, device) -> int:
+    if ws.device != device:
+        _refuse(f"ws must be on {device}, got one on {ws.device}")
+    return ws.numel()
+
+
 def rope_turns(rot_dim: int, theta: float = 10000.0, inv_freq=None, device="cuda") -> torch.Tensor:
     """Frequencies of a rotation over rot_dim elements for qk_norm_rope: int64 bits of
     round(2^64 f / 2 pi) per pair, f = theta^(-2d/rot_dim) radians per position, or
@@ -689,7 +695,7 @@ class KVBatch:
         R, at = self._rows(n), self._pos(pos)
         if ws is None:
             ws = _status_block(dev, stream)
-        st = load().tf_kv_store(self._c, k_new.data_ptr(), v_new.data_ptr(), ld, R, at, _ptr(ws), ws.numel(),
+        st = load().tf_kv_store(self._c, k_new.data_ptr(), v_new.data_ptr(), ld, R, at, _ptr(ws), _bytes(ws, dev),
                                 _stream(stream))
         if st:
             _check(st)
@@ -714,7 +720,8 @@ class KVBatch:
                 _refuse("k and v must have the same row stride")
         if ws is None:
             ws = workspace(256, dev, stream)
-        st = load().tf_kv_load(self._c, at, R, k.data_ptr(), v.data_ptr(), ld, _ptr(ws), ws.numel(), _stream(stream))
+        st = load().tf_kv_load(self._c, at, R, k.data_ptr(), v.data_ptr(), ld, _ptr(ws), _bytes(ws, dev),
+                               _stream(stream))
         if st:
             _check(st)
         return k, v
@@ -730,6 +737,8 @@ class KVBatch:
         cols, dev, n = self.n_kv * group * HEAD_DIM, self.device, q.shape[0]
         ldq = _bits16(q, "q", 1, cols, dev)
         R, at = self._rows(n), self._pos(pos)
+        if prefix is not None and prefix.device != dev:
+            _refuse(f"prefix must be on {dev}, got one on {prefix.device}")
         if out is None:
             out, ldo = _empty((n, cols), torch.bfloat16, dev, stream), cols
         else:
@@ -737,7 +746,7 @@ class KVBatch:
         if ws is None:
             ws = workspace(self.attention_workspace_bytes(group, R, prefix_len), dev, stream)
         st = load().tf_attention_batch(self._c, prefix._c if prefix is not None else None, prefix_len, group,
-                                       q.data_ptr(), ldq, R, at, out.data_ptr(), ldo, _ptr(ws), ws.numel(),
+                                       q.data_ptr(), ldq, R, at, out.data_ptr(), ldo, _ptr(ws), _bytes(ws, dev),
                                        _stream(stream))
         if st:
             _check(st)
