@@ -1,6 +1,6 @@
-"""What the batch-decoding calls are given on another device than the cache is refused
-before the library sees it (no GPU needed: the library is stood in for, the cache is on
-the CPU, the other device is "meta")."""
+"""What the batch-decoding calls are given on another device than the cache, or of the
+wrong rank or count, is refused before the library sees it (no GPU needed: the library
+is stood in for, the cache is on the CPU, the other device is "meta")."""
 
 import types
 
@@ -46,3 +46,19 @@ def test_another_device_is_refused(cache, name):
     with pytest.raises(tf.TFError) as e:
         CASES[name](cache)
     assert e.value.status == tf.TF_ERR_INVALID_ARG
+
+
+SCALAR = torch.tensor(1.0, dtype=torch.bfloat16)
+MALFORMED = dict(
+    store_scalar=lambda c: c.store(SCALAR, SCALAR, POS),
+    attention_scalar=lambda c: c.attention(SCALAR, 1, POS),
+    attention_group=lambda c: c.attention(bf16(), -1, POS),
+    store_to_none=lambda c: tf.KVBatch(0, 2, 256, device="cpu").store(bf16(), bf16(), POS),
+    attention_of_none=lambda c: tf.KVBatch(0, 2, 256, device="cpu").attention(bf16(), 1, POS),
+)
+
+
+@pytest.mark.parametrize("name", MALFORMED)
+def test_malformed_arguments_are_refused_as_others_are(cache, name):
+    with pytest.raises(tf.TFError):
+        MALFORMED[name](cache)

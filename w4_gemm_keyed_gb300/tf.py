@@ -676,7 +676,7 @@ class KVBatch:
         return b
 
     def _rows(self, n: int) -> int:
-        if n % self.n_seq or not n:
+        if not n or not self.n_seq or n % self.n_seq:
             _refuse(f"{n} rows are not a positive multiple of {self.n_seq} sequences")
         return n // self.n_seq
 
@@ -688,8 +688,9 @@ class KVBatch:
     def store(self, k_new: torch.Tensor, v_new: torch.Tensor, pos: torch.Tensor, ws: torch.Tensor = None, stream=None):
         """Entries pos[b] + r of sequence b from rows b*R + r of k_new, v_new (bf16
         [n_seq*R][n_kv*128]); returns the workspace whose status the call sets."""
-        n, cols, dev = k_new.shape[0], self.n_kv * HEAD_DIM, self.device
+        cols, dev = self.n_kv * HEAD_DIM, self.device
         ld = _bits16(k_new, "k_new", 1, cols, dev)
+        n = k_new.shape[0]
         if _bits16(v_new, "v_new", 1, cols, dev) != ld or v_new.shape[0] != n:
             _refuse("k_new and v_new must have the same rows and row stride")
         R, at = self._rows(n), self._pos(pos)
@@ -734,8 +735,11 @@ class KVBatch:
         """bf16 [n_seq*R][n_kv*group*128]: rows at own positions pos[b] + r attending over
         entries 0..prefix_len-1 of the one-sequence batch `prefix` and 0..pos[b]+r of
         their own; idle sequences' rows are zeros."""
-        cols, dev, n = self.n_kv * group * HEAD_DIM, self.device, q.shape[0]
+        if group < 1:
+            raise TFError(TF_ERR_UNSUPPORTED, f"group={group} outside [1, 16]")
+        cols, dev = self.n_kv * group * HEAD_DIM, self.device
         ldq = _bits16(q, "q", 1, cols, dev)
+        n = q.shape[0]
         R, at = self._rows(n), self._pos(pos)
         if prefix is not None and prefix.device != dev:
             _refuse(f"prefix must be on {dev}, got one on {prefix.device}")
