@@ -710,7 +710,8 @@ class KVBatch:
         if not 0 < R <= self.max_len:
             _refuse(f"R={R} outside [1, max_len={self.max_len}]")
         if k is None and v is None:
-            k, v, ld = *(_empty((n, cols), torch.bfloat16, dev, stream) for _ in range(2)), cols
+            k, ld = _empty((n, cols), torch.bfloat16, dev, stream), cols
+            v = _empty((n, cols), torch.bfloat16, dev, stream)
         else:
             ld = _bits16(v if k is None else k, "v" if k is None else "k", n, cols, dev)
             if k is None:
