@@ -556,9 +556,12 @@ TF_API tf_status tf_attention_verify(const tf_kv_cache *c, int32_t group, const 
  *   format; may be NULL when prefix_len = 0) and entries 0..pos[b]+r of its own
  *   cache, the pass's own rows already stored:
  *     s_t = q . k_t / sqrt(128),  out = sum_t exp(s_t - max s) v_t / sum_t exp(s_t - max s).
- *   The prefix is read once for the whole batch.  Entries no row attends over
- *   may hold anything, infinities and NaN included.  n_seq in 1..1024.  ws:
- *   tf_attention_batch_workspace_bytes of scratch (0: unsupported arguments).
+ *   The softmax weights are rounded to bf16 for the product with v (fp32 in
+ *   their sum; tf_attention_verify keeps about 16 bits of them).  The prefix is
+ *   read once for the whole batch.  Entries no row attends over may hold
+ *   anything, infinities and NaN included.  n_seq in 1..1024.  ws:
+ *   tf_attention_batch_workspace_bytes of scratch (0: unsupported arguments),
+ *   which follows max_len, n_seq and prefix_len, whatever the positions are.
  */
 #define TF_KV_BF16 0
 #define TF_KV_E4M3 1

@@ -20,16 +20,18 @@
 // both operands in shared memory and S in tensor memory, then P (bf16, in place
 // of S) times V with P read from tensor memory.  A tile of 128 vectors is filled
 // by rows x group; with few of them the rest are idle, and a 128-key tile still
-// takes an SM about 2,000 cycles where all SMs together get one from HBM in
+// takes an SM about 2,000 cycles where HBM delivers one (K and V) to each SM in
 // 2,800, so few rows need no form of their own.
 //
-// What bounds it (GB300, us measured): many rows, the tensor cores and the
-// hand-over between them and the softmax: a step of two tiles and 128 keys takes
-// about 2,700 cycles where its products take 2,080 (512 rows x 64 heads over 32768
-// entries 420 us, 1.29 PFLOP/s; of that the steps about 300, passing from item to item 42,
-// joining about 47).  Few rows, HBM: 12 rows x 20 heads over 130001 entries 51 us, 5.2
-// TB/s.  E4M3 caches with many rows, the issue slots that expansion shares with
-// the softmax: 240 rows x 64 heads over 20000 entries 208 us.
+// What bounds it (GB300, measured call after call on the same inputs): many rows, the
+// tensor cores and the hand-over between them and the softmax: a step of two tiles and
+// 128 keys takes about 2,700 cycles where its products take 2,080 (512 rows x 64 heads over
+// 32768 entries 424 us, 1.29 PFLOP/s; 444 to 448 with other inputs each call; of that the
+// steps about 300, passing from item to item 42, joining about 47).  Few rows, HBM: 12 rows
+// x 20 heads over 130001 entries 51 us, 5.2 TB/s.  E4M3 caches with many rows, the chain
+// of hand-overs that expanding each tile makes longer, with no unit near its limit (issue
+// 45 %, ALU 34 %, tensor 33 %, shared memory 19 %): 240 rows x 64 heads over 20000
+// entries 212 us, 169 as a bf16 cache.
 #include <atomic>
 
 #include <cuda.h>
@@ -65,15 +67,14 @@ constexpr int kExpandWarp = 12, kExpandWarps = 8;
 template <bool E4M3>
 struct Form {
     static constexpr int stages = E4M3 ? 3 : 5;         // bf16 K and V tiles in shared memory
-    // E4M3 tiles on their way (3 + 3: 213 us and 71.9 us at 240 rows over 20000 entries and
-    // 12 rows over 130001; 4 + 2: 214.6 and 73.5, 3 + 4 as 3 + 3)
+    // E4M3 tiles on their way (4 expanded + 2 raw: 0.7 % slower at 240 rows over 20000 entries,
+    // 2 % at 12 rows over 130001; 3 + 4 as 3 + 3)
     static constexpr int raw = E4M3 ? 3 : 0;
     static constexpr int threads = E4M3 ? 640 : 384;
     static constexpr int readers = kSoftmaxWarps + 1 + (E4M3 ? kExpandWarps : 0);  // of the item ring
     // registers a thread: the softmax warps' and the others', together no more
-    // than the launch's share (96 a thread of 640, 168 of 384).  With 144 and 64, 208
-    // and 88, 240 rows (E4M3) and 512 rows (bf16) took 212 and 432 us; with these 211
-    // and 428.
+    // than the launch's share (96 a thread of 640, 168 of 384).  With 144 and 64 (240 E4M3
+    // rows), 208 and 88 (512 bf16 rows): 0.5 % and 1 % slower.
     static constexpr int regs_softmax = E4M3 ? 168 : 216, regs_other = E4M3 ? 48 : 72;
     static_assert(256 * regs_softmax + (threads - 256) * regs_other <= threads * (E4M3 ? 96 : 168), "register split");
 };
@@ -107,8 +108,8 @@ __host__ __device__ inline int prefix_part(int prefix_len, int n_kv) {
     // Parts that make about kItems items where the batch is a single tile, none
     // shorter than kMinPrefixPart.  Few rows want many parts (each SM streams one),
     // many rows few (each is stored and joined per vector).  12 rows over 130001
-    // entries / 512 rows over 32768, 4 and 8 heads: 152 items 57 / 546 us, 100
-    // items 56 / 522 us, 76 items 67 / 512 us.
+    // entries / 512 rows over 32768, 4 and 8 heads, against 100 items with kernels slower
+    // than these: 152 items 2 % / 5 % slower, 76 items 20 % slower / 2 % faster.
     constexpr int kItems = 100;
     const long long even = ((long long)prefix_len * n_kv + kItems - 1) / kItems;
     const long long part = (even + kTile - 1) / kTile * kTile;
@@ -453,7 +454,7 @@ __device__ __forceinline__ void mend_values(uint8_t *v, int first_hidden, int va
 
 // The whole warp follows the items; the elected lane waits, issues and commits, so
 // that nothing but those is on the products' path (with every lane in every wait
-// and a predicate on each product, 512 rows over 32768 entries took 499 us).
+// and a predicate on each product, the call took 8 % longer at 512 rows over 32768 entries).
 template <bool E4M3>
 __device__ void multiply(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint8_t *stages, uint32_t tmem) {
     constexpr int kStages = Form<E4M3>::stages;
@@ -667,8 +668,8 @@ __device__ void softmax(const KernelArgs &k, Shared *sh, uint32_t tmem) {
                 const uint32_t t_s = tmem + kTmemS + buf * kTile + my_lanes;
                 const int last = lim - i * kTile;
                 const bool part_seen = __any_sync(0xFFFFFFFFu, last < kTile - 1);
-                // bf16 caches: all scores in registers (512 rows over 32768 entries: 428 us; with
-                // the upper half read again for its weights, as below, 449).  The softmax of
+                // bf16 caches: all scores in registers (512 rows over 32768 entries: 5 % slower with
+                // the upper half read again for its weights, as below).  The softmax of
                 // E4M3 caches has fewer: 64 scores at a time, the upper half for its maximum
                 // first, and once more after the lower half's weights have been stored; its
                 // loops stay rolled, as instructions are fetched anew for every role between.
@@ -892,8 +893,8 @@ __global__ void __launch_bounds__(Form<E4M3>::threads, 1) attn_batch_kernel(cons
 // parts fixes.  Where there are many vectors, 520 bytes per vector and part from HBM
 // or L2 and the instructions that find them bound it (with a quad a thread and 64-bit
 // products for every part's place, 512 rows x 64 heads x 14 parts took 74 us, with
-// two quads 55; CTAs of four quads, 256 threads, made the whole call 424 us, these
-// 416); where there are few, the chain of three loads does.
+// two quads 55; CTAs of four quads, 256 threads, made the whole call 2 % slower than
+// these); where there are few, the chain of three loads does.
 constexpr int kJoinRuns = 4, kJoinUnroll = 4, kJoinThreads = 32 * kJoinRuns;
 
 __global__ void __launch_bounds__(kJoinThreads, 6) attn_batch_join_kernel(AttnBatchArgs a, Plan p, const float *opart,

@@ -668,7 +668,9 @@ class KVBatch:
 
     @classmethod
     def of(cls, cache: KVCache) -> "KVBatch":
-        """A batch of one sequence over the memory of an existing KVCache."""
+        """A batch of one sequence over the memory of an existing KVCache.  Its attention
+        returns bf16 and rounds the softmax weights to bf16; KVCache.attention returns fp32
+        and keeps about 16 bits of them."""
         b = cls.__new__(cls)
         b.k, b.v, b.k_scale, b.v_scale = cache.k[None], cache.v[None], None, None
         b.n_seq, b.n_kv, b.max_len, b.fmt = 1, cache.n_kv, cache.max_len, "bf16"
