@@ -28,8 +28,9 @@
  *   need zeroed when they finish, so a workspace can be reused by later calls
  *   of the same entry point for the same matrix, layer, model or cache on the
  *   same stream without clearing it again).  The lane GEMMs, tf_decoder_block,
- *   tf_embed_rows, tf_kv_append, tf_kv_store, tf_kv_load and tf_attention_batch
- *   may use one workspace in turn, for any matrices and caches, and tf_attention_batch
+ *   tf_embed_rows, tf_kv_append, tf_kv_store, tf_kv_load, tf_kv_keep, tf_tree_accept,
+ *   tf_attention_batch, tf_attention_tree and tf_attention_prompt
+ *   may use one workspace in turn, for any matrices and caches, and the last three
  *   any that was zero-filled once; otherwise a workspace is cleared before
  *   another entry point uses it.  Its first 256 bytes hold no operator's
  *   scratch.  Calls that overlap in time must not share a workspace.
@@ -77,6 +78,7 @@ typedef enum tf_status {
 #define TF_DEV_NONFINITE_LOGIT 2  /* a logit was NaN or +-inf (its row's token is -1) */
 #define TF_DEV_BAD_TOKEN 3        /* a token id outside [0, vocab) reached the embedding */
 #define TF_DEV_BAD_POSITION 4     /* a KV-cache call saw *pos < 0 or *pos + R > max_len (nothing written) */
+#define TF_DEV_BAD_TREE 5         /* parents or a path that no tree has (its sequence is treated as idle) */
 
 /* Thread-local description of the last host-side error ("" when none). */
 TF_API const char *tf_last_error(void);
@@ -591,6 +593,88 @@ TF_API size_t tf_attention_batch_workspace_bytes(const tf_kv_batch *own, int32_t
 TF_API tf_status tf_attention_batch(const tf_kv_batch *own, const tf_kv_batch *prefix, int32_t prefix_len,
                                     int32_t group, const uint16_t *q, int32_t ldq, int32_t R, const int64_t *pos,
                                     uint16_t *out, int32_t ldo, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Whole prompts.
+ *
+ * The method reads a prompt before it drafts (README, the decode tables); fed
+ * 16 rows a pass, a prompt's entries are read again for every pass.  This call
+ * attends over whole prompts at once, several packed one after the other.
+ * ------------------------------------------------------------------------
+ * tf_attention_prompt: sequence s holds rows starts[s] .. starts[s + 1] - 1 (starts:
+ *   dev int64 [n_seq + 1], read on the device; n_seq in 1..1024; a sequence may
+ *   be empty), and row i of it attends over its rows 0 .. i:
+ *     s_t = q . k_t / sqrt(128),  out = sum_t e^(s_t - max s) v_t / sum_t e^(s_t - max s).
+ *   q: dev bf16 [rows][ldq], query head h at columns h*128, reading KV head
+ *   h / group (group in 1..16, n_kv in 1..128); k, v: dev bf16 [rows][ldk], [rows][ldv],
+ *   KV head j at columns j*128; out: dev bf16 [rows][ldo], rounded once.  Each ld a
+ *   multiple of 8, each pointer 16-B aligned; the three inputs may be columns of one
+ *   array (what tf_qk_norm_rope leaves); out overlaps none of them.  Rows before
+ *   starts[0] and from starts[n_seq] on are not written, and may hold anything.  Starts that
+ *   fall, or lie outside [0, rows], record TF_DEV_BAD_POSITION and nothing is
+ *   written.  The softmax weights are rounded to bf16 for the product with v
+ *   (fp32 in their sum).  A row's bits depend on its query, its place in
+ *   its sequence and rows 0 .. i of the sequence alone: not on other rows (infinities
+ *   and NaN in them included), other sequences, or where the sequence lies.
+ *   rows = 0 does nothing.  ws: >= 256 B.
+ */
+TF_API tf_status tf_attention_prompt(const uint16_t *q, int32_t ldq, const uint16_t *k, int32_t ldk,
+                                     const uint16_t *v, int32_t ldv, int32_t rows, int32_t n_kv, int32_t group,
+                                     const int64_t *starts, int32_t n_seq, uint16_t *out, int32_t ldo, void *ws,
+                                     size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Trees of drafted tokens.
+ *
+ * A pass may verify a tree of drafts instead of a chain: several continuations
+ * of one token, of which at most one survives.  The guarantee is the chain's
+ * (README, the two guarantees): a node's bits are those of decoding its path one
+ * token a pass, so the tree changes the speed and never a token.
+ *
+ * A tree has n rows, n in 1..TF_MAX_NODES, per sequence; node i of sequence b is row
+ * b * n + i.  parents: dev int32 [n_seq][n]: parents[b][0] = -1 (node 0, the
+ * root, is the last committed token), parents[b][i] a node before i, or -1
+ * for an unused row, which is no node's parent.  A path, root included, has at most
+ * TF_MAX_PATH nodes.  pos[b] is the root's position in the sequence's own cache
+ * (-1: idle): node i's entry is stored at pos[b] + i (tf_kv_store with R = n), but the node
+ * stands at position pos[b] + depth(i) (for tf_qk_norm_rope and tf_keyed_sample).
+ * Parents that are no tree record TF_DEV_BAD_TREE, and the sequence is treated
+ * as idle.
+ * ------------------------------------------------------------------------
+ * tf_attention_tree: as tf_attention_batch, with row i of sequence b attending over the prefix's
+ *   entries, own entries 0 .. pos[b] - 1 and the entries of its path's nodes, itself
+ *   included.  n rows per sequence (pos[b] + n <= max_len, n * group may exceed 128).
+ *   Rows of idle sequences and unused rows are zeros.  A node's bits depend on its query,
+ *   its position pos[b] + depth, prefix_len and the entries it sees, in path order: the same
+ *   whether an entry is a node of this pass or was committed before.  ws:
+ *   tf_attention_tree_workspace_bytes (0: unsupported arguments).
+ * tf_tree_accept: from the root, the walk goes to the lowest-numbered child whose
+ *   token (tokens: dev int32 [n_seq][n], a node's drafted token; the root's is not
+ *   read) is the one sampled at the walk's last node (sampled: dev int32 [n_seq][n]: what
+ *   decoding samples after each node).  accepted[b]: drafts accepted, i.e. steps of the walk;
+ *   bonus[b]: the token sampled at its last node; path[b][d], committed[b][d] (dev
+ *   int32 [n_seq][TF_MAX_PATH]): its node at depth d and the token sampled there, -1 past its end.
+ *   pos: dev int64 [n_seq]; idle sequences get accepted, bonus, path and committed
+ *   of -1.  ws: >= 256 B.
+ * tf_kv_keep: entry pos[b] + path[b][d] of sequence b becomes its entry pos[b] + d,
+ *   for every depth of the path (as tf_tree_accept leaves it: rising from
+ *   node 0, -1 past its end), as stored, in either format.  Entries past
+ *   the path's keep what they held.  A path that does not rise from node 0 records TF_DEV_BAD_TREE, one past
+ *   max_len TF_DEV_BAD_POSITION; nothing of its sequence is moved.  ws: >= 256 B.
+ */
+#define TF_MAX_NODES 64
+#define TF_MAX_PATH 16
+
+TF_API size_t tf_attention_tree_workspace_bytes(const tf_kv_batch *own, int32_t group, int32_t n, int32_t prefix_len);
+TF_API tf_status tf_attention_tree(const tf_kv_batch *own, const tf_kv_batch *prefix, int32_t prefix_len,
+                                   int32_t group, const uint16_t *q, int32_t ldq, int32_t n, const int64_t *pos,
+                                   const int32_t *parents, uint16_t *out, int32_t ldo, void *ws, size_t ws_bytes,
+                                   void *stream);
+TF_API tf_status tf_tree_accept(const int32_t *parents, const int32_t *tokens, const int32_t *sampled,
+                                const int64_t *pos, int32_t n_seq, int32_t n, int32_t *accepted, int32_t *bonus,
+                                int32_t *path, int32_t *committed, void *ws, size_t ws_bytes, void *stream);
+TF_API tf_status tf_kv_keep(const tf_kv_batch *c, const int64_t *pos, const int32_t *path, void *ws,
+                            size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
  * Pieces of the synthetic decoder (the steps tf_verify_step chains), public so

@@ -1,7 +1,7 @@
 // extern "C" entry points of libtf: argument validation, workspace layout and
 // launch sequencing.  Every step of the verify pass runs in this library's own
 // kernels (w4_gemm.cu, sampler.cu, glue.cu, attention.cu, kv_batch.cu,
-// attn_batch.cu); nothing here computes
+// attn_batch.cu, attn_prompt.cu, tree.cu); nothing here computes
 // on the host.
 #include <cmath>
 #include <cstdarg>
@@ -11,8 +11,10 @@
 #include "../../include/tf.h"
 #include "attention.cuh"
 #include "attn_batch.cuh"
+#include "attn_prompt.cuh"
 #include "glue.cuh"
 #include "sampler.cuh"
+#include "tree.cuh"
 #include "w4_gemm.cuh"
 
 using namespace tfk;
@@ -866,6 +868,31 @@ bool attn_batch_supported(const tf_kv_batch *own, int32_t group, int32_t R, int3
            prefix_len >= 0;
 }
 
+// prefix, queries, positions and output of tf_attention_batch and tf_attention_tree
+tf_status check_attention(const tf_kv_batch *own, const tf_kv_batch *prefix, int32_t prefix_len, int32_t group,
+                          const uint16_t *q, int32_t ldq, const int64_t *pos, const uint16_t *out, int32_t ldo) {
+    tf_status st = TF_OK;
+    if (prefix_len < 0) return fail(TF_ERR_INVALID_ARG, "prefix_len=%d must be >= 0", prefix_len);
+    if (prefix_len > 0) {
+        if ((st = check_batch(prefix, "prefix")) != TF_OK) return st;
+        if (prefix->n_seq != 1 || prefix->n_kv != own->n_kv || prefix->format != own->format)
+            return fail(TF_ERR_INVALID_ARG, "prefix must be one sequence with own's n_kv and format");
+        if (prefix_len > prefix->max_len)
+            return fail(TF_ERR_INVALID_ARG, "prefix_len=%d exceeds the prefix's max_len=%d", prefix_len, prefix->max_len);
+    }
+    const int n_q = own->n_kv * group;
+    if (!q || !pos || !out || !aligned(pos, 8)) return fail(TF_ERR_INVALID_ARG, "null or misaligned q, pos or out");
+    if (!aligned(q, 16) || ldq < n_q * kHeadDim || ldq % 8)
+        return fail(TF_ERR_INVALID_ARG, "q must be 16-B aligned with ldq a multiple of 8 and >= %d", n_q * kHeadDim);
+    if (!aligned(out, 16) || ldo < n_q * kHeadDim || ldo % 8)
+        return fail(TF_ERR_INVALID_ARG, "out must be 16-B aligned with ldo a multiple of 8 and >= %d", n_q * kHeadDim);
+    return TF_OK;
+}
+
+bool attn_tree_supported(const tf_kv_batch *own, int32_t group, int32_t n, int32_t prefix_len) {
+    return group >= 1 && group <= 16 && n >= 1 && n <= TF_MAX_NODES && n <= own->max_len && prefix_len >= 0;
+}
+
 }  // namespace
 
 tf_status tf_qk_norm_rope(const void *x, int32_t x_fp32, int32_t ldx, int32_t n_seq, int32_t R, int32_t n_q,
@@ -955,20 +982,7 @@ tf_status tf_attention_batch(const tf_kv_batch *own, const tf_kv_batch *prefix, 
     if (group < 1 || group > 16) return fail(TF_ERR_UNSUPPORTED, "group=%d outside [1, 16]", group);
     if (R < 1 || R > TF_MAX_ROWS) return fail(TF_ERR_INVALID_ARG, "R=%d outside [1, %d]", R, TF_MAX_ROWS);
     if (R * group > 128) return fail(TF_ERR_UNSUPPORTED, "R=%d x group=%d exceeds 128", R, group);
-    if (prefix_len < 0) return fail(TF_ERR_INVALID_ARG, "prefix_len=%d must be >= 0", prefix_len);
-    if (prefix_len > 0) {
-        if ((st = check_batch(prefix, "prefix")) != TF_OK) return st;
-        if (prefix->n_seq != 1 || prefix->n_kv != own->n_kv || prefix->format != own->format)
-            return fail(TF_ERR_INVALID_ARG, "prefix must be one sequence with own's n_kv and format");
-        if (prefix_len > prefix->max_len)
-            return fail(TF_ERR_INVALID_ARG, "prefix_len=%d exceeds the prefix's max_len=%d", prefix_len, prefix->max_len);
-    }
-    const int n_q = own->n_kv * group;
-    if (!q || !pos || !out || !aligned(pos, 8)) return fail(TF_ERR_INVALID_ARG, "null or misaligned q, pos or out");
-    if (!aligned(q, 16) || ldq < n_q * kHeadDim || ldq % 8)
-        return fail(TF_ERR_INVALID_ARG, "q must be 16-B aligned with ldq a multiple of 8 and >= %d", n_q * kHeadDim);
-    if (!aligned(out, 16) || ldo < n_q * kHeadDim || ldo % 8)
-        return fail(TF_ERR_INVALID_ARG, "out must be 16-B aligned with ldo a multiple of 8 and >= %d", n_q * kHeadDim);
+    if ((st = check_attention(own, prefix, prefix_len, group, q, ldq, pos, out, ldo)) != TF_OK) return st;
     if ((st = check_ws(ws, ws_bytes, tf_attention_batch_workspace_bytes(own, group, R, prefix_len))) != TF_OK) return st;
     AttnBatchArgs a{};
     a.own = kv_batch(*own);
@@ -986,6 +1000,123 @@ tf_status tf_attention_batch(const tf_kv_batch *own, const tf_kv_batch *prefix, 
     const char *why = "";
     cudaError_t e = launch_attn_batch(a, static_cast<cudaStream_t>(stream), &why);
     if (e != cudaSuccess) return fail(TF_ERR_CUDA, "tf_attention_batch: %s %s", cudaGetErrorString(e), why);
+    return ok();
+}
+
+size_t tf_attention_tree_workspace_bytes(const tf_kv_batch *own, int32_t group, int32_t n, int32_t prefix_len) {
+    if (!own || own->n_seq < 1 || own->n_seq > TF_MAX_SEQS || own->n_kv < 1 || own->n_kv > 128 || own->max_len <= 0 ||
+        own->max_len % kKvPart || !attn_tree_supported(own, group, n, prefix_len))
+        return 0;
+    return attn_tree_bytes(kv_batch(*own), prefix_len, group, n);
+}
+
+tf_status tf_attention_tree(const tf_kv_batch *own, const tf_kv_batch *prefix, int32_t prefix_len, int32_t group,
+                            const uint16_t *q, int32_t ldq, int32_t n, const int64_t *pos, const int32_t *parents,
+                            uint16_t *out, int32_t ldo, void *ws, size_t ws_bytes, void *stream) {
+    tf_status st = check_batch(own, "own");
+    if (st != TF_OK) return st;
+    if (group < 1 || group > 16) return fail(TF_ERR_UNSUPPORTED, "group=%d outside [1, 16]", group);
+    if (n < 1 || n > TF_MAX_NODES) return fail(TF_ERR_INVALID_ARG, "n=%d outside [1, %d]", n, TF_MAX_NODES);
+    if ((st = check_attention(own, prefix, prefix_len, group, q, ldq, pos, out, ldo)) != TF_OK) return st;
+    if (!parents || !aligned(parents, 4)) return fail(TF_ERR_INVALID_ARG, "null or misaligned parents");
+    if ((st = check_ws(ws, ws_bytes, tf_attention_tree_workspace_bytes(own, group, n, prefix_len))) != TF_OK) return st;
+    AttnTreeArgs a{};
+    a.own = kv_batch(*own);
+    if (prefix_len > 0) a.prefix = kv_batch(*prefix);
+    a.prefix_len = prefix_len;
+    a.group = group;
+    a.n = n;
+    a.q = q;
+    a.ldq = ldq;
+    a.pos = pos;
+    a.parents = parents;
+    a.out = out;
+    a.ldo = ldo;
+    a.err = static_cast<int *>(ws);
+    a.ws = ws;
+    const char *why = "";
+    cudaError_t e = launch_attn_tree(a, static_cast<cudaStream_t>(stream), &why);
+    if (e != cudaSuccess) return fail(TF_ERR_CUDA, "tf_attention_tree: %s %s", cudaGetErrorString(e), why);
+    return ok();
+}
+
+tf_status tf_attention_prompt(const uint16_t *q, int32_t ldq, const uint16_t *k, int32_t ldk, const uint16_t *v,
+                              int32_t ldv, int32_t rows, int32_t n_kv, int32_t group, const int64_t *starts,
+                              int32_t n_seq, uint16_t *out, int32_t ldo, void *ws, size_t ws_bytes, void *stream) {
+    if (group < 1 || group > 16) return fail(TF_ERR_UNSUPPORTED, "group=%d outside [1, 16]", group);
+    if (n_kv < 1 || n_kv > 128) return fail(TF_ERR_UNSUPPORTED, "n_kv=%d outside [1, 128]", n_kv);
+    if (n_seq < 1 || n_seq > TF_MAX_SEQS) return fail(TF_ERR_UNSUPPORTED, "n_seq=%d outside [1, %d]", n_seq, TF_MAX_SEQS);
+    if (rows < 0) return fail(TF_ERR_INVALID_ARG, "rows=%d must be >= 0", rows);
+    const int n_q = n_kv * group;
+    if ((long long)rows * n_q > 0x7FFFFFFFLL)
+        return fail(TF_ERR_UNSUPPORTED, "rows=%d of %d query heads exceed one launch", rows, n_q);
+    if (!starts || !aligned(starts, 8)) return fail(TF_ERR_INVALID_ARG, "null or misaligned starts");
+    tf_status st = check_ws(ws, ws_bytes, 256);
+    if (st != TF_OK) return st;
+    if (rows == 0) return ok();
+    const struct { const void *p; int ld, heads; const char *name; } arrays[] = {
+        {q, ldq, n_q, "q"}, {k, ldk, n_kv, "k"}, {v, ldv, n_kv, "v"}, {out, ldo, n_q, "out"}};
+    for (const auto &t : arrays)
+        if (!t.p || !aligned(t.p, 16) || t.ld < t.heads * kHeadDim || t.ld % 8)
+            return fail(TF_ERR_INVALID_ARG, "%s must be non-null and 16-B aligned with a row stride that is a multiple "
+                        "of 8 and >= %d, got %d", t.name, t.heads * kHeadDim, t.ld);
+    AttnPromptArgs a{};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.ldq = ldq;
+    a.ldk = ldk;
+    a.ldv = ldv;
+    a.rows = rows;
+    a.n_kv = n_kv;
+    a.group = group;
+    a.starts = starts;
+    a.n_seq = n_seq;
+    a.out = out;
+    a.ldo = ldo;
+    a.err = static_cast<int *>(ws);
+    a.ws = ws;
+    const char *why = "";
+    cudaError_t e = launch_attn_prompt(a, static_cast<cudaStream_t>(stream), &why);
+    if (e != cudaSuccess) return fail(TF_ERR_CUDA, "tf_attention_prompt: %s %s", cudaGetErrorString(e), why);
+    return ok();
+}
+
+tf_status tf_tree_accept(const int32_t *parents, const int32_t *tokens, const int32_t *sampled, const int64_t *pos,
+                         int32_t n_seq, int32_t n, int32_t *accepted, int32_t *bonus, int32_t *path,
+                         int32_t *committed, void *ws, size_t ws_bytes, void *stream) {
+    if (n_seq < 1 || n_seq > TF_MAX_SEQS) return fail(TF_ERR_UNSUPPORTED, "n_seq=%d outside [1, %d]", n_seq, TF_MAX_SEQS);
+    if (n < 1 || n > TF_MAX_NODES) return fail(TF_ERR_INVALID_ARG, "n=%d outside [1, %d]", n, TF_MAX_NODES);
+    if (!parents || !tokens || !sampled || !pos || !accepted || !bonus || !path || !committed || !aligned(pos, 8))
+        return fail(TF_ERR_INVALID_ARG, "null or misaligned pointer");
+    tf_status st = check_ws(ws, ws_bytes, 256);
+    if (st != TF_OK) return st;
+    TreeAcceptArgs a{};
+    a.parents = parents;
+    a.tokens = tokens;
+    a.sampled = sampled;
+    a.pos = pos;
+    a.n_seq = n_seq;
+    a.n = n;
+    a.accepted = accepted;
+    a.bonus = bonus;
+    a.path = path;
+    a.committed = committed;
+    a.err = static_cast<int *>(ws);
+    cudaError_t e = launch_tree_accept(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "tf_tree_accept");
+    return ok();
+}
+
+tf_status tf_kv_keep(const tf_kv_batch *c, const int64_t *pos, const int32_t *path, void *ws, size_t ws_bytes,
+                     void *stream) {
+    tf_status st = check_batch(c, "KV batch");
+    if (st != TF_OK) return st;
+    if (!pos || !path || !aligned(pos, 8) || !aligned(path, 4))
+        return fail(TF_ERR_INVALID_ARG, "null or misaligned pos or path");
+    if ((st = check_ws(ws, ws_bytes, 256)) != TF_OK) return st;
+    cudaError_t e = launch_kv_keep(kv_batch(*c), pos, path, static_cast<int *>(ws), static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "tf_kv_keep");
     return ok();
 }
 

@@ -19,11 +19,12 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtf.so")
 
 TF_OK, TF_ERR_INVALID_ARG, TF_ERR_UNSUPPORTED, TF_ERR_CUDA, TF_ERR_TIMEOUT, TF_ERR_WORKSPACE = range(6)
-TF_DEV_OK, TF_DEV_TIMEOUT, TF_DEV_NONFINITE_LOGIT, TF_DEV_BAD_TOKEN, TF_DEV_BAD_POSITION = range(5)
+TF_DEV_OK, TF_DEV_TIMEOUT, TF_DEV_NONFINITE_LOGIT, TF_DEV_BAD_TOKEN, TF_DEV_BAD_POSITION, TF_DEV_BAD_TREE = range(6)
 HEAD_DIM = 128
 TF_OP_LANE_GEMM, TF_OP_KEYED_SAMPLE, TF_OP_ATTENTION = 1, 2, 3
 MAX_ROWS = 16
 MAX_QUERIES = 128       # rows x query heads per KV head of one sequence in KVBatch.attention
+MAX_NODES, MAX_PATH = 64, 16    # rows of a tree of drafts, and nodes on one of its paths, at most
 MAX_TOP_K = 64
 KV_FORMATS = {"bf16": 0, "e4m3": 1}
 
@@ -112,6 +113,12 @@ SIGNATURES = [
     ("tf_attention_batch_workspace_bytes", SZ, [ctypes.POINTER(KVBatchC), I32, I32, I32]),
     ("tf_attention_batch", ctypes.c_int, [ctypes.POINTER(KVBatchC), ctypes.POINTER(KVBatchC), I32, I32, P, I32, I32,
                                           P, P, I32, P, SZ, P]),
+    ("tf_attention_prompt", ctypes.c_int, [P, I32, P, I32, P, I32, I32, I32, I32, P, I32, P, I32, P, SZ, P]),
+    ("tf_attention_tree_workspace_bytes", SZ, [ctypes.POINTER(KVBatchC), I32, I32, I32]),
+    ("tf_attention_tree", ctypes.c_int, [ctypes.POINTER(KVBatchC), ctypes.POINTER(KVBatchC), I32, I32, P, I32, I32,
+                                         P, P, P, I32, P, SZ, P]),
+    ("tf_tree_accept", ctypes.c_int, [P, P, P, P, I32, I32, P, P, P, P, P, SZ, P]),
+    ("tf_kv_keep", ctypes.c_int, [ctypes.POINTER(KVBatchC), P, P, P, SZ, P]),
     ("tf_selfcheck_scratch_bytes", SZ, [I32]),
     ("tf_selfcheck_row_invariance", ctypes.c_int, [ctypes.POINTER(W4MatrixC), P, I32, P, SZ, P, SZ, P,
                                                    ctypes.POINTER(I32)]),
@@ -758,6 +765,113 @@ class KVBatch:
         if st:
             _check(st)
         return out
+
+
+    def tree_attention_workspace_bytes(self, group: int, n: int, prefix_len: int = 0) -> int:
+        return int(load().tf_attention_tree_workspace_bytes(self._c, group, n, prefix_len))
+
+    def tree_attention(self, q: torch.Tensor, group: int, pos: torch.Tensor, parents: torch.Tensor,
+                       prefix: "KVBatch" = None, prefix_len: int = 0, out: torch.Tensor = None,
+                       ws: torch.Tensor = None, stream=None) -> torch.Tensor:
+        """bf16 [n_seq*n][n_kv*group*128]: node i of sequence b's tree (parents int32 [n_seq][n],
+        -1 for the root, node 0, and for unused rows; entry pos[b] + i stored) attending over entries
+        0..prefix_len-1 of `prefix`, own entries 0..pos[b]-1 and its path's; rows of
+        idle sequences and unused rows are zeros."""
+        if group < 1:
+            raise TFError(TF_ERR_UNSUPPORTED, f"group={group} outside [1, 16]")
+        cols, dev = self.n_kv * group * HEAD_DIM, self.device
+        ldq = _bits16(q, "q", 1, cols, dev)
+        rows, at = q.shape[0], self._pos(pos)
+        n = self._rows(rows)
+        tree = _int32(parents, "parents", (self.n_seq, n), dev)
+        if prefix is not None and prefix.device != dev:
+            _refuse(f"prefix must be on {dev}, got one on {prefix.device}")
+        if out is None:
+            out, ldo = _empty((rows, cols), torch.bfloat16, dev, stream), cols
+        else:
+            ldo = _bits16(out, "out", rows, cols, dev)
+        if ws is None:
+            ws = workspace(self.tree_attention_workspace_bytes(group, n, prefix_len), dev, stream)
+        st = load().tf_attention_tree(self._c, prefix._c if prefix is not None else None, prefix_len, group,
+                                      q.data_ptr(), ldq, n, at, tree, out.data_ptr(), ldo, _ptr(ws), _bytes(ws, dev),
+                                      _stream(stream))
+        if st:
+            _check(st)
+        return out
+
+    def keep(self, pos: torch.Tensor, path: torch.Tensor, ws: torch.Tensor = None, stream=None):
+        """Entry pos[b] + path[b][d] becomes entry pos[b] + d, for every depth of the accepted
+        paths (int32 [n_seq][MAX_PATH], -1 past their ends: ``tree_accept``'s); returns the
+        workspace whose status the call sets."""
+        dev, at = self.device, self._pos(pos)
+        way = _int32(path, "path", (self.n_seq, MAX_PATH), dev)
+        if ws is None:
+            ws = _status_block(dev, stream)
+        st = load().tf_kv_keep(self._c, at, way, _ptr(ws), _bytes(ws, dev), _stream(stream))
+        if st:
+            _check(st)
+        return ws
+
+
+def _int32(t: torch.Tensor, name: str, shape: tuple, device) -> int:
+    if t.dtype is not torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+        _refuse(f"{name} must be a contiguous int32 {list(shape)} tensor on {device}, got {tuple(t.shape)} {t.dtype} on "
+                f"{t.device}")
+    return t.data_ptr()
+
+
+def tree_accept(parents: torch.Tensor, tokens: torch.Tensor, sampled: torch.Tensor, pos: torch.Tensor,
+                ws: torch.Tensor = None, stream=None):
+    """(accepted [n_seq], bonus [n_seq], path [n_seq][MAX_PATH], committed [n_seq][MAX_PATH]), int32: the walk
+    down each sequence's tree (parents, drafted tokens and the token sampled after each
+    node, int32 [n_seq][n]) to the lowest-numbered child that holds the sampled token;
+    -1 past a path's end and for idle sequences (pos[b] = -1)."""
+    dev, shape = parents.device, parents.shape
+    if not parents.is_cuda or len(shape) != 2:
+        _refuse(f"parents must be a CUDA [n_seq][n] tensor, got {tuple(shape)} on {dev}")
+    B, n = shape
+    tree, drafted, drawn = (_int32(t, name, shape, dev) for t, name in
+                            ((parents, "parents"), (tokens, "tokens"), (sampled, "sampled")))
+    if _positions(pos, dev) != B:
+        _refuse(f"pos must hold {B} positions")
+    if ws is None:
+        ws = workspace(256, dev, stream)
+    accepted, bonus = (_empty((B,), torch.int32, dev, stream) for _ in range(2))
+    path, committed = (_empty((B, MAX_PATH), torch.int32, dev, stream) for _ in range(2))
+    st = load().tf_tree_accept(tree, drafted, drawn, pos.data_ptr(), B, n, accepted.data_ptr(), bonus.data_ptr(),
+                               path.data_ptr(), committed.data_ptr(), _ptr(ws), _bytes(ws, dev), _stream(stream))
+    if st:
+        _check(st)
+    return accepted, bonus, path, committed
+
+
+def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, n_kv: int, group: int, starts: torch.Tensor,
+                     out: torch.Tensor = None, ws: torch.Tensor = None, stream=None) -> torch.Tensor:
+    """bf16 [rows][n_kv*group*128]: causal attention of whole prompts.  Sequence s holds rows
+    starts[s] .. starts[s+1]-1 (int64 [n_seq + 1], on the device) of q [rows][n_kv*group*128]
+    and of k and v [rows][n_kv*128] (bf16 / int16 bits, any row stride that is a multiple of 8:
+    columns of one projection, say); rows outside every sequence are not written."""
+    if group < 1 or n_kv < 1:
+        raise TFError(TF_ERR_UNSUPPORTED, f"n_kv={n_kv}, group={group} must be >= 1")
+    dev, cols = q.device, n_kv * group * HEAD_DIM
+    if not q.is_cuda:
+        _refuse(f"q must be a CUDA tensor, got one on {dev}")
+    ldq = _bits16(q, "q", 0, cols, dev)
+    rows = q.shape[0]
+    ldk, ldv = _bits16(k, "k", rows, n_kv * HEAD_DIM, dev), _bits16(v, "v", rows, n_kv * HEAD_DIM, dev)
+    n = _positions(starts, dev) - 1
+    if out is None:
+        out, ldo = _empty((rows, cols), torch.bfloat16, dev, stream), cols
+    else:
+        ldo = _bits16(out, "out", rows, cols, dev)
+    if ws is None:
+        ws = workspace(256, dev, stream)
+    st = load().tf_attention_prompt(q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, rows, n_kv, group,
+                                    starts.data_ptr(), n, out.data_ptr(), ldo, _ptr(ws), _bytes(ws, dev),
+                                    _stream(stream))
+    if st:
+        _check(st)
+    return out
 
 
 def rmsnorm_bf16(x: torch.Tensor, eps: float, out: torch.Tensor = None, stream=None) -> torch.Tensor:
