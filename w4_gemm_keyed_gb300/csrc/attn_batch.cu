@@ -34,28 +34,48 @@
 // entries 212 us, 169 as a bf16 cache.
 #include <atomic>
 
-#include <cuda.h>
 #include <cudaTypedefs.h>
 
 #include "attn_batch.cuh"
-#include "tf_tcgen05.cuh"
+#include "attn_tiles.cuh"
 #include "w4_gemm.cuh"
 
 namespace tfk {
 
+// cuTensorMapEncodeTiled, or null where the driver has none.
+static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool there = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                               cudaSuccess &&
+                           q == cudaDriverEntryPointSuccess;
+        return there ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
+    }();
+    return fn;
+}
+
+bool encode_tiles(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
+                  const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle, const char **why) {
+    const cuuint32_t ones[3] = {1, 1, 1};
+    const auto fn = tensor_map_encoder();
+    if (!fn) {
+        *why = "cuTensorMapEncodeTiled is unavailable";
+        return false;
+    }
+    if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, ones,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
+        *why = "cuTensorMapEncodeTiled rejected the layout";
+        return false;
+    }
+    return true;
+}
+
 namespace {
 
-constexpr float kScaleLog2 = 0.12751743074439720f;   // log2(e) / sqrt(128)
-// A vector's reference maximum moves only when a score passes it by more than
-// 2^8 in weight: weights stay below 2^8 (exact in the sums' exponents), and the
-// output is rescaled rarely.  The decision is the vector's own.
-constexpr float kMaxSlack = 8.0f / kScaleLog2;
-
-constexpr int kTile = 128;              // query vectors and keys per matrix product
 constexpr int kOwnPart = 512;           // own entries per part
 constexpr int kMinPrefixPart = 512;     // shared entries per part, at least
-constexpr int kHalfBytes = kTile * 128; // 64 elements of 128 rows
-constexpr int kTileBytes = 2 * kHalfBytes;
 constexpr int kRing = 4;                // items known ahead
 constexpr int kGroups = 256;            // entries of the table of own parts
 constexpr int kSoftmaxWarps = 8, kProducerWarp = 8, kMmaWarp = 9;
@@ -158,15 +178,6 @@ constexpr size_t kSmemBytes = size_t(2 + Form<E4M3>::stages) * kTileBytes + size
                               sizeof(Shared);
 static_assert(kSmemBytes<false> <= 227 * 1024 && kSmemBytes<true> <= 227 * 1024, "shared memory");
 
-template <int N>
-__device__ __forceinline__ void regs_raise() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_lower() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // A wait of one thread that is its warp's only one in the role.
 __device__ __forceinline__ bool lane_wait(Shared *sh, uint64_t *bar, uint32_t parity) {
     return mbar_wait_or_abort(&sh->abort, bar, parity);
@@ -178,36 +189,6 @@ __device__ __forceinline__ bool lane_wait(Shared *sh, uint64_t *bar, uint32_t pa
 // rows over bf16 ones 0.6 %.
 __device__ __forceinline__ bool warp_wait(Shared *sh, uint64_t *bar, uint32_t parity) {
     return mbar_warp_wait_or_abort(&sh->abort, bar, parity);
-}
-
-// A bounded wait for what is still in flight when a role ends.
-__device__ __forceinline__ void wait_drained(uint64_t *bar, uint32_t parity) {
-    for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait(bar, parity); ++i) {
-    }
-}
-
-// K and V tiles are taken in the order K0 K1 V0 K2 V1 ... V(n-1) of each item.
-__device__ __forceinline__ int k_order(int i) { return i == 0 ? 0 : 2 * i - 1; }
-__device__ __forceinline__ int v_order(int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; }
-// The tile at place t of that order: whether it is a V tile, and which.
-__device__ __forceinline__ bool order_is_v(int t, int n) { return t == 2 * n - 1 || (t != 0 && t % 2 == 0); }
-__device__ __forceinline__ int order_tile(int t, int n) {
-    return t == 2 * n - 1 ? n - 1 : (t == 0 ? 0 : (t % 2 == 0 ? t / 2 - 1 : (t + 1) / 2));
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
-__device__ __forceinline__ bool bf16x2_nonfinite(uint32_t w) {
-    return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-}
-__device__ __forceinline__ uint32_t bf16x2_finite(uint32_t w) {   // non-finite halves -> 0
-    if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
-    if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
-    return w;
 }
 
 // ------------------------------------------------------------------ item order
@@ -1014,48 +995,18 @@ __global__ void __launch_bounds__(kJoinThreads, 6) attn_batch_join_kernel(AttnBa
     *reinterpret_cast<uint4 *>(a.out + (size_t)row * a.ldo + (size_t)(j * a.group + v - row * a.group) * kHeadDim + 4 * quad) = y;
 }
 
-// cuTensorMapEncodeTiled, or null where the driver has none.
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        const bool there = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                               cudaSuccess &&
-                           q == cudaDriverEntryPointSuccess;
-        return there ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
-    }();
-    return fn;
-}
-
-bool encode(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
-            const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle, const char **why) {
-    const cuuint32_t ones[3] = {1, 1, 1};
-    const auto fn = tensor_map_encoder();
-    if (!fn) {
-        *why = "cuTensorMapEncodeTiled is unavailable";
-        return false;
-    }
-    if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, ones,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
-        *why = "cuTensorMapEncodeTiled rejected the layout";
-        return false;
-    }
-    return true;
-}
-
 // Innermost first: an entry's 128 elements, entries, (sequence, head).  The cache
 // is stored with its 16-byte chunks already permuted by position, as the
 // 128-byte swizzle wants them in shared memory, so the copy permutes nothing.
 bool encode_cache(CUtensorMap *m, const void *base, int rows, int max_len, int outer, const char **why) {
-    return encode(m, base, {cuuint64_t(kHeadDim), cuuint64_t(rows), cuuint64_t(outer)},
+    return encode_tiles(m, base, {cuuint64_t(kHeadDim), cuuint64_t(rows), cuuint64_t(outer)},
                   {cuuint64_t(kHeadDim) * 2, cuuint64_t(max_len) * kHeadDim * 2}, {64, kTile, 1},
                   CU_TENSOR_MAP_SWIZZLE_NONE, why);
 }
 
 // Innermost first: a head's 128 elements, heads, rows.
 bool encode_queries(CUtensorMap *m, const AttnBatchArgs &a, const char **why) {
-    return encode(m, a.q, {cuuint64_t(kHeadDim), cuuint64_t(a.own.n_kv) * a.group, cuuint64_t(a.own.n_seq) * a.R},
+    return encode_tiles(m, a.q, {cuuint64_t(kHeadDim), cuuint64_t(a.own.n_kv) * a.group, cuuint64_t(a.own.n_seq) * a.R},
                   {cuuint64_t(kHeadDim) * 2, cuuint64_t(a.ldq) * 2},
                   {64, cuuint32_t(a.group), cuuint32_t(kTile / a.group)}, CU_TENSOR_MAP_SWIZZLE_128B, why);
 }

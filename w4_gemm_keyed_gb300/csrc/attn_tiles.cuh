@@ -1,0 +1,65 @@
+// What the tcgen05 attention kernels share: tiles of 128 query vectors, the order of
+// their K and V tiles, and small device helpers.
+#pragma once
+#include <cuda.h>
+
+#include "kv_batch.cuh"
+#include "tf_tcgen05.cuh"
+
+namespace tfk {
+
+constexpr float kScaleLog2 = 0.12751743074439720f;   // log2(e) / sqrt(128)
+// A vector's reference maximum moves only when a score passes it by more than
+// 2^8 in weight: weights stay below 2^8 (exact in the sums' exponents), and the
+// output is rescaled rarely.  The decision is the vector's own.
+constexpr float kMaxSlack = 8.0f / kScaleLog2;
+
+constexpr int kTile = 128;              // query vectors and keys per matrix product
+constexpr int kHalfBytes = kTile * 128; // 64 elements of 128 rows
+constexpr int kTileBytes = 2 * kHalfBytes;
+
+template <int N>
+__device__ __forceinline__ void regs_raise() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_lower() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// A bounded wait for what is still in flight when a role ends.
+__device__ __forceinline__ void wait_drained(uint64_t *bar, uint32_t parity) {
+    for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait(bar, parity); ++i) {
+    }
+}
+
+// K and V tiles are taken in the order K0 K1 V0 K2 V1 ... V(n-1) of each item.
+__device__ __forceinline__ int k_order(int i) { return i == 0 ? 0 : 2 * i - 1; }
+__device__ __forceinline__ int v_order(int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; }
+// The tile at place t of that order: whether it is a V tile, and which.
+__device__ __forceinline__ bool order_is_v(int t, int n) { return t == 2 * n - 1 || (t != 0 && t % 2 == 0); }
+__device__ __forceinline__ int order_tile(int t, int n) {
+    return t == 2 * n - 1 ? n - 1 : (t == 0 ? 0 : (t % 2 == 0 ? t / 2 - 1 : (t + 1) / 2));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+__device__ __forceinline__ bool bf16x2_nonfinite(uint32_t w) {
+    return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+__device__ __forceinline__ uint32_t bf16x2_finite(uint32_t w) {   // non-finite halves -> 0
+    if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+    if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
+    return w;
+}
+
+// Tiled map of bf16 elements, innermost dimension first (its stride is 1; strides in
+// bytes); false and *why where there is none.
+bool encode_tiles(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
+                  const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle, const char **why);
+
+}  // namespace tfk
