@@ -237,6 +237,19 @@ def test_many_sequences(tf):
     c.check(out)
 
 
+@pytest.mark.parametrize("n_kv,g,longest", [(8, 8, 301), (8, 8, 20), (4, 5, 140), (8, 16, 33)])
+def test_many_items_a_processor(tf, n_kv, g, longest):
+    """Items of one and of two tiles, of one key tile and of several, one after the other: sequence by
+    sequence the bits of calls that hold it alone."""
+    rng = inputs.rng_for(longest)
+    c, ws = Case(longest, [int(n) for n in rng.integers(1, longest + 1, 60)], n_kv, g), tf.workspace(256)
+    out = c.run(tf, ws=ws)
+    assert tf.workspace_status(ws) == tf.TF_DEV_OK
+    for a, b in list(zip(c.starts[:-1], c.starts[1:]))[::7]:
+        assert torch.equal(out[a:b], c.run(tf, x=c.x[a:b].contiguous(), starts=[0, b - a]))
+    assert torch.equal(out, c.run(tf, ws=ws)) and tf.workspace_status(ws) == tf.TF_DEV_OK
+
+
 def test_graphs_share_a_workspace_and_read_the_starts_anew(tf):
     a, b = Case(31, [200, 90], 2, 4), Case(32, [40, 40, 300], 1, 8)
     ws, cases = tf.workspace(256), []

@@ -48,6 +48,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+// 32 bytes, 32-byte aligned: a whole sector by one thread.
+__device__ __forceinline__ void st_global_32(void *p, const uint32_t *v) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ bool bf16x2_nonfinite(uint32_t w) {
     return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
 }
