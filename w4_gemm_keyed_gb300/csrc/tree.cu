@@ -6,8 +6,6 @@ namespace tfk {
 
 namespace {
 
-constexpr float kScale = 0.08838834764831845f;      // 1 / sqrt(128)
-
 // ------------------------------------------------------------- acceptance
 // A warp per sequence, two nodes a lane.  Each step asks every node at once whether
 // it is a child of the walk's last node that holds the token sampled there; the
@@ -113,107 +111,6 @@ __global__ void __launch_bounds__(32 * kKeepWarps) kv_keep_kernel(KvBatch c, con
     if (E4M3 && lane < n) scale[base + lane] = uint8_t(s);
 }
 
-// ------------------------------------------------------- attention of a tree's nodes
-// A warp per (node, query head): keys 32 at a time in the order of the path, a key per
-// lane for the scores, four output columns per lane for the sums, all in fp32.
-template <bool E4M3>
-struct Entry {      // one half (K or V) of a cache's entries
-    const void *data;
-    const uint8_t *scale;
-    __device__ uint32_t factor(size_t e) const { return E4M3 ? e4m3_factor(scale[e]) : 0u; }
-    __device__ void eight(size_t e, int c, uint32_t f, float (&x)[8]) const {   // elements 8c .. 8c + 7
-        uint32_t w[4];
-        if constexpr (E4M3) {
-            const uint2 p = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(data) + e * kHeadDim +
-                                                             16 * (c & 7) + 8 * (c >> 3));
-            e4m3_expand(p.x, f, w[0], w[1]);
-            e4m3_expand(p.y, f, w[2], w[3]);
-        } else {
-            const uint4 p = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(data) + e * kHeadDim +
-                                                             8 * (c ^ int(e & 7)));
-            w[0] = p.x, w[1] = p.y, w[2] = p.z, w[3] = p.w;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    }
-};
-
-constexpr int kAttnWarps = 4;
-
-template <bool E4M3>
-__global__ void __launch_bounds__(32 * kAttnWarps) attn_tree_kernel(AttnTreeArgs a) {
-    __shared__ float s_q[kAttnWarps][kHeadDim];
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.y;
-    const int n_q = a.own.n_kv * a.group, unit = blockIdx.x * kAttnWarps + warp;
-    if (unit >= a.n * n_q) return;
-    const int node = unit / n_q, h = unit - node * n_q, j = h / a.group, row = b * a.n + node;
-    const int32_t *parents = a.parents + (size_t)b * a.n;
-    int d[2];
-    const bool tree = tree_depths(parents, a.n, d);
-    const long long pos = seq_position(a.pos, b, a.n, a.own.max_len, a.err, unit == 0 && lane == 0);
-    if (unit == 0 && lane == 0 && pos >= 0 && !tree) set_error(a.err, kDevBadTree);
-    const int d0 = __shfl_sync(0xFFFFFFFFu, d[0], node & 31), d1 = __shfl_sync(0xFFFFFFFFu, d[1], node & 31);
-    const int depth = node < 32 ? d0 : d1;
-    uint2 *out = reinterpret_cast<uint2 *>(a.out + (size_t)row * a.ldo + h * kHeadDim) + lane;
-    if (pos < 0 || !tree || depth < 0) {
-        *out = make_uint2(0u, 0u);
-        return;
-    }
-    int my_node = node;     // lane t: the path's node at depth t
-    for (int up = node, t = depth; t >= 0; --t, up = parents[up])
-        if (lane == t) my_node = up;
-    const uint16_t *q = a.q + (size_t)row * a.ldq + h * kHeadDim;
-    for (int i = lane; i < kHeadDim; i += 32) s_q[warp][i] = __uint_as_float(uint32_t(q[i]) << 16) * kScale;
-    __syncwarp();
-    const long long total = a.prefix_len + pos + depth + 1;
-    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (long long t0 = 0; t0 < total; t0 += 32) {
-        const long long t = t0 + lane;
-        const long long y = t - a.prefix_len;       // own position
-        const int on = __shfl_sync(0xFFFFFFFFu, my_node, int(max(0ll, min(31ll, y - pos))));
-        const bool shared = y < 0, seen = t < total;
-        const Entry<E4M3> k = {shared ? a.prefix.k : a.own.k, shared ? a.prefix.k_scale : a.own.k_scale};
-        const size_t e = shared ? (size_t)j * a.prefix.max_len + t
-                                : (size_t)(b * a.own.n_kv + j) * a.own.max_len + (y < pos ? y : pos + on);
-        float s = -INFINITY;
-        if (seen) {
-            s = 0.f;
-            const uint32_t f = k.factor(e);
-            for (int c = 0; c < 16; ++c) {
-                float x[8];
-                k.eight(e, c, f, x);
-                for (int i = 0; i < 8; ++i) s = fmaf(x[i], s_q[warp][8 * c + i], s);
-            }
-        }
-        float top = s;
-        for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
-        top = fmaxf(top, m);
-        const float scale = top == -INFINITY ? 1.f : expf(m - top), w = seen ? expf(s - top) : 0.f;
-        float sum = w;
-        for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, i);
-        l = l * scale + sum;
-        m = top;
-        for (int i = 0; i < 4; ++i) o[i] *= scale;
-        const int keys = int(min(32ll, total - t0));
-        for (int u = 0; u < keys; ++u) {
-            const float wu = __shfl_sync(0xFFFFFFFFu, w, u);
-            const size_t eu = __shfl_sync(0xFFFFFFFFu, (unsigned long long)e, u);
-            const bool su = t0 + u < a.prefix_len;
-            const Entry<E4M3> v = {su ? a.prefix.v : a.own.v, su ? a.prefix.v_scale : a.own.v_scale};
-            float x[8];
-            v.eight(eu, lane >> 1, v.factor(eu), x);
-            for (int i = 0; i < 4; ++i) o[i] = fmaf(wu, lane & 1 ? x[4 + i] : x[i], o[i]);
-        }
-    }
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(o[0] / l, o[1] / l), hi = __floats2bfloat162_rn(o[2] / l, o[3] / l);
-    *out = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
-}
-
 }  // namespace
 
 cudaError_t launch_tree_accept(const TreeAcceptArgs &a, cudaStream_t s) {
@@ -224,14 +121,6 @@ cudaError_t launch_kv_keep(const KvBatch &c, const int64_t *pos, const int32_t *
     const dim3 grid((2 * c.n_kv + kKeepWarps - 1) / kKeepWarps, c.n_seq), block(32 * kKeepWarps);
     return c.format == kKvE4m3 ? launch_pdl(kv_keep_kernel<true>, grid, block, 0, s, c, pos, path, err)
                                : launch_pdl(kv_keep_kernel<false>, grid, block, 0, s, c, pos, path, err);
-}
-
-size_t attn_tree_bytes(const KvBatch &, int, int, int) { return 256; }
-
-cudaError_t launch_attn_tree(const AttnTreeArgs &a, cudaStream_t s, const char **) {
-    const dim3 grid((a.n * a.own.n_kv * a.group + kAttnWarps - 1) / kAttnWarps, a.own.n_seq), block(32 * kAttnWarps);
-    return a.own.format == kKvE4m3 ? launch_pdl(attn_tree_kernel<true>, grid, block, 0, s, a)
-                                   : launch_pdl(attn_tree_kernel<false>, grid, block, 0, s, a);
 }
 
 }  // namespace tfk

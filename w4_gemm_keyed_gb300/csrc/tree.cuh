@@ -1,5 +1,5 @@
-// Trees of drafted tokens: their shape, acceptance along them, the entries of an
-// accepted path, and attention of their nodes.
+// Trees of drafted tokens: their shape, acceptance along them, and the entries of an
+// accepted path.
 #pragma once
 #include "kv_batch.cuh"
 
@@ -60,22 +60,5 @@ cudaError_t launch_tree_accept(const TreeAcceptArgs &a, cudaStream_t s);
 
 // entries pos[b] + path[b][d] -> pos[b] + d
 cudaError_t launch_kv_keep(const KvBatch &c, const int64_t *pos, const int32_t *path, int *err, cudaStream_t s);
-
-struct AttnTreeArgs {
-    KvBatch own, prefix;    // prefix: n_seq = 1; not read when prefix_len == 0
-    int prefix_len;
-    int group, n;
-    const uint16_t *q;      // bf16 [n_seq * n][ldq]
-    int ldq;
-    const int64_t *pos;     // [n_seq]
-    const int32_t *parents; // [n_seq][n]
-    uint16_t *out;          // bf16 [n_seq * n][ldo]
-    int ldo;
-    int *err;
-    void *ws;               // attn_tree_bytes()
-};
-size_t attn_tree_bytes(const KvBatch &own, int prefix_len, int group, int n);
-// *why is set where the failure is not a CUDA call's.
-cudaError_t launch_attn_tree(const AttnTreeArgs &a, cudaStream_t s, const char **why);
 
 }  // namespace tfk
