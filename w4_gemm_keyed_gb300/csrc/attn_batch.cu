@@ -9,7 +9,7 @@
 // kOwnPart.  An item is one part of one KV head with the query vectors that
 // read it: for a prefix part, up to 256 of the batch's n_seq * R * group vectors
 // (the prefix is read once for all of them, from HBM once and from L2 for the
-// rest), for an own part the sequence's R * group (up to 256 of a tree's).  Within an item each vector
+// rest), for an own part the sequence's R * group.  Within an item each vector
 // folds its keys in ascending order, 128 at a time, with a running maximum; the
 // parts' results (maximum m, weight sum l, unnormalised output o, fp32) are
 // joined per vector in ascending order by a second kernel.  So a row's bits
@@ -22,11 +22,6 @@
 // by rows x group; with few of them the rest are idle, and a 128-key tile still
 // takes an SM about 2,000 cycles where HBM delivers one (K and V) to each SM in
 // 2,800, so few rows need no form of their own.
-//
-// Trees of drafts (tree.cuh) use the same items and parts for the entries that lie kMaxPath
-// positions or more before a node; the entries nearer than that, every node of its path among
-// them, are folded in path order by the kernel that joins the parts, so that a node's
-// bits do not tell whether an ancestor is a node of the pass or was committed before.
 //
 // What bounds it (GB300, measured call after call on the same inputs): many rows, the
 // tensor cores and the hand-over between them and the softmax: a step of two tiles and
@@ -43,7 +38,6 @@
 
 #include "attn_batch.cuh"
 #include "attn_tiles.cuh"
-#include "tree.cuh"
 #include "w4_gemm.cuh"
 
 namespace tfk {
@@ -119,14 +113,13 @@ struct Item {
 };
 
 // Prefix partials: [part][n_kv][tiles][32 quads][tile vectors][4]; own partials:
-// [part][n_seq][n_kv][32 quads][R * group][4], a tree's in tiles as the prefix's.  Maxima and sums: the same
+// [part][n_seq][n_kv][32 quads][R * group][4].  Maxima and sums: the same
 // without the quads.  Quad-major so that a warp's 32 vectors store and load 512
 // consecutive bytes.
 struct Plan {
     int n_vec, tile, tiles, pairs;      // vectors; per tile; tiles and pairs of them per KV head
     int part, n_parts;          // prefix part length and count
     int own_parts_max;
-    int own_tile, own_pairs, own_slots;     // a sequence's own vectors: per tile, pairs of tiles, slots per part and head
     long long own0;             // index of the first own vector slot after the prefix's
     long long slots;            // vector slots in all
 };
@@ -152,12 +145,8 @@ Plan plan_of(const KvBatch &own, int prefix_len, int group, int R) {
     p.part = prefix_part(prefix_len, own.n_kv);
     p.n_parts = (prefix_len + p.part - 1) / p.part;
     p.own_parts_max = (own.max_len + kOwnPart - 1) / kOwnPart;
-    p.own_tile = R * group < p.tile ? R * group : p.tile;
-    const int own_tiles = (R * group + p.own_tile - 1) / p.own_tile;
-    p.own_pairs = (own_tiles + 1) / 2;
-    p.own_slots = own_tiles * p.own_tile;       // R * group where that is one tile
     p.own0 = (long long)p.n_parts * own.n_kv * p.tiles * p.tile;
-    p.slots = p.own0 + (long long)p.own_parts_max * own.n_kv * own.n_seq * p.own_slots;
+    p.slots = p.own0 + (long long)p.own_parts_max * own.n_kv * p.n_vec;
     return p;
 }
 
@@ -205,16 +194,11 @@ __device__ __forceinline__ bool warp_wait(Shared *sh, uint64_t *bar, uint32_t pa
 // ------------------------------------------------------------------ item order
 // Prefix items first (the longest), vector pairs fastest so that the CTAs working
 // on one part read it from L2; then own items, heads fastest.
-// Own items of sequence b and a head.  A tree's are over the entries before the root: its deepest
-// nodes see all of them here, the others up to 15 fewer.
-template <bool TREE>
 __device__ int own_parts(const KernelArgs &k, int b, bool report) {
     const long long p = seq_position(k.a.pos, b, k.a.R, k.a.own.max_len, k.a.err, report);
-    if (TREE) return p < 0 ? 0 : int((p + kOwnPart - 1) / kOwnPart) * k.p.own_pairs;
     return p < 0 ? 0 : int((p + k.a.R - 1) / kOwnPart) + 1;
 }
 
-template <bool TREE>
 __device__ Item item_of(const KernelArgs &k, const Shared *sh, unsigned i, int group_seqs) {
     Item it{};
     const unsigned n_kv = k.a.own.n_kv, rg = k.a.R * k.a.group, pairs = k.p.pairs;
@@ -247,20 +231,9 @@ __device__ Item item_of(const KernelArgs &k, const Shared *sh, unsigned i, int g
     }
     u -= sh->before[lo];
     int b = lo * group_seqs;
-    for (int n; u >= (n = own_parts<TREE>(k, b, false)); ++b) u -= n;
+    for (int n; u >= (n = own_parts(k, b, false)); ++b) u -= n;
     const long long p = k.a.pos[b];
     it.b = b;
-    if constexpr (TREE) {
-        const int part = idx_div(u, k.p.own_pairs), first = (u - part * k.p.own_pairs) * 2 * k.p.tile;
-        it.vec0 = b * rg + first;
-        it.n_vec = min(2 * k.p.tile, int(rg) - first);
-        it.key0 = part * kOwnPart;
-        it.n_keys = int(min((long long)kOwnPart, p - it.key0));
-        it.lim0 = int(p - kMaxPath - it.key0);      // the root's
-        it.stride = k.p.own_tile;
-        it.part = k.p.own0 + (((long long)part * k.a.own.n_seq + b) * n_kv + it.j) * k.p.own_slots + first;
-        return it;
-    }
     it.vec0 = b * rg;
     it.n_vec = rg;
     it.key0 = u * kOwnPart;
@@ -282,7 +255,7 @@ __device__ Item item_of(const KernelArgs &k, const Shared *sh, unsigned i, int g
 //               S columns so that the next key tile's scores are computed
 //               while this one's are being exponentiated.
 
-template <bool E4M3, bool TREE>
+template <bool E4M3>
 __device__ void produce(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint8_t *stages) {
     constexpr int kStages = E4M3 ? Form<E4M3>::raw : Form<E4M3>::stages;
     uint64_t *const full = E4M3 ? sh->raw_full : sh->kv_full, *const empty = E4M3 ? sh->raw_empty : sh->kv_empty;
@@ -293,7 +266,7 @@ __device__ void produce(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint8
     for (int g0 = 0; g0 < n_groups; g0 += 32) {
         int n = 0;
         for (int b = (g0 + lane) * group_seqs; b < min(n_seq, (g0 + lane + 1) * group_seqs); ++b)
-            n += own_parts<TREE>(k, b, blockIdx.x == 0);
+            n += own_parts(k, b, blockIdx.x == 0);
         int sum = n;
         for (int o = 1; o < 32; o <<= 1) {
             const int t = __shfl_up_sync(0xFFFFFFFFu, sum, o);
@@ -314,7 +287,7 @@ __device__ void produce(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint8
     for (unsigned n = 0;; ++n) {
         const int slot = n % kRing;
         if (n >= kRing && !lane_wait(sh, &sh->item_empty[slot], (n / kRing - 1) & 1)) break;
-        const Item it = item_of<TREE>(k, sh, i, group_seqs);
+        const Item it = item_of(k, sh, i, group_seqs);
         sh->item[slot] = it;
         mbar_arrive(&sh->item_full[slot]);
         const unsigned taken = atomicAdd(k.next, 1u);       // the item after this one
@@ -641,7 +614,7 @@ __device__ __forceinline__ bool any_nonfinite(const KernelArgs &k, const Item &i
     return __any_sync(0xFFFFFFFFu, bad);
 }
 
-template <bool E4M3, bool TREE>
+template <bool E4M3>
 __device__ void softmax(const KernelArgs &k, Shared *sh, uint32_t tmem) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wg = warp >> 2;
     const uint32_t my_lanes = uint32_t(32 * (warp & 3)) << 16;
@@ -665,18 +638,7 @@ __device__ void softmax(const KernelArgs &k, Shared *sh, uint32_t tmem) {
         const int v = 32 * (warp & 3) + lane;               // vector within the tile
         const int n_here = min(k.p.tile, it.n_vec - wg * k.p.tile);     // of this tile
         const bool active = 32 * (warp & 3) < n_here;
-        int lim = it.lim0;                                              // last visible part entry
-        if (it.b >= 0) {
-            if constexpr (TREE) {
-                int d[2];       // depths of the sequence's nodes; the join leaves out rows that have none
-                tree_depths(k.a.parents + (size_t)it.b * k.a.R, k.a.R, d);
-                const int node = (it.vec0 + wg * k.p.tile + min(v, n_here - 1)) / k.a.group - it.b * k.a.R;
-                const int d0 = __shfl_sync(0xFFFFFFFFu, d[0], node & 31), d1 = __shfl_sync(0xFFFFFFFFu, d[1], node & 31);
-                lim += node < 32 ? d0 : d1;
-            } else {
-                lim += min(v, it.n_vec - 1) / k.a.group;
-            }
-        }
+        const int lim = it.b < 0 ? it.lim0 : it.lim0 + min(v, it.n_vec - 1) / k.a.group;     // last visible part entry
         float m = -INFINITY, l = 0.f;
         for (int i = 0; i < tiles; ++i) {
             const int buf = two ? wg : i & 1;
@@ -844,7 +806,7 @@ __device__ void softmax(const KernelArgs &k, Shared *sh, uint32_t tmem) {
     }
 }
 
-template <bool E4M3, bool TREE>
+template <bool E4M3>
 __global__ void __launch_bounds__(Form<E4M3>::threads, 1) attn_batch_kernel(const __grid_constant__ KernelArgs k) {
     using F = Form<E4M3>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -887,11 +849,11 @@ __global__ void __launch_bounds__(Form<E4M3>::threads, 1) attn_batch_kernel(cons
     grid_launch_dependents();
     if (warp < kSoftmaxWarps) {
         regs_raise<F::regs_softmax>();
-        softmax<E4M3, TREE>(k, sh, tmem);
+        softmax<E4M3>(k, sh, tmem);
     } else {
         regs_lower<F::regs_other>();
         if (warp == kProducerWarp)
-            produce<E4M3, TREE>(k, sh, q_tiles, E4M3 ? raw : stages);
+            produce<E4M3>(k, sh, q_tiles, E4M3 ? raw : stages);
         else if (warp == kMmaWarp)
             multiply<E4M3>(k, sh, q_tiles, stages, tmem);
         else if (E4M3 && warp >= kExpandWarp)
@@ -1033,199 +995,6 @@ __global__ void __launch_bounds__(kJoinThreads, 6) attn_batch_join_kernel(AttnBa
     *reinterpret_cast<uint4 *>(a.out + (size_t)row * a.ldo + (size_t)(j * a.group + v - row * a.group) * kHeadDim + 4 * quad) = y;
 }
 
-// ------------------------------------------------------------------ a tree's near entries and the join
-// A CTA takes one node and KV head.  The near entries are those at the last kMaxPath own
-// positions up to the node's, its path's last nodes among them: 16 keys, in path order and in fp32,
-// worked on before the attention grid has ended.  Then the parts' results in ascending order, the
-// near ones last.  A thread takes one (query head, column quad) at a time, heads fastest as the
-// parts' results are stored, so that a row's group of 8 heads reads 128 consecutive bytes.
-constexpr int kTreeThreads = 128, kTreeUnroll = 4, kMaxGroup = 16, kMaxUnits = kMaxGroup * 32 / kTreeThreads;
-
-template <bool E4M3>
-__device__ __forceinline__ uint4 cache_chunk(const void *data, const uint8_t *scale, size_t entry, int c) {   // elements 8c .. 8c + 7
-    uint4 x;
-    if constexpr (E4M3) {
-        const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(data) + entry * kHeadDim + 16 * (c & 7) +
-                                                         8 * (c >> 3));
-        const uint32_t f = e4m3_factor(scale[entry]);
-        e4m3_expand(w.x, f, x.x, x.y);
-        e4m3_expand(w.y, f, x.z, x.w);
-    } else {
-        x = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(data) + entry * kHeadDim + 8 * (c ^ int(entry & 7)));
-    }
-    return x;
-}
-
-template <bool E4M3>
-__global__ void __launch_bounds__(kTreeThreads, 6) attn_tree_join_kernel(AttnBatchArgs a, Plan p, const float *opart,
-                                                                         const float2 *ml, unsigned *next) {
-    // rows of 16 chunks of 8 bf16, chunk c of row r at c XOR (r % 8): rows are read side by side
-    __shared__ uint4 s_q[kMaxGroup][16], s_k[kMaxPath][16], s_v[kMaxPath][16];
-    __shared__ float s_w[kMaxGroup][kMaxPath + 1];
-    __shared__ float2 s_ml[kMaxGroup];
-    __shared__ int s_entry[kMaxPath], s_near, s_depth;
-    const int tid = threadIdx.x, g = a.group, j = blockIdx.y, row = blockIdx.x;
-    const int b = idx_div(row, a.R), node = row - b * a.R, n_kv = a.own.n_kv;
-    const long long pos = seq_position(a.pos, b, a.R, a.own.max_len, a.err, false);
-    if (tid < 32) {
-        const int32_t *parents = a.parents + (size_t)b * a.R;
-        int d[2];
-        const bool tree = tree_depths(parents, a.R, d);
-        if (!tree && pos >= 0 && node == 0 && j == 0 && tid == 0) set_error(a.err, kDevBadTree);
-        const int d0 = __shfl_sync(0xFFFFFFFFu, d[0], node & 31), d1 = __shfl_sync(0xFFFFFFFFu, d[1], node & 31);
-        const int depth = tree && pos >= 0 ? (node < 32 ? d0 : d1) : -1;
-        if (tid == 0) {
-            // own positions first .. pos + depth, nearest last
-            const int near = depth < 0 ? 0 : int(min((long long)kMaxPath, pos + depth + 1));
-            const long long first = pos + depth + 1 - near;
-            int up = node;
-            for (int t = near - 1; t >= 0; --t) {
-                const long long y = first + t;
-                s_entry[t] = int(y < pos ? y : pos + up);
-                if (y > pos) up = parents[up];
-            }
-            s_near = near;
-            s_depth = depth;
-        }
-    }
-    __syncthreads();
-    const int near = s_near, depth = s_depth;
-    if (near == 0) {        // an idle sequence, no tree, or an unused row
-        for (int i = tid; i < g * 16; i += kTreeThreads)
-            *reinterpret_cast<uint4 *>(a.out + (size_t)row * a.ldo + (size_t)j * g * kHeadDim + 8 * i) = make_uint4(0u, 0u, 0u, 0u);
-        grid_dependency_wait();
-        grid_launch_dependents();
-        if (row == 0 && j == 0 && tid == 0) *next = 0u;
-        return;
-    }
-    const size_t base = (size_t)(b * n_kv + j) * a.own.max_len;
-    for (int i = tid; i < near * 16; i += kTreeThreads) {
-        const int t = i >> 4, c = i & 15;
-        const size_t e = base + s_entry[t];
-        s_k[t][c ^ (t & 7)] = cache_chunk<E4M3>(a.own.k, a.own.k_scale, e, c);
-        s_v[t][c ^ (t & 7)] = cache_chunk<E4M3>(a.own.v, a.own.v_scale, e, c);
-    }
-    for (int i = tid; i < g * 16; i += kTreeThreads) {
-        const int h = i >> 4, c = i & 15;
-        s_q[h][c ^ (h & 7)] = *reinterpret_cast<const uint4 *>(a.q + (size_t)row * a.ldq + (size_t)j * g * kHeadDim + 8 * i);
-    }
-    __syncthreads();
-    auto low = [](uint32_t w) { return __uint_as_float(w << 16); };
-    auto high = [](uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); };
-    for (int i = tid; i < g * kMaxPath; i += kTreeThreads) {
-        const int h = i / kMaxPath, t = i % kMaxPath;
-        float sum[2] = {0.f, 0.f};
-        if (t < near) {
-#pragma unroll 4
-            for (int c = 0; c < 16; ++c) {
-                const uint4 x = s_q[h][c ^ (h & 7)], y = s_k[t][c ^ (t & 7)];
-                sum[0] = fmaf(low(x.x), low(y.x), sum[0]);
-                sum[1] = fmaf(high(x.x), high(y.x), sum[1]);
-                sum[0] = fmaf(low(x.y), low(y.y), sum[0]);
-                sum[1] = fmaf(high(x.y), high(y.y), sum[1]);
-                sum[0] = fmaf(low(x.z), low(y.z), sum[0]);
-                sum[1] = fmaf(high(x.z), high(y.z), sum[1]);
-                sum[0] = fmaf(low(x.w), low(y.w), sum[0]);
-                sum[1] = fmaf(high(x.w), high(y.w), sum[1]);
-            }
-        }
-        s_w[h][t] = t < near ? sum[0] + sum[1] : -INFINITY;
-    }
-    __syncthreads();
-    for (int h = tid; h < g; h += kTreeThreads) {
-        float m = -INFINITY, l = 0.f;
-        for (int t = 0; t < near; ++t) m = fmaxf(m, s_w[h][t]);
-        const float mc = m == -INFINITY ? 0.f : m;
-        for (int t = 0; t < near; ++t) {
-            const float w = ex2_approx((s_w[h][t] - mc) * kScaleLog2);
-            s_w[h][t] = w;
-            l += w;
-        }
-        s_ml[h] = make_float2(m, l);
-    }
-    __syncthreads();
-    // this thread's (head, quad) pairs: the near entries' share
-    const int units = g * 32;
-    float4 o[kMaxUnits];
-#pragma unroll
-    for (int i = 0; i < kMaxUnits; ++i) {
-        const int unit = tid + i * kTreeThreads;
-        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (unit < units) {
-            const int quad = idx_div(unit, g), h = unit - quad * g;
-            for (int t = 0; t < near; ++t) {
-                const uint2 y = reinterpret_cast<const uint2 *>(&s_v[t][(quad >> 1) ^ (t & 7)])[quad & 1];
-                const float w = s_w[h][t];
-                o[i].x = fmaf(w, low(y.x), o[i].x);
-                o[i].y = fmaf(w, high(y.x), o[i].y);
-                o[i].z = fmaf(w, low(y.y), o[i].z);
-                o[i].w = fmaf(w, high(y.y), o[i].w);
-            }
-        }
-    }
-    // The parts' results come from the attention grid; all else from before it, which it had
-    // waited for when it let this grid start.
-    grid_dependency_wait();
-    grid_launch_dependents();
-    if (row == 0 && j == 0 && tid == 0) *next = 0u;
-    const long long far = pos + depth + 1 - kMaxPath;       // own entries that lie farther
-    const int n = p.n_parts + (far > 0 ? int((far + kOwnPart - 1) / kOwnPart) : 0);
-    const size_t step0 = (size_t)n_kv * p.tiles * p.tile, step1 = (size_t)n_kv * a.own.n_seq * p.own_slots;
-    const float4 *const values = reinterpret_cast<const float4 *>(opart);
-#pragma unroll
-    for (int i = 0; i < kMaxUnits; ++i) {
-        const int unit = tid + i * kTreeThreads;
-        if (unit >= units) break;
-        const int quad = idx_div(unit, g), h = unit - quad * g;
-        const int v0 = row * g + h, tile0 = idx_div(v0, p.tile), in0 = v0 - tile0 * p.tile;
-        const int v1 = node * g + h, tile1 = idx_div(v1, p.own_tile), in1 = v1 - tile1 * p.own_tile;
-        const size_t slot0 = (size_t)(j * p.tiles + tile0) * p.tile;
-        const size_t slot1 = (size_t)p.own0 + (size_t)(b * n_kv + j) * p.own_slots + (size_t)tile1 * p.own_tile;
-        auto sums = [&](int c) { return ml[c < p.n_parts ? slot0 + c * step0 + in0 : slot1 + (c - p.n_parts) * step1 + in1]; };
-        auto share = [&](int c) {
-            return __ldcs(values + (c < p.n_parts ? (slot0 + c * step0) * 32 + (size_t)quad * p.tile + in0
-                                                  : (slot1 + (c - p.n_parts) * step1) * 32 + (size_t)quad * p.own_tile + in1));
-        };
-        const float2 mine = s_ml[h];
-        float top = mine.x;
-        for (int c = 0; c < n; ++c) top = fmaxf(top, sums(c).x);
-        if (top == -INFINITY) top = 0.f;
-        float l = 0.f;
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto add = [&](float m, float w, const float4 &x) {
-            const float f = ex2_approx((m - top) * kScaleLog2);
-            l = fmaf(w, f, l);
-            sum.x = fmaf(x.x, f, sum.x);
-            sum.y = fmaf(x.y, f, sum.y);
-            sum.z = fmaf(x.z, f, sum.z);
-            sum.w = fmaf(x.w, f, sum.w);
-        };
-        for (int c = 0; c < n; c += kTreeUnroll) {
-            float2 w[kTreeUnroll];
-            float4 x[kTreeUnroll];
-#pragma unroll
-            for (int u = 0; u < kTreeUnroll; ++u)
-                if (c + u < n) {
-                    w[u] = sums(c + u);
-                    x[u] = share(c + u);
-                }
-#pragma unroll
-            for (int u = 0; u < kTreeUnroll; ++u)
-                if (c + u < n) add(w[u].x, w[u].y, x[u]);
-        }
-        add(mine.x, mine.y, o[i]);
-        auto pair = [&](float e0, float e1) {
-            const __nv_bfloat162 r = __floats2bfloat162_rn(__fdiv_rn(e0, l), __fdiv_rn(e1, l));
-            return *reinterpret_cast<const uint32_t *>(&r);
-        };
-        // the queries' place in shared memory takes the outputs: every thread is past its scores
-        reinterpret_cast<uint2 *>(&s_q[h][(quad >> 1) ^ (h & 7)])[quad & 1] = make_uint2(pair(sum.x, sum.y), pair(sum.z, sum.w));
-    }
-    __syncthreads();
-    for (int i = tid; i < g * 16; i += kTreeThreads)
-        *reinterpret_cast<uint4 *>(a.out + (size_t)row * a.ldo + (size_t)j * g * kHeadDim + 8 * i) = s_q[i >> 4][(i & 15) ^ (i >> 4 & 7)];
-}
-
 // Innermost first: an entry's 128 elements, entries, (sequence, head).  The cache
 // is stored with its 16-byte chunks already permuted by position, as the
 // 128-byte swizzle wants them in shared memory, so the copy permutes nothing.
@@ -1255,69 +1024,47 @@ size_t attn_batch_bytes(const KvBatch &own, int prefix_len, int group, int R) {
     return kResultsAt + size_t(p.slots) * (kHeadDim * sizeof(float) + sizeof(float2));
 }
 
-namespace {
-
-// The attention kernel's launch, common to chains and trees; fills in k.
-template <bool TREE>
-cudaError_t launch_items(const AttnBatchArgs &a, KernelArgs *k, cudaStream_t s, const char **why) {
+cudaError_t launch_attn_batch(const AttnBatchArgs &a, cudaStream_t s, const char **why) {
     static std::atomic<bool> opted_in[kMaxDevices] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices || !opted_in[dev]) {
-        e = cudaFuncSetAttribute(attn_batch_kernel<false, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(attn_batch_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  int(kSmemBytes<false>));
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(attn_batch_kernel<true, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            e = cudaFuncSetAttribute(attn_batch_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      int(kSmemBytes<true>));
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < kMaxDevices) opted_in[dev] = true;
     }
-    k->a = a;
-    k->p = plan_of(a.own, a.prefix_len, a.group, a.R);
+    KernelArgs k{};
+    k.a = a;
+    k.p = plan_of(a.own, a.prefix_len, a.group, a.R);
     char *base = static_cast<char *>(a.ws);
-    k->next = reinterpret_cast<unsigned *>(base + kCounterAt);
-    k->opart = reinterpret_cast<float *>(base + kResultsAt);
-    k->ml = reinterpret_cast<float2 *>(base + kResultsAt + size_t(k->p.slots) * kHeadDim * sizeof(float));
+    k.next = reinterpret_cast<unsigned *>(base + kCounterAt);
+    k.opart = reinterpret_cast<float *>(base + kResultsAt);
+    k.ml = reinterpret_cast<float2 *>(base + kResultsAt + size_t(k.p.slots) * kHeadDim * sizeof(float));
     const bool e4m3 = a.own.format == kKvE4m3;
-    if (!encode_queries(&k->map[4], a, why)) return cudaErrorInvalidValue;
+    if (!encode_queries(&k.map[4], a, why)) return cudaErrorInvalidValue;
     if (!e4m3) {
         const KvBatch &pre = a.prefix_len > 0 ? a.prefix : a.own;
         const int pre_rows = a.prefix_len > 0 ? a.prefix_len : a.own.max_len;
-        if (!encode_cache(&k->map[0], pre.k, pre_rows, pre.max_len, pre.n_kv, why) ||
-            !encode_cache(&k->map[1], pre.v, pre_rows, pre.max_len, pre.n_kv, why) ||
-            !encode_cache(&k->map[2], a.own.k, a.own.max_len, a.own.max_len, a.own.n_seq * a.own.n_kv, why) ||
-            !encode_cache(&k->map[3], a.own.v, a.own.max_len, a.own.max_len, a.own.n_seq * a.own.n_kv, why))
+        if (!encode_cache(&k.map[0], pre.k, pre_rows, pre.max_len, pre.n_kv, why) ||
+            !encode_cache(&k.map[1], pre.v, pre_rows, pre.max_len, pre.n_kv, why) ||
+            !encode_cache(&k.map[2], a.own.k, a.own.max_len, a.own.max_len, a.own.n_seq * a.own.n_kv, why) ||
+            !encode_cache(&k.map[3], a.own.v, a.own.max_len, a.own.max_len, a.own.n_seq * a.own.n_kv, why))
             return cudaErrorInvalidValue;
     }
-    const long long items = (long long)a.own.n_kv * ((long long)k->p.n_parts * k->p.pairs +
-                                                     (long long)a.own.n_seq * k->p.own_parts_max * k->p.own_pairs);
+    const long long items = (long long)a.own.n_kv * ((long long)k.p.n_parts * k.p.pairs +
+                                                     (long long)a.own.n_seq * k.p.own_parts_max);
     const int sms = device_sm_count();
     const dim3 grid(unsigned(items < sms ? items : sms));
-    return e4m3 ? launch_pdl(attn_batch_kernel<true, TREE>, grid, dim3(Form<true>::threads), kSmemBytes<true>, s, *k)
-                : launch_pdl(attn_batch_kernel<false, TREE>, grid, dim3(Form<false>::threads), kSmemBytes<false>, s, *k);
-}
-
-}  // namespace
-
-cudaError_t launch_attn_batch(const AttnBatchArgs &a, cudaStream_t s, const char **why) {
-    KernelArgs k{};
-    const cudaError_t e = launch_items<false>(a, &k, s, why);
+    e = e4m3 ? launch_pdl(attn_batch_kernel<true>, grid, dim3(Form<true>::threads), kSmemBytes<true>, s, k)
+             : launch_pdl(attn_batch_kernel<false>, grid, dim3(Form<false>::threads), kSmemBytes<false>, s, k);
     if (e != cudaSuccess) return e;
     return launch_pdl(attn_batch_join_kernel, dim3((k.p.n_vec + 31) / 32, a.own.n_kv, 16), dim3(kJoinThreads), 0, s, a, k.p,
                       (const float *)k.opart, (const float2 *)k.ml, k.next);
-}
-
-cudaError_t launch_attn_tree(const AttnBatchArgs &a, cudaStream_t s, const char **why) {
-    KernelArgs k{};
-    const cudaError_t e = launch_items<true>(a, &k, s, why);
-    if (e != cudaSuccess) return e;
-    const dim3 grid(a.own.n_seq * a.R, a.own.n_kv);
-    return a.own.format == kKvE4m3
-               ? launch_pdl(attn_tree_join_kernel<true>, grid, dim3(kTreeThreads), 0, s, a, k.p, (const float *)k.opart,
-                            (const float2 *)k.ml, k.next)
-               : launch_pdl(attn_tree_join_kernel<false>, grid, dim3(kTreeThreads), 0, s, a, k.p, (const float *)k.opart,
-                            (const float2 *)k.ml, k.next);
 }
 
 }  // namespace tfk

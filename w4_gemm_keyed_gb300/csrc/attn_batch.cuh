@@ -1,5 +1,5 @@
-// Attention of a batch of sequences over a shared prefix and their own caches, in
-// chains of rows or in trees: declarations.
+// Attention of a batch of sequences over a shared prefix and their own caches:
+// declarations.
 #pragma once
 #include "kv_batch.cuh"
 
@@ -12,7 +12,6 @@ struct AttnBatchArgs {
     const uint16_t *q;      // bf16 [n_seq * R][ldq]
     int ldq;
     const int64_t *pos;     // [n_seq]
-    const int32_t *parents; // [n_seq][R]: a tree's (launch_attn_tree)
     uint16_t *out;          // bf16 [n_seq * R][ldo]
     int ldo;
     int *err;
@@ -22,7 +21,5 @@ struct AttnBatchArgs {
 size_t attn_batch_bytes(const KvBatch &own, int prefix_len, int group, int R);
 // *why is set where the failure is not a CUDA call's.
 cudaError_t launch_attn_batch(const AttnBatchArgs &a, cudaStream_t s, const char **why);
-// Rows are nodes of a tree per sequence (tree.cuh), R of them.
-cudaError_t launch_attn_tree(const AttnBatchArgs &a, cudaStream_t s, const char **why);
 
 }  // namespace tfk

@@ -1,0 +1,920 @@
+// Attention of trees of drafted tokens over a shared prefix, their sequences' own entries
+// and their paths.
+//
+// Node i of sequence b (depth d, position pos[b] + d) attends over the prefix's entries
+// 0 .. P - 1, its sequence's own entries 0 .. pos[b] - 1 and those of its path's nodes:
+//   s_t = q . k_t / sqrt(128),  o = sum_t e^(s_t - m) v_t / sum_t e^(s_t - m).
+//
+// A node's bits must not tell whether an ancestor is a node of this pass or was
+// committed before.  So the entries at its last kMaxPath own positions, every node of its path among
+// them, are "near": they are folded in path order and in fp32.  The others, all of them
+// before the root, are "far" and lie on a fixed grid of parts:
+// kOwnPart own entries, or of the prefix a length that P and the number of KV heads
+// fix.  A far part is folded by the flow of attn_flow.cuh, each vector for itself, and its result stored (maximum m,
+// weight sum l, unnormalised output o, fp32); a second kernel works on the near entries and adds up all parts in ascending
+// order, the near ones last.  So bits depend on a node's query, position, P and the entries that it sees.
+#include <atomic>
+
+#include "attn_flow.cuh"
+#include "attn_tree.cuh"
+#include "tree.cuh"
+#include "w4_gemm.cuh"
+
+namespace tfk {
+
+namespace {
+
+using namespace flow;
+
+constexpr int kOwnPart = 320;           // own entries per part
+constexpr int kMinPrefixPart = 320;     // shared entries per part, at least
+constexpr int kPrefixItems = 76;        // of a batch that is one pair of tiles, about
+constexpr int kExpandPairs = 2;         // pairs of query tiles from which on an E4M3 prefix is expanded first
+constexpr int kFewJoins = 304;           // CTAs of the sum with all columns below which they take a quarter
+constexpr int kGroups = 256;            // entries of the table of own items
+constexpr int kProducerWarp = 8, kScoreWarp = 9, kOutputWarp = 10, kMendWarp = 11;
+constexpr int kExpandWarp = 12, kExpandWarps = 4;       // E4M3: of K tiles, and as many of V tiles
+constexpr int kRawBytes = kKeys * kHeadDim;
+static_assert(kOwnPart % kKeys == 0 && kMinPrefixPart % kKeys == 0, "whole key tiles");
+
+// What the cache's format changes: an E4M3 tile (10 KB and 80 scale bytes) is copied into a raw
+// stage and expanded into a bf16 tile by four more warps for K and four for V, so the products are those of a
+// bf16 cache holding the same values.  Where many items read it, the prefix is expanded into the workspace first.
+template <bool E4M3>
+struct Form {
+    static constexpr int stages = E4M3 ? 2 : 3;         // bf16 K tiles, and V tiles, in shared memory
+    static constexpr int queries = 3;                   // query tiles
+    static constexpr int raw = E4M3 ? 2 : 0;            // E4M3 K tiles, and V tiles, on their way
+    static constexpr int threads = E4M3 ? 640 : 384;
+    static constexpr int readers = kSoftmaxWarps + 2 + (E4M3 ? 2 * kExpandWarps : 0);   // of the item ring
+    // registers a thread: the softmax warps' and the others', together no more than the launch's
+    static constexpr int regs_softmax = E4M3 ? 168 : 200, regs_other = E4M3 ? 48 : 104;
+    static_assert(256 * regs_softmax + (threads - 256) * regs_other <= threads * (E4M3 ? 96 : 168), "register split");
+};
+
+struct Item : ItemBase {
+    int j, b;           // KV head, sequence (-1: prefix)
+    int row0, key0;     // first row, first entry
+    int lim0;           // last entry of the item that a root sees (own), n_keys - 1 (prefix)
+    int block;          // of its results: (slot, KV head)
+};
+
+// Results: values [slot][n_kv][32 quads of columns][vectors][4], so that the 32 vectors of a warp store and load
+// 512 consecutive bytes (with a vector's 128 values side by side, 32 bytes a thread, an item of 5 x 24 nodes took
+// 15 us, 12 of them for its stores), and maxima and sums [slot][n_kv][vectors].  Slots: the prefix's parts, then own ones.
+struct Plan {
+    int rows, rows_tile;        // of the batch; of a tile of query vectors
+    int pairs, own_pairs;       // items over all rows, and over a sequence's
+    int part, n_parts;          // the prefix's parts: length and number
+    int own_parts_max;
+    int expanded;               // whether an E4M3 prefix is expanded into the workspace first
+};
+
+__host__ __device__ inline int prefix_part(int prefix_len, int n_kv) {
+    const int parts = kPrefixItems / n_kv > 0 ? kPrefixItems / n_kv : 1, even = (prefix_len - 1) / parts + 1;
+    const long long part = ((long long)even + kKeys - 1) / kKeys * kKeys;
+    return int(part < kMinPrefixPart ? kMinPrefixPart : (part > 0x7FFFFFFF ? 0x7FFFFFFF / kKeys * kKeys : part));
+}
+
+Plan plan_of(const KvBatch &own, int prefix_len, int group, int n) {
+    Plan p;
+    p.rows = own.n_seq * n;
+    p.rows_tile = kTile / group;
+    p.pairs = (p.rows + 2 * p.rows_tile - 1) / (2 * p.rows_tile);
+    p.own_pairs = (n + 2 * p.rows_tile - 1) / (2 * p.rows_tile);
+    p.part = prefix_len > 0 ? prefix_part(prefix_len, own.n_kv) : kMinPrefixPart;
+    p.n_parts = prefix_len > 0 ? (prefix_len - 1) / p.part + 1 : 0;
+    p.own_parts_max = (own.max_len + kOwnPart - 1) / kOwnPart;
+    p.expanded = own.format == kKvE4m3 && prefix_len > 0 && p.pairs >= kExpandPairs;
+    return p;
+}
+
+// Entries of a head of the expanded prefix, and its bytes (K and V).
+inline int expanded_len(int prefix_len) { return (prefix_len + 7) & ~7; }
+size_t expanded_bytes(const Plan &p, int prefix_len, int n_kv) {
+    return p.expanded ? size_t(4) * expanded_len(prefix_len) * n_kv * kHeadDim : 0;
+}
+
+long long slots_of(const Plan &p, int n_kv, int group) {
+    return (long long)(p.n_parts + p.own_parts_max) * n_kv * p.rows * group;
+}
+
+struct KernelArgs {
+    CUtensorMap map[5];     // prefix K, V; own K, V (bf16 caches); queries
+    AttnTreeArgs a;
+    Plan p;
+    float *values;          // [slots][128]
+    float2 *ml;             // [slots]: (maximum score, weight sum)
+    unsigned *next;         // items taken beyond the first of each CTA; zero between calls
+};
+
+template <bool E4M3>
+struct __align__(16) Shared : SharedBase<Item, Form<E4M3>::stages, Form<E4M3>::stages, Form<E4M3>::queries> {
+    uint64_t raw_full[2][2], raw_empty[2][2];   // K, V
+    unsigned before[kGroups + 1];       // own items of the sequence groups before each
+    int8_t depth[kRing][kMaxNodes];     // of an own item's nodes
+};
+// query tiles, bf16 stages, raw stages, their scales, then Shared
+template <bool E4M3>
+constexpr size_t kSmemBytes = size_t(Form<E4M3>::queries) * kTileBytes + size_t(2 * Form<E4M3>::stages) * kKeyBytes +
+                              size_t(2 * Form<E4M3>::raw) * (kRawBytes + kTile) + sizeof(Shared<E4M3>);
+static_assert(kSmemBytes<false> <= 227 * 1024 && kSmemBytes<true> <= 227 * 1024, "shared memory");
+
+// Two parts' factors in their sum, and its maximum.
+struct Factors {
+    float top, a, b;
+};
+__device__ __forceinline__ Factors factors(float ma, float mb) {
+    const float top = fmaxf(ma, mb), t = top == -INFINITY ? 0.f : top;
+    return {top, ex2_approx((ma - t) * kScaleLog2), ex2_approx((mb - t) * kScaleLog2)};
+}
+__device__ __forceinline__ float fold(const Factors &f, float x, float y) { return fmaf(y, f.b, __fmul_rn(x, f.a)); }
+
+__device__ __forceinline__ float4 fold(const Factors &f, const float4 &x, const float4 &y) {
+    return make_float4(fold(f, x.x, y.x), fold(f, x.y, y.y), fold(f, x.z, y.z), fold(f, x.w, y.w));
+}
+
+// ------------------------------------------------------------------ item order
+// The prefix's parts first (the longest), pairs of tiles fastest so that the CTAs
+// working on one part read it from L2; then own parts, heads fastest.
+__device__ int own_items(const KernelArgs &k, int b, bool report) {     // a head's, over the entries before the root
+    const long long p = seq_position(k.a.pos, b, k.a.n, k.a.own.max_len, k.a.err, report);
+    return p < 0 ? 0 : int((p + kOwnPart - 1) / kOwnPart) * k.p.own_pairs;
+}
+
+__device__ Item item_of(const KernelArgs &k, const unsigned *before, unsigned i, int group_seqs) {
+    Item it{};
+    const unsigned n_kv = k.a.own.n_kv, pairs = k.p.pairs;
+    const unsigned n_prefix = k.p.n_parts * n_kv * pairs;
+    if (i < n_prefix) {
+        it.block = idx_div(i, pairs);
+        const int c = idx_div(it.block, n_kv);
+        it.j = it.block - c * n_kv;
+        it.b = -1;
+        it.row0 = (i - it.block * pairs) * 2 * k.p.rows_tile;
+        it.n_rows = min(2 * k.p.rows_tile, k.p.rows - it.row0);
+        it.key0 = c * k.p.part;
+        it.n_keys = min(k.p.part, k.a.prefix_len - it.key0);
+        it.lim0 = it.n_keys - 1;
+        return it;
+    }
+    i -= n_prefix;
+    const int n_groups = (k.a.own.n_seq + group_seqs - 1) / group_seqs;
+    if (i >= before[n_groups] * n_kv) return it;
+    int u = idx_div(i, n_kv);
+    it.j = i - u * n_kv;
+    int lo = 0, hi = n_groups - 1;      // last group whose items start at or before u
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (before[mid] <= unsigned(u))
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    u -= before[lo];
+    int b = lo * group_seqs;
+    for (int n; u >= (n = own_items(k, b, false)); ++b) u -= n;
+    const long long p = k.a.pos[b];
+    const int c = idx_div(u, k.p.own_pairs), first = (u - c * k.p.own_pairs) * 2 * k.p.rows_tile;
+    it.block = (k.p.n_parts + c) * n_kv + it.j;
+    it.b = b;
+    it.row0 = b * k.a.n + first;
+    it.n_rows = min(2 * k.p.rows_tile, k.a.n - first);
+    it.key0 = c * kOwnPart;
+    it.n_keys = int(min((long long)kOwnPart, p - it.key0));
+    it.lim0 = int(p - kMaxPath - it.key0);
+    return it;
+}
+
+// ------------------------------------------------------------------ roles, beside those of the flow
+//   warp 8        finds the items and streams their query vectors and K and V tiles by TMA
+//   warps 0-7     also store an item's results
+//   warps 12-19   (E4M3) expand K tiles (12-15) and V tiles
+template <bool E4M3>
+__device__ void produce(const KernelArgs &k, Shared<E4M3> *sh, uint8_t *q_tiles, uint8_t *stages, uint8_t *raw) {
+    using F = Form<E4M3>;
+    const int lane = threadIdx.x & 31, n_seq = k.a.own.n_seq, g = k.a.group;
+    const int group_seqs = (n_seq + kGroups - 1) / kGroups;
+    const int n_groups = (n_seq + group_seqs - 1) / group_seqs;
+    int total = 0;
+    for (int g0 = 0; g0 < n_groups; g0 += 32) {
+        int n = 0;
+        for (int b = (g0 + lane) * group_seqs; b < min(n_seq, (g0 + lane + 1) * group_seqs); ++b)
+            n += own_items(k, b, blockIdx.x == 0);
+        int sum = n;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            if (lane >= o) sum += t;
+        }
+        if (g0 + lane < n_groups) sh->before[g0 + lane] = total + sum - n;
+        total += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    }
+    if (lane == 0) sh->before[n_groups] = total;
+    __syncwarp();
+
+    unsigned i = blockIdx.x;
+    unsigned loaded_k = 0, loaded_v = 0, raw_k = 0, raw_v = 0, queries = 0;     // tiles so far
+    unsigned mended = 0;            // of them V tiles to mend
+    unsigned to_mend = 0;           // bit st: the last tile of V stage st is one
+    constexpr int kRaw = E4M3 ? F::raw : 1;
+    bool ok = true;
+    // One thread.  The stage of a ring's next tile, once it is free.
+    auto room = [&](uint64_t *empty, unsigned n, int stages_of) {
+        const int st = n % stages_of;
+        ok = ok && (n < unsigned(stages_of) || lane_wait(sh, &empty[st], (n / stages_of - 1) & 1));
+        return st;
+    };
+    auto drain = [&](uint64_t *full, unsigned count, int stages_of, unsigned except) {
+        for (unsigned t = count > unsigned(stages_of) ? count - stages_of : 0; t < count; ++t)
+            if (!(except >> (t % stages_of) & 1u)) wait_drained(&full[t % stages_of], (t / stages_of) & 1);
+    };
+    for (unsigned n = 0;; ++n) {
+        const int slot = n % kRing;
+        const Item it = item_of(k, sh->before, i, group_seqs);
+        if (n >= kRing && !warp_wait(sh, &sh->item_empty[slot], (n / kRing - 1) & 1)) break;
+        if (it.n_rows && it.b >= 0) {
+            int d[2];       // of no tree: anything small; what its rows get is not used
+            tree_depths(k.a.parents + (size_t)it.b * k.a.n, k.a.n, d);
+            sh->depth[slot][lane] = int8_t(d[0]);
+            sh->depth[slot][lane + 32] = int8_t(d[1]);
+            __syncwarp();
+        }
+        unsigned taken = 0;
+        if (lane == 0) {
+            if (E4M3 && it.n_rows && it.b >= 0 && loaded_k > 0) {
+                // the last copies into bf16 stages have arrived before others fill these: no prefix part follows an own one
+                drain(sh->k_full, loaded_k, F::stages, 0u);
+                drain(sh->v_full, loaded_v, F::stages, 0u);
+                loaded_k = loaded_v = 0;
+            }
+            sh->item[slot] = it;
+            sh->bad[slot] = 0;
+            mbar_arrive(&sh->item_full[slot]);
+            if (it.n_rows) taken = atomicAdd(k.next, 1u);       // the item after this one
+        }
+        if (it.n_rows == 0) break;
+        if (lane == 0) {
+            const bool own = it.b >= 0;
+            const int tiles = (it.n_keys + kKeys - 1) / kKeys, outer = own ? it.b * k.a.own.n_kv + it.j : it.j;
+            // A tile of queries is whole rows of the KV head's query heads, one box of (64
+            // elements, heads, rows) per half.  Rows of the box past the item's
+            // fill vectors that nothing reads: rows of a product never mix.
+            for (int t = 0; t < 2 && t * k.p.rows_tile < it.n_rows; ++t) {
+                const int buf = room(sh->q_empty, queries, F::queries);
+                if (!ok) break;
+                ++queries;
+                const int row = it.row0 + t * k.p.rows_tile;
+                mbar_arrive_expect_tx(&sh->q_full[buf], 2 * uint32_t(k.p.rows_tile * g) * 128u);
+                tma_load_3d(q_tiles + buf * kTileBytes, &k.map[4], 0, it.j * g, row, &sh->q_full[buf]);
+                tma_load_3d(q_tiles + buf * kTileBytes + kHalfBytes, &k.map[4], 64, it.j * g, row, &sh->q_full[buf]);
+            }
+            // one tile of entries key0 + key ..
+            auto load = [&](bool is_v, int key) {
+                const int row = it.key0 + key;
+                if (E4M3 && (own || !k.p.expanded)) {
+                    unsigned &loaded = is_v ? raw_v : raw_k;
+                    const int st = room(sh->raw_empty[is_v], loaded, kRaw), at = (is_v ? kRaw : 0) + st;
+                    if (!ok) return;
+                    ++loaded;
+                    const KvBatch &cache = own ? k.a.own : k.a.prefix;
+                    const uint32_t rows = uint32_t(min(kKeys, it.n_keys - key)), scales = (rows + 15u) & ~15u;
+                    const size_t entry = (size_t)outer * cache.max_len + (size_t)row;
+                    uint64_t *bar = &sh->raw_full[is_v][st];
+                    mbar_arrive_expect_tx(bar, rows * kHeadDim + scales);
+                    bulk_g2s(raw + size_t(at) * kRawBytes,
+                             static_cast<const uint8_t *>(is_v ? cache.v : cache.k) + entry * kHeadDim, rows * kHeadDim, bar);
+                    bulk_g2s(raw + size_t(2 * kRaw) * kRawBytes + at * kTile, (is_v ? cache.v_scale : cache.k_scale) + entry,
+                             scales, bar);
+                } else {
+                    unsigned &loaded = is_v ? loaded_v : loaded_k;
+                    const int st = room(is_v ? sh->v_empty : sh->k_empty, loaded, F::stages);
+                    if (!ok) return;
+                    ++loaded;
+                    uint64_t *bar = is_v ? &sh->v_full[st] : &sh->k_full[st];
+                    uint8_t *dst = stages + size_t(is_v ? F::stages + st : st) * kKeyBytes;
+                    if (is_v && !E4M3) {
+                        to_mend &= ~(1u << st);
+                        const int first = max(0, it.lim0 + 1 - key);
+                        if (own && first < kKeys) {     // past the last entry that every node sees: handed over by the mender
+                            const int m = mended++ % kMends;
+                            sh->mend[m] = {st, slot, first, min(kKeys, it.n_keys - key)};
+                            to_mend |= 1u << st;
+                            bar = &sh->mend_full[m];
+                        }
+                    }
+                    const CUtensorMap *map = &k.map[(own ? 2 : 0) + (is_v ? 1 : 0)];
+                    mbar_arrive_expect_tx(bar, kKeyBytes);
+                    tma_load_3d(dst, map, 0, row, outer, bar);
+                    tma_load_3d(dst + kKeyHalf, map, 64, row, outer, bar);
+                    if (E4M3)       // the arrivals of the warps that expand other tiles
+                        for (int w = 1; w < kExpandWarps; ++w) mbar_arrive(bar);
+                }
+            };
+            for (int t = 0; t <= tiles && ok; ++t) {        // K(0), then K(t) and V(t - 1)
+                if (t < tiles) load(false, t * kKeys);
+                if (t > 0 && ok) load(true, (t - 1) * kKeys);
+            }
+        }
+        __syncwarp();
+        if (!__shfl_sync(0xFFFFFFFFu, int(ok), 0)) break;
+        i = gridDim.x + __shfl_sync(0xFFFFFFFFu, taken, 0);
+    }
+    if (lane != 0) return;
+    // no copy outlives the CTA
+    if constexpr (E4M3) {
+        drain(sh->raw_full[0], raw_k, kRaw, 0u);
+        drain(sh->raw_full[1], raw_v, kRaw, 0u);
+    } else {
+        drain(sh->mend_full, mended, kMends, 0u);
+        sh->mend[mended % kMends].stage = -1;
+        mbar_arrive(&sh->mend_full[mended % kMends]);
+    }
+    drain(sh->k_full, loaded_k, F::stages, 0u);
+    drain(sh->v_full, loaded_v, F::stages, to_mend);
+    drain(sh->q_full, queries, F::queries, 0u);
+}
+
+// E4M3 tiles -> bf16 tiles, eight lanes an entry.  Rows of a V tile past the
+// part's last entry become zeros up to the 16-row step the product reads, and so
+// do entries marked NaN that some nodes do not see (0 * NaN would reach those;
+// the nodes that see them get the NaN back when the result is stored).
+template <bool IS_V>
+__device__ void expand_tiles(const KernelArgs &k, Shared<true> *sh, uint8_t *tiles_out, const uint8_t *raw) {
+    using F = Form<true>;
+    constexpr int kRows = 4 * kExpandWarps, kSteps = kKeys / kRows;    // rows all warps take at a time
+    static_assert(kRows % 8 == 0 && kKeys % kRows == 0, "a thread's rows share their place in the swizzle");
+    const int lane = threadIdx.x & 31, tid = threadIdx.x - 32 * (kExpandWarp + (IS_V ? kExpandWarps : 0)), group = tid & 7, row0 = tid >> 3;
+    const uint8_t *scales = raw + size_t(2 * F::raw) * kRawBytes + (IS_V ? F::raw * kTile : 0);
+    raw += IS_V ? F::raw * kRawBytes : 0;
+    uint64_t *const raw_full = sh->raw_full[IS_V], *const raw_empty = sh->raw_empty[IS_V];
+    uint64_t *const full = IS_V ? sh->v_full : sh->k_full, *const empty = IS_V ? sh->v_empty : sh->k_empty;
+    Ring<F::raw> from;
+    Ring<F::stages> to;
+    to.parity = 1u;     // of a fresh barrier, the phase before the first counts as over
+    for (unsigned n = 0;; ++n) {
+        const int slot = n % kRing;
+        if (!warp_wait(sh, &sh->item_full[slot], (n / kRing) & 1)) return;
+        const int n_rows = sh->item[slot].n_rows, n_keys = sh->item[slot].n_keys, lim0 = sh->item[slot].lim0;
+        if (n_rows == 0) return;
+        const int tiles = (n_keys + kKeys - 1) / kKeys;
+        if (k.p.expanded && sh->item[slot].b < 0) {
+            // Copied as bf16: the ring's places pass by.  When the first own item is known, all of its
+            // stage's uses but the last are over (the last copy's producer had waited for that).
+            to.step(tiles);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
+            continue;
+        }
+        for (int t = 0; t < tiles; ++t) {
+            const int key = t * kKeys, valid = min(kKeys, n_keys - key);
+            const int fill = IS_V ? (valid + 15) & ~15 : valid, hidden = lim0 + 1 - key;
+            if (!warp_wait(sh, &raw_full[from.at], from.parity)) return;
+            if (!warp_wait(sh, &empty[to.at], to.parity)) return;
+            const uint8_t *src = raw + size_t(from.at) * kRawBytes + row0 * kHeadDim + 16 * group;
+            const uint8_t *sc = scales + from.at * kTile + row0;
+            uint8_t *dst = tiles_out + size_t(to.at) * kKeyBytes + row0 * 128 + ((group ^ (row0 & 7)) << 4);
+            const bool whole = valid == kKeys && !(IS_V && hidden < kKeys);     // nothing to leave out
+            uint4 w[kSteps];
+            uint32_t f[kSteps];
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                w[i] = *reinterpret_cast<const uint4 *>(src + i * kRows * kHeadDim);
+                f[i] = sc[i * kRows];
+            }
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int row = row0 + i * kRows;
+                if (!whole) {
+                    if (row >= fill) break;
+                    if (row >= valid || (IS_V && f[i] == uint32_t(kScaleNan) && row >= hidden)) {
+                        if (row < valid) *reinterpret_cast<volatile int *>(&sh->bad[slot]) = 1;
+                        w[i] = make_uint4(0u, 0u, 0u, 0u);
+                        f[i] = 0u;
+                    }
+                }
+                const uint32_t factor = e4m3_factor(f[i]);
+                uint4 lo, hi;
+                e4m3_expand(w[i].x, factor, lo.x, lo.y);
+                e4m3_expand(w[i].y, factor, lo.z, lo.w);
+                e4m3_expand(w[i].z, factor, hi.x, hi.y);
+                e4m3_expand(w[i].w, factor, hi.z, hi.w);
+                *reinterpret_cast<uint4 *>(dst + i * kRows * 128) = lo;
+                *reinterpret_cast<uint4 *>(dst + i * kRows * 128 + kKeyHalf) = hi;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&full[to.at]);
+                mbar_arrive(&raw_empty[from.at]);
+            }
+            from.step();
+            to.step();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
+    }
+}
+
+// Nodes that see an own entry with non-finite values get them back: they had been left out of the
+// product.  out: a stored result, its quads `step` apart; first .. last: the item's entries in question.
+template <bool E4M3>
+__device__ __noinline__ void add_nonfinite(const AttnTreeArgs &a, int b, int j, int key0, int first, int last, float4 *out,
+                                           size_t step) {
+    const size_t base = (size_t)(b * a.own.n_kv + j) * a.own.max_len + (size_t)key0;
+    for (int d = 0; d < kHeadDim; ++d) {
+        float x = 0.f;
+        for (int t = first; t <= last; ++t) {
+            const size_t entry = base + t;
+            if constexpr (E4M3) {
+                if (a.own.v_scale[entry] == kScaleNan) x = __uint_as_float(0x7FC00000u);
+            } else {
+                const uint16_t v =
+                    static_cast<const uint16_t *>(a.own.v)[entry * kHeadDim + 8 * ((d >> 3) ^ int(entry & 7)) + (d & 7)];
+                if ((v & 0x7F80u) == 0x7F80u) x += __uint_as_float(uint32_t(v) << 16);
+            }
+        }
+        if (x != 0.f) reinterpret_cast<float *>(out + (d >> 2) * step)[d & 3] += x;
+    }
+}
+
+// The last entry of the item that a row's node sees.
+template <typename SHARED>
+__device__ __forceinline__ int last_seen(const SHARED *sh, const KernelArgs &k, int slot, const Item &it, int row) {
+    return it.b < 0 ? it.lim0 : it.lim0 + sh->depth[slot][it.row0 + row - it.b * k.a.n];
+}
+
+// An item's results, by the warps of its softmax: a thread per vector.
+template <bool E4M3>
+__device__ bool store_results(const KernelArgs &k, Shared<E4M3> *sh, uint32_t tmem, int slot, int t, int n_here, float m,
+                              float l, unsigned steps) {
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, v = 32 * quarter + lane;
+    const int g = k.a.group, my_row = v / g, n_vec = k.p.rows * g;
+    if (!warp_wait(sh, &sh->o_done[t], (steps - 1) & 1)) return false;
+    if (32 * quarter < n_here * g) {
+        tc_fence_after();
+        const uint32_t t_o = tmem + kTmemO + t * kHeadDim + (uint32_t(32 * quarter) << 16);
+        const Item &it = sh->item[slot];
+        const bool mine = my_row < n_here;
+        const size_t block = it.block;
+        const int at = (it.row0 + t * k.p.rows_tile) * g + v;
+        float4 *const out = reinterpret_cast<float4 *>(k.values) + block * 32 * n_vec + at;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tc_ld32(t_o + 32 * c, o);
+            tc_wait_ld();
+            tc_pin32(o);
+            if (c == 3) {       // the next item's products may begin
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->o_free[t]);
+            }
+            if (mine) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    out[(size_t)(8 * c + e) * n_vec] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                                   __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+            }
+        }
+        if (mine) {
+            k.ml[block * n_vec + at] = make_float2(m, l);
+            if (*reinterpret_cast<volatile int *>(&sh->bad[slot]) != 0)
+                add_nonfinite<E4M3>(k.a, it.b, it.j, it.key0, max(0, it.lim0 + 1),
+                                    min(it.n_keys - 1, last_seen(sh, k, slot, it, t * k.p.rows_tile + my_row)), out, n_vec);
+        }
+    } else {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->o_free[t]);
+    }
+    return true;
+}
+
+template <bool E4M3>
+__global__ void __launch_bounds__(Form<E4M3>::threads, 1) attn_tree_kernel(const __grid_constant__ KernelArgs k) {
+    using F = Form<E4M3>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *q_tiles = smem, *stages = smem + F::queries * kTileBytes, *raw = stages + size_t(2 * F::stages) * kKeyBytes;
+    uint8_t *const v_tiles = stages + size_t(F::stages) * kKeyBytes;
+    Shared<E4M3> *sh = reinterpret_cast<Shared<E4M3> *>(raw + size_t(2 * F::raw) * (kRawBytes + kTile));
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        sh->init(E4M3 ? kExpandWarps : 1, F::readers, 4);
+        for (int i = 0; i < 2 * F::raw; ++i) {
+            mbar_init(&sh->raw_full[i & 1][i >> 1], 1);
+            mbar_init(&sh->raw_empty[i & 1][i >> 1], kExpandWarps);
+        }
+        fence_mbar_init();
+    }
+    if (warp == kScoreWarp) tc_alloc(&sh->tmem, kTmemCols);
+    if (warp == kProducerWarp && (threadIdx.x & 31) < 5 && (!E4M3 || (threadIdx.x & 31) == 4 || (k.p.expanded && (threadIdx.x & 31) < 2)))
+        prefetch_tensormap(&k.map[threadIdx.x & 31]);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh->tmem;
+    grid_dependency_wait();     // queries, positions, parents and entries come from the preceding grids
+    grid_launch_dependents();
+    if (warp < kSoftmaxWarps) {
+        regs_raise<F::regs_softmax>();
+        const auto sight = [&](int slot, const Item &it, int tile, int n_here, int mine, int, int) {
+            const int last = last_seen(sh, k, slot, it, tile * k.p.rows_tile + min(mine, n_here - 1));
+            if (it.b < 0) return Sight{last, last, last};
+            return Sight{last, __reduce_min_sync(0xFFFFFFFFu, last), __reduce_max_sync(0xFFFFFFFFu, last)};
+        };
+        softmax<true>(sh, k.p.rows_tile, k.a.group, tmem, sight, [&](int slot, int tile, int n_here, float m, float l, unsigned steps) {
+            return store_results<E4M3>(k, sh, tmem, slot, tile, n_here, m, l, steps);
+        });
+    } else {
+        regs_lower<F::regs_other>();
+        if (E4M3 && warp >= kExpandWarp) {
+            if constexpr (E4M3) {
+                if (warp < kExpandWarp + kExpandWarps)
+                    expand_tiles<false>(k, sh, stages, raw);
+                else
+                    expand_tiles<true>(k, sh, v_tiles, raw);
+            }
+        } else if (warp == kProducerWarp) {
+            produce<E4M3>(k, sh, q_tiles, stages, raw);
+        } else if (warp == kMendWarp) {
+            if constexpr (!E4M3) mend_tiles(sh, v_tiles);
+        } else if (elect_one()) {
+            if (warp == kScoreWarp)
+                issue_scores(sh, k.p.rows_tile, q_tiles, stages, tmem);
+            else
+                issue_outputs(sh, k.p.rows_tile, v_tiles, tmem);
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (threadIdx.x == 0 && sh->abort) set_error(k.a.err, kDevTimeout);
+    if (warp == kScoreWarp) tc_dealloc(tmem, kTmemCols);
+}
+
+// ------------------------------------------------------------------ an E4M3 prefix as bf16
+// Eight lanes an entry, entries in the layout of a bf16 cache.  HBM bounds it: 129 bytes read and 256 written.
+constexpr int kExpandEntries = 128;     // a CTA's
+
+__global__ void __launch_bounds__(256) expand_prefix_kernel(KvBatch c, int len, int out_len, uint4 *k_out, uint4 *v_out) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int group = threadIdx.x & 7, row0 = blockIdx.x * kExpandEntries + (threadIdx.x >> 3), j = blockIdx.y;
+    const uint8_t *codes = static_cast<const uint8_t *>(blockIdx.z ? c.v : c.k) + (size_t)j * c.max_len * kHeadDim;
+    const uint8_t *scales = (blockIdx.z ? c.v_scale : c.k_scale) + (size_t)j * c.max_len;
+    uint4 *out = (blockIdx.z ? v_out : k_out) + (size_t)j * out_len * 16;
+    constexpr int kSteps = kExpandEntries / 32;
+    uint4 w[kSteps];
+    uint32_t f[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        const int row = min(row0 + 32 * i, len - 1);
+        w[i] = *reinterpret_cast<const uint4 *>(codes + (size_t)row * kHeadDim + 16 * group);
+        f[i] = scales[row];
+    }
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        const int row = row0 + 32 * i;
+        if (row >= len) break;
+        const uint32_t factor = e4m3_factor(f[i]);
+        uint4 lo, hi;
+        e4m3_expand(w[i].x, factor, lo.x, lo.y);
+        e4m3_expand(w[i].y, factor, lo.z, lo.w);
+        e4m3_expand(w[i].z, factor, hi.x, hi.y);
+        e4m3_expand(w[i].w, factor, hi.z, hi.w);
+        out[(size_t)row * 16 + (group ^ (row & 7))] = lo;
+        out[(size_t)row * 16 + 8 + (group ^ (row & 7))] = hi;
+    }
+}
+
+// ------------------------------------------------------------------ near entries, and the sum
+// A CTA takes up to 32 vectors (whole nodes) of one KV head.  First the near entries, before the
+// attention grid has ended: a warp a node, at most 16 keys in path order, one matrix product (bf16 operands, fp32
+// sums) for the scores of its heads and one for their outputs.  Then the far results are added up, the near ones last:
+// a lane per vector, a warp QUADS quads of columns.  It reads 520 bytes per vector and slot, and nothing else counts where
+// there are many.  With few vectors, the loads that follow one another count: CTAs of a quarter of the columns (which work
+// on the near entries four times) keep four times as many on their way.
+constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps, kJoinVecs = 32;
+constexpr int kNearPitch = kHeadDim + 4;        // floats: lanes that read a quad of consecutive vectors meet no bank twice
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+template <bool E4M3>
+__device__ __forceinline__ uint4 cache_chunk(const void *data, const uint8_t *scale, size_t entry, int c) {   // elements 8c .. 8c + 7
+    uint4 x;
+    if constexpr (E4M3) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(data) + entry * kHeadDim + 16 * (c & 7) +
+                                                         8 * (c >> 3));
+        const uint32_t f = e4m3_factor(scale[entry]);
+        e4m3_expand(w.x, f, x.x, x.y);
+        e4m3_expand(w.y, f, x.z, x.w);
+    } else {
+        x = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(data) + entry * kHeadDim + 8 * (c ^ int(entry & 7)));
+    }
+    return x;
+}
+
+struct __align__(16) JoinShared {
+    float near[kJoinVecs][kNearPitch];      // near outputs; then, as bf16, the rows' outputs
+    float2 ml[kJoinVecs];
+    int depth[kJoinVecs];                   // of the nodes; -1: idle sequence, no tree or unused row
+    uint4 v[kJoinWarps][kMaxPath][16];      // a node's near values, chunk c of row t at c XOR (t % 8)
+};
+
+// One node's near entries; whole warp.  Rows of the products are the group's heads, a lane's are lane / 4 and that + 8.
+template <bool E4M3>
+__device__ void near_entries(const AttnTreeArgs &a, JoinShared *sh, int row, int j, int nth, uint4 (*s_v)[16]) {
+    const int lane = threadIdx.x & 31, g = a.group, r = lane >> 2, c4 = lane & 3;
+    const int b = idx_div(row, a.n), node = row - b * a.n;
+    const long long pos = seq_position(a.pos, b, a.n, a.own.max_len, a.err, false);
+    const int32_t *parents = a.parents + (size_t)b * a.n;
+    int d[2];
+    const bool tree = tree_depths(parents, a.n, d);
+    if (!tree && pos >= 0 && node == 0 && j == 0 && lane == 0) set_error(a.err, kDevBadTree);
+    auto of = [](const int (&v)[2], int i) {
+        const int lo = __shfl_sync(0xFFFFFFFFu, v[0], i & 31), hi = __shfl_sync(0xFFFFFFFFu, v[1], i & 31);
+        return i < 32 ? lo : hi;
+    };
+    const int depth = of(d, node);
+    const bool none = !tree || pos < 0 || depth < 0;
+    if (lane == 0) sh->depth[nth] = none ? -1 : depth;
+    if (none) return;
+    // lane t < near: the entry at own position first + t, of a node `up` steps above where it is one of the path
+    const int near = int(min((long long)kMaxPath, pos + depth + 1));
+    const long long first = pos + depth + 1 - near;
+    int up = max(0, near - 1 - lane), at = node;
+    int above[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int i = lane + 32 * h;
+        above[h] = i < a.n ? max(0, parents[i]) : 0;
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {       // above: 2^s steps
+        const int higher = of(above, at);
+        if (up >> s & 1) at = higher;
+        const int u0 = of(above, above[0]), u1 = of(above, above[1]);
+        above[0] = u0;
+        above[1] = u1;
+    }
+    const long long y = first + lane;
+    const int my_entry = int(y < pos ? y : pos + at);
+    const size_t base = (size_t)(b * a.own.n_kv + j) * a.own.max_len;
+
+    // Queries and keys: a lane's 16-byte chunk 4i + c4 gives four pairs, the operands of two steps of 16 elements; the sums
+    // take the elements in another order than memory has them, the same for both.
+    uint4 q[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            q[h][i] = r + 8 * h < g ? *reinterpret_cast<const uint4 *>(a.q + (size_t)row * a.ldq +
+                                                                       (size_t)(j * g + r + 8 * h) * kHeadDim + 8 * (4 * i + c4))
+                                    : make_uint4(0u, 0u, 0u, 0u);
+    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {       // keys 8n .. 8n + 7, the lane's is 8n + r
+        const size_t e = base + __shfl_sync(0xFFFFFFFFu, my_entry, 8 * n + r);
+        uint4 k[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            k[i] = 8 * n + r < near ? cache_chunk<E4M3>(a.own.k, a.own.k_scale, e, 4 * i + c4) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            mma_bf16(s[n], q[0][i].x, q[1][i].x, q[0][i].y, q[1][i].y, k[i].x, k[i].y);
+            mma_bf16(s[n], q[0][i].z, q[1][i].z, q[0][i].w, q[1][i].w, k[i].z, k[i].w);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kMaxPath / 2; ++i) {
+        const int t = 2 * i + (lane >> 4), c = lane & 15;
+        const size_t e = base + __shfl_sync(0xFFFFFFFFu, my_entry, t);
+        s_v[t][c ^ (t & 7)] = t < near ? cache_chunk<E4M3>(a.own.v, a.own.v_scale, e, c) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    __syncwarp();
+    // weights: s[n][2h + i] is head r + 8h and key 8n + 2 c4 + i
+    uint32_t w[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (8 * n + 2 * c4 + i >= near) s[n][2 * h + i] = -INFINITY;
+                m = fmaxf(m, s[n][2 * h + i]);
+            }
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        const float mc = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const float x = ex2_approx((s[n][2 * h] - mc) * kScaleLog2), z = ex2_approx((s[n][2 * h + 1] - mc) * kScaleLog2);
+            l += x + z;
+            // weights meet V as bf16 (off by at most 2^-8 of each, half a step); the sums keep them whole
+            const __nv_bfloat162 pk = __floats2bfloat162_rn(x, z);
+            w[n][h] = *reinterpret_cast<const uint32_t *>(&pk);
+        }
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
+        if (c4 == 0 && r + 8 * h < g) sh->ml[nth * g + r + 8 * h] = make_float2(m, l);
+    }
+    // outputs, 16 columns at a time
+    const int t = lane & 15;
+    const uint32_t v_row = smem_u32(&s_v[t][0]);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+        uint32_t v[4];      // keys 0-7 and 8-15 of columns 16n .., then of columns 16n + 8 ..
+        ldsm_x4_trans(v_row + 16 * ((2 * n + (lane >> 4)) ^ (t & 7)), v);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float o[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_bf16(o, w[0][0], w[0][1], w[1][0], w[1][1], v[2 * i], v[2 * i + 1]);
+            const int col = 16 * n + 8 * i + 2 * c4;
+            if (r < g) *reinterpret_cast<float2 *>(&sh->near[nth * g + r][col]) = make_float2(o[0], o[1]);
+            if (r + 8 < g) *reinterpret_cast<float2 *>(&sh->near[nth * g + r + 8][col]) = make_float2(o[2], o[3]);
+        }
+    }
+    __syncwarp();       // the next node's values may come
+}
+
+template <bool E4M3, int QUADS>
+__global__ void __launch_bounds__(kJoinThreads, 2) attn_tree_join_kernel(AttnTreeArgs a, Plan p, const float *results,
+                                                                         const float2 *ml, unsigned *next) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    JoinShared *sh = reinterpret_cast<JoinShared *>(smem);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = a.group, j = blockIdx.y, n_kv = a.own.n_kv;
+    const int quad0 = blockIdx.z * (kJoinWarps * QUADS) + warp * QUADS;
+    const int nodes = kJoinVecs / g, row0 = blockIdx.x * nodes, here = min(nodes, p.rows - row0), n_vec = p.rows * g;
+    for (int i = warp; i < here; i += kJoinWarps) near_entries<E4M3>(a, sh, row0 + i, j, i, sh->v[warp]);
+    __syncthreads();
+    // The results come from the attention grid; all else from before it, which it had
+    // waited for when it let this grid start.
+    grid_dependency_wait();
+    grid_launch_dependents();
+    if (blockIdx.x == 0 && j == 0 && blockIdx.z == 0 && threadIdx.x == 0) *next = 0u;
+    const int nth = lane / g, depth = nth < here ? sh->depth[nth] : -1;
+    float4 sum[QUADS];
+    float l = 1.f;
+#pragma unroll
+    for (int i = 0; i < QUADS; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (depth >= 0) {
+        const long long far = a.pos[idx_div(row0 + nth, a.n)] + depth + 1 - kMaxPath;       // own entries that lie farther
+        const int n = p.n_parts + (far > 0 ? int((far + kOwnPart - 1) / kOwnPart) : 0);
+        const int v = row0 * g + lane;
+        const float2 *my_ml = ml + (size_t)j * n_vec + v;
+        const float4 *x = reinterpret_cast<const float4 *>(results) + ((size_t)j * 32 + quad0) * n_vec + v;
+        const size_t step = (size_t)n_kv * n_vec;
+        float m = -INFINITY;
+        l = 0.f;
+        auto add = [&](const float2 &part, const float4 (&y)[QUADS]) {
+            const Factors f = factors(m, part.x);
+            m = f.top;
+            l = fold(f, l, part.y);
+#pragma unroll
+            for (int i = 0; i < QUADS; ++i) sum[i] = fold(f, sum[i], y[i]);
+        };
+        constexpr int kAhead = 16 / QUADS;
+        float2 w[kAhead];
+        float4 y[kAhead][QUADS];
+        auto load = [&](int u) {
+            w[u] = *my_ml;
+#pragma unroll
+            for (int i = 0; i < QUADS; ++i) y[u][i] = __ldcs(x + (size_t)i * n_vec);
+            my_ml += step;
+            x += step * 32;
+        };
+        for (int c = 0; c < n; c += kAhead) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (c + u < n) load(u);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (c + u < n) add(w[u], y[u]);
+        }
+#pragma unroll
+        for (int i = 0; i < QUADS; ++i)
+            y[0][i] = *reinterpret_cast<const float4 *>(&sh->near[lane][4 * (quad0 + i)]);
+        add(sh->ml[lane], y[0]);
+    }
+    __syncthreads();    // the near outputs are read
+    uint16_t *const rows = reinterpret_cast<uint16_t *>(&sh->near[0][0]);
+    constexpr int kPitch = kHeadDim + 8;        // 16-bit elements
+    auto pair = [&](float e0, float e1) {
+        const __nv_bfloat162 r = __floats2bfloat162_rn(__fdiv_rn(e0, l), __fdiv_rn(e1, l));
+        return *reinterpret_cast<const uint32_t *>(&r);
+    };
+#pragma unroll
+    for (int i = 0; i < QUADS; ++i)
+        *reinterpret_cast<uint2 *>(rows + lane * kPitch + 4 * (quad0 + i)) =
+            make_uint2(pair(sum[i].x, sum[i].y), pair(sum[i].z, sum[i].w));
+    __syncthreads();
+    constexpr int kChunks = kJoinWarps * QUADS / 2;     // 16-byte chunks of a vector
+    for (int i = threadIdx.x; i < here * g * kChunks; i += kJoinThreads) {
+        const int v = i / kChunks, c = i % kChunks + blockIdx.z * kChunks, at = v / g;
+        *reinterpret_cast<uint4 *>(a.out + (size_t)(row0 + at) * a.ldo + (size_t)(j * g + v - at * g) * kHeadDim + 8 * c) =
+            *reinterpret_cast<const uint4 *>(rows + v * kPitch + 8 * c);
+    }
+}
+
+// Innermost first: an entry's 128 elements, entries, (sequence, head).  The cache
+// is stored with its 16-byte chunks already permuted by position, as the
+// 128-byte swizzle wants them in shared memory (parts and tiles start at multiples of 8), so the copy
+// permutes nothing.
+bool encode_cache(CUtensorMap *m, const void *base, int rows, int max_len, int outer, const char **why) {
+    return encode_tiles(m, base, {cuuint64_t(kHeadDim), cuuint64_t(rows), cuuint64_t(outer)},
+                        {cuuint64_t(kHeadDim) * 2, cuuint64_t(max_len) * kHeadDim * 2}, {64, kKeys, 1},
+                        CU_TENSOR_MAP_SWIZZLE_NONE, why);
+}
+
+}  // namespace
+
+// Workspace: the status block, whose byte 128 is the item counter, then the lane
+// GEMM's split-K counters, not used here, then the results.  No operator
+// has scratch in the status block, so the counter is zero whatever a workspace
+// was used for before, and a GEMM that uses it next finds its counters as it left them.
+constexpr size_t kCounterAt = 128, kResultsAt = 256 + kCounterBytes;
+
+size_t attn_tree_bytes(const KvBatch &own, int prefix_len, int group, int n) {
+    const Plan p = plan_of(own, prefix_len, group, n);
+    return kResultsAt + size_t(slots_of(p, own.n_kv, group)) * (kHeadDim * sizeof(float) + sizeof(float2)) +
+           expanded_bytes(p, prefix_len, own.n_kv);
+}
+
+template <bool E4M3>
+static cudaError_t launch_form(const AttnTreeArgs &a, KernelArgs &k, cudaStream_t s) {
+    static std::atomic<bool> opted_in[kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices || !opted_in[dev]) {
+        e = cudaFuncSetAttribute(attn_tree_kernel<E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemBytes<E4M3>));
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(attn_tree_join_kernel<E4M3, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(JoinShared)));
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(attn_tree_join_kernel<E4M3, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(JoinShared)));
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < kMaxDevices) opted_in[dev] = true;
+    }
+    const long long jobs = (long long)a.own.n_kv * ((long long)k.p.n_parts * k.p.pairs +
+                                                    (long long)a.own.n_seq * k.p.own_parts_max * k.p.own_pairs);
+    const int sms = device_sm_count();
+    e = launch_pdl(attn_tree_kernel<E4M3>, dim3(unsigned(jobs < sms ? jobs : sms)), dim3(Form<E4M3>::threads), kSmemBytes<E4M3>,
+                   s, k);
+    if (e != cudaSuccess) return e;
+    const int nodes = kJoinVecs / a.group, tiles = (k.p.rows + nodes - 1) / nodes;
+    const bool few = tiles * a.own.n_kv < kFewJoins;
+    return launch_pdl(few ? attn_tree_join_kernel<E4M3, 1> : attn_tree_join_kernel<E4M3, 4>, dim3(tiles, a.own.n_kv, few ? 4 : 1),
+                      dim3(kJoinThreads), sizeof(JoinShared), s, a, k.p, (const float *)k.values, (const float2 *)k.ml, k.next);
+}
+
+cudaError_t launch_attn_tree(const AttnTreeArgs &a, cudaStream_t s, const char **why) {
+    KernelArgs k{};
+    k.a = a;
+    k.p = plan_of(a.own, a.prefix_len, a.group, a.n);
+    char *base = static_cast<char *>(a.ws);
+    k.next = reinterpret_cast<unsigned *>(base + kCounterAt);
+    const size_t slots = size_t(slots_of(k.p, a.own.n_kv, a.group));
+    char *const expanded = base + kResultsAt;
+    const size_t half = expanded_bytes(k.p, a.prefix_len, a.own.n_kv) / 2;
+    k.values = reinterpret_cast<float *>(expanded + 2 * half);
+    k.ml = reinterpret_cast<float2 *>(k.values + slots * kHeadDim);
+    const bool e4m3 = a.own.format == kKvE4m3;
+    if (!encode_tiles(&k.map[4], a.q, {cuuint64_t(kHeadDim), cuuint64_t(a.own.n_kv) * a.group, cuuint64_t(k.p.rows)},
+                      {cuuint64_t(kHeadDim) * 2, cuuint64_t(a.ldq) * 2},
+                      {64, cuuint32_t(a.group), cuuint32_t(k.p.rows_tile)}, CU_TENSOR_MAP_SWIZZLE_128B, why))
+        return cudaErrorInvalidValue;
+    if (!e4m3) {
+        const KvBatch &pre = a.prefix_len > 0 ? a.prefix : a.own;
+        const int pre_rows = a.prefix_len > 0 ? a.prefix_len : a.own.max_len;
+        if (!encode_cache(&k.map[0], pre.k, pre_rows, pre.max_len, pre.n_kv, why) ||
+            !encode_cache(&k.map[1], pre.v, pre_rows, pre.max_len, pre.n_kv, why) ||
+            !encode_cache(&k.map[2], a.own.k, a.own.max_len, a.own.max_len, a.own.n_seq * a.own.n_kv, why) ||
+            !encode_cache(&k.map[3], a.own.v, a.own.max_len, a.own.max_len, a.own.n_seq * a.own.n_kv, why))
+            return cudaErrorInvalidValue;
+    }
+    if (k.p.expanded) {
+        const int len = expanded_len(a.prefix_len);
+        if (!encode_cache(&k.map[0], expanded, a.prefix_len, len, a.own.n_kv, why) ||
+            !encode_cache(&k.map[1], expanded + half, a.prefix_len, len, a.own.n_kv, why))
+            return cudaErrorInvalidValue;
+        const dim3 grid((a.prefix_len + kExpandEntries - 1) / kExpandEntries, a.own.n_kv, 2);
+        const cudaError_t e = launch_pdl(expand_prefix_kernel, grid, dim3(256), 0, s, a.prefix, a.prefix_len, len,
+                                         reinterpret_cast<uint4 *>(expanded), reinterpret_cast<uint4 *>(expanded + half));
+        if (e != cudaSuccess) return e;
+    }
+    return e4m3 ? launch_form<true>(a, k, s) : launch_form<false>(a, k, s);
+}
+
+}  // namespace tfk

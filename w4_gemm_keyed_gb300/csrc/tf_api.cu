@@ -11,6 +11,7 @@
 #include "../../include/tf.h"
 #include "attention.cuh"
 #include "attn_batch.cuh"
+#include "attn_tree.cuh"
 #include "attn_prompt.cuh"
 #include "glue.cuh"
 #include "sampler.cuh"
@@ -1007,7 +1008,7 @@ size_t tf_attention_tree_workspace_bytes(const tf_kv_batch *own, int32_t group, 
     if (!own || own->n_seq < 1 || own->n_seq > TF_MAX_SEQS || own->n_kv < 1 || own->n_kv > 128 || own->max_len <= 0 ||
         own->max_len % kKvPart || !attn_tree_supported(own, group, n, prefix_len))
         return 0;
-    return attn_batch_bytes(kv_batch(*own), prefix_len, group, n);
+    return attn_tree_bytes(kv_batch(*own), prefix_len, group, n);
 }
 
 tf_status tf_attention_tree(const tf_kv_batch *own, const tf_kv_batch *prefix, int32_t prefix_len, int32_t group,
@@ -1020,12 +1021,12 @@ tf_status tf_attention_tree(const tf_kv_batch *own, const tf_kv_batch *prefix, i
     if ((st = check_attention(own, prefix, prefix_len, group, q, ldq, pos, out, ldo)) != TF_OK) return st;
     if (!parents || !aligned(parents, 4)) return fail(TF_ERR_INVALID_ARG, "null or misaligned parents");
     if ((st = check_ws(ws, ws_bytes, tf_attention_tree_workspace_bytes(own, group, n, prefix_len))) != TF_OK) return st;
-    AttnBatchArgs a{};
+    AttnTreeArgs a{};
     a.own = kv_batch(*own);
     if (prefix_len > 0) a.prefix = kv_batch(*prefix);
     a.prefix_len = prefix_len;
     a.group = group;
-    a.R = n;
+    a.n = n;
     a.q = q;
     a.ldq = ldq;
     a.pos = pos;
