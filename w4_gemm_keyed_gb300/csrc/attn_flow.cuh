@@ -115,11 +115,6 @@ struct Ring {
             parity ^= 1u;
         }
     }
-    __device__ void step(int n) {
-        const int rounds = (at + n) / N;
-        at = at + n - rounds * N;
-        parity ^= unsigned(rounds) & 1u;
-    }
 };
 
 // V tiles that hold rows some vectors of the item do not see: rows past the item's

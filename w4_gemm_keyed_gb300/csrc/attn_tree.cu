@@ -29,27 +29,27 @@ using namespace flow;
 constexpr int kOwnPart = 320;           // own entries per part
 constexpr int kMinPrefixPart = 320;     // shared entries per part, at least
 constexpr int kPrefixItems = 76;        // of a batch that is one pair of tiles, about
+constexpr int kSms = 152;
 constexpr int kExpandPairs = 2;         // pairs of query tiles from which on an E4M3 prefix is expanded first
-constexpr int kFewJoins = 304;           // CTAs of the sum with all columns below which they take a quarter
-constexpr int kGroups = 256;            // entries of the table of own items
+constexpr int kGroups = 128;            // entries of the table of own items
 constexpr int kProducerWarp = 8, kScoreWarp = 9, kOutputWarp = 10, kMendWarp = 11;
-constexpr int kExpandWarp = 12, kExpandWarps = 4;       // E4M3: of K tiles, and as many of V tiles
+constexpr int kExpandWarp = 12, kExpandWarps = 4;       // E4M3: for K tiles, and as many for V tiles
 constexpr int kRawBytes = kKeys * kHeadDim;
 static_assert(kOwnPart % kKeys == 0 && kMinPrefixPart % kKeys == 0, "whole key tiles");
 
 // What the cache's format changes: an E4M3 tile (10 KB and 80 scale bytes) is copied into a raw
-// stage and expanded into a bf16 tile by four more warps for K and four for V, so the products are those of a
+// stage and expanded into a bf16 tile by four more warps for K, four for V, so the products are those of a
 // bf16 cache holding the same values.  Where many items read it, the prefix is expanded into the workspace first.
 template <bool E4M3>
 struct Form {
-    static constexpr int stages = E4M3 ? 2 : 3;         // bf16 K tiles, and V tiles, in shared memory
-    static constexpr int queries = 3;                   // query tiles
-    static constexpr int raw = E4M3 ? 2 : 0;            // E4M3 K tiles, and V tiles, on their way
+    static constexpr int k_stages = 3, v_stages = E4M3 ? 2 : 3;     // bf16 tiles in shared memory
+    static constexpr int queries = E4M3 ? 2 : 3;        // query tiles
+    static constexpr int raw = E4M3 ? 3 : 0;            // E4M3 K tiles, and V tiles, on their way
     static constexpr int threads = E4M3 ? 640 : 384;
     static constexpr int readers = kSoftmaxWarps + 2 + (E4M3 ? 2 * kExpandWarps : 0);   // of the item ring
-    // registers a thread: the softmax warps' and the others', together no more than the launch's
-    static constexpr int regs_softmax = E4M3 ? 168 : 200, regs_other = E4M3 ? 48 : 104;
-    static_assert(256 * regs_softmax + (threads - 256) * regs_other <= threads * (E4M3 ? 96 : 168), "register split");
+    // registers a thread: the softmax warps', the next four's and the expanding ones', together no more than the launch's
+    static constexpr int regs_softmax = E4M3 ? 144 : 200, regs_other = E4M3 ? 64 : 104, regs_expand = 64;
+    static_assert(256 * regs_softmax + 128 * regs_other + (threads - 384) * regs_expand <= threads * (E4M3 ? 96 : 168), "register split");
 };
 
 struct Item : ItemBase {
@@ -64,6 +64,7 @@ struct Item : ItemBase {
 // 15 us, 12 of them for its stores), and maxima and sums [slot][n_kv][vectors].  Slots: the prefix's parts, then own ones.
 struct Plan {
     int rows, rows_tile;        // of the batch; of a tile of query vectors
+    int rows_item, own_rows_item;       // of an item over the prefix, over own entries: one or two tiles
     int pairs, own_pairs;       // items over all rows, and over a sequence's
     int part, n_parts;          // the prefix's parts: length and number
     int own_parts_max;
@@ -80,12 +81,22 @@ Plan plan_of(const KvBatch &own, int prefix_len, int group, int n) {
     Plan p;
     p.rows = own.n_seq * n;
     p.rows_tile = kTile / group;
-    p.pairs = (p.rows + 2 * p.rows_tile - 1) / (2 * p.rows_tile);
-    p.own_pairs = (n + 2 * p.rows_tile - 1) / (2 * p.rows_tile);
     p.part = prefix_len > 0 ? prefix_part(prefix_len, own.n_kv) : kMinPrefixPart;
     p.n_parts = prefix_len > 0 ? (prefix_len - 1) / p.part + 1 : 0;
     p.own_parts_max = (own.max_len + kOwnPart - 1) / kOwnPart;
-    p.expanded = own.format == kKvE4m3 && prefix_len > 0 && p.pairs >= kExpandPairs;
+    // Two tiles share each K and V tile, and a step of both takes 1.7 times as long as of one alone: one tile an
+    // item where the SMs are then done sooner.  Own parts: at most as many as the caches hold.
+    auto items = [](int rows, int rows_item) { return (rows + rows_item - 1) / rows_item; };
+    const int both = 2 * p.rows_tile;
+    auto rows_item = [&](long long parts, int rows) {
+        auto rounds = [&](int of) { return (parts * items(rows, of) + kSms - 1) / kSms; };
+        return 17 * rounds(both) <= 10 * rounds(p.rows_tile) ? both : p.rows_tile;
+    };
+    p.rows_item = rows_item((long long)p.n_parts * own.n_kv, p.rows);
+    p.own_rows_item = rows_item((long long)p.own_parts_max * own.n_kv * own.n_seq, n);
+    p.pairs = items(p.rows, p.rows_item);
+    p.own_pairs = items(n, p.own_rows_item);
+    p.expanded = own.format == kKvE4m3 && prefix_len > 0 && items(p.rows, both) >= kExpandPairs;
     return p;
 }
 
@@ -109,14 +120,14 @@ struct KernelArgs {
 };
 
 template <bool E4M3>
-struct __align__(16) Shared : SharedBase<Item, Form<E4M3>::stages, Form<E4M3>::stages, Form<E4M3>::queries> {
-    uint64_t raw_full[2][2], raw_empty[2][2];   // K, V
+struct __align__(16) Shared : SharedBase<Item, Form<E4M3>::k_stages, Form<E4M3>::v_stages, Form<E4M3>::queries> {
+    uint64_t raw_full[2][3], raw_empty[2][3];   // K, V
     unsigned before[kGroups + 1];       // own items of the sequence groups before each
     int8_t depth[kRing][kMaxNodes];     // of an own item's nodes
 };
 // query tiles, bf16 stages, raw stages, their scales, then Shared
 template <bool E4M3>
-constexpr size_t kSmemBytes = size_t(Form<E4M3>::queries) * kTileBytes + size_t(2 * Form<E4M3>::stages) * kKeyBytes +
+constexpr size_t kSmemBytes = size_t(Form<E4M3>::queries) * kTileBytes + size_t(Form<E4M3>::k_stages + Form<E4M3>::v_stages) * kKeyBytes +
                               size_t(2 * Form<E4M3>::raw) * (kRawBytes + kTile) + sizeof(Shared<E4M3>);
 static_assert(kSmemBytes<false> <= 227 * 1024 && kSmemBytes<true> <= 227 * 1024, "shared memory");
 
@@ -151,8 +162,8 @@ __device__ Item item_of(const KernelArgs &k, const unsigned *before, unsigned i,
         const int c = idx_div(it.block, n_kv);
         it.j = it.block - c * n_kv;
         it.b = -1;
-        it.row0 = (i - it.block * pairs) * 2 * k.p.rows_tile;
-        it.n_rows = min(2 * k.p.rows_tile, k.p.rows - it.row0);
+        it.row0 = (i - it.block * pairs) * k.p.rows_item;
+        it.n_rows = min(k.p.rows_item, k.p.rows - it.row0);
         it.key0 = c * k.p.part;
         it.n_keys = min(k.p.part, k.a.prefix_len - it.key0);
         it.lim0 = it.n_keys - 1;
@@ -175,11 +186,11 @@ __device__ Item item_of(const KernelArgs &k, const unsigned *before, unsigned i,
     int b = lo * group_seqs;
     for (int n; u >= (n = own_items(k, b, false)); ++b) u -= n;
     const long long p = k.a.pos[b];
-    const int c = idx_div(u, k.p.own_pairs), first = (u - c * k.p.own_pairs) * 2 * k.p.rows_tile;
+    const int c = idx_div(u, k.p.own_pairs), first = (u - c * k.p.own_pairs) * k.p.own_rows_item;
     it.block = (k.p.n_parts + c) * n_kv + it.j;
     it.b = b;
     it.row0 = b * k.a.n + first;
-    it.n_rows = min(2 * k.p.rows_tile, k.a.n - first);
+    it.n_rows = min(k.p.own_rows_item, k.a.n - first);
     it.key0 = c * kOwnPart;
     it.n_keys = int(min((long long)kOwnPart, p - it.key0));
     it.lim0 = int(p - kMaxPath - it.key0);
@@ -243,8 +254,8 @@ __device__ void produce(const KernelArgs &k, Shared<E4M3> *sh, uint8_t *q_tiles,
         if (lane == 0) {
             if (E4M3 && it.n_rows && it.b >= 0 && loaded_k > 0) {
                 // the last copies into bf16 stages have arrived before others fill these: no prefix part follows an own one
-                drain(sh->k_full, loaded_k, F::stages, 0u);
-                drain(sh->v_full, loaded_v, F::stages, 0u);
+                drain(sh->k_full, loaded_k, F::k_stages, 0u);
+                drain(sh->v_full, loaded_v, F::v_stages, 0u);
                 loaded_k = loaded_v = 0;
             }
             sh->item[slot] = it;
@@ -287,11 +298,11 @@ __device__ void produce(const KernelArgs &k, Shared<E4M3> *sh, uint8_t *q_tiles,
                              scales, bar);
                 } else {
                     unsigned &loaded = is_v ? loaded_v : loaded_k;
-                    const int st = room(is_v ? sh->v_empty : sh->k_empty, loaded, F::stages);
+                    const int st = room(is_v ? sh->v_empty : sh->k_empty, loaded, is_v ? F::v_stages : F::k_stages);
                     if (!ok) return;
                     ++loaded;
                     uint64_t *bar = is_v ? &sh->v_full[st] : &sh->k_full[st];
-                    uint8_t *dst = stages + size_t(is_v ? F::stages + st : st) * kKeyBytes;
+                    uint8_t *dst = stages + size_t(is_v ? F::k_stages + st : st) * kKeyBytes;
                     if (is_v && !E4M3) {
                         to_mend &= ~(1u << st);
                         const int first = max(0, it.lim0 + 1 - key);
@@ -329,8 +340,8 @@ __device__ void produce(const KernelArgs &k, Shared<E4M3> *sh, uint8_t *q_tiles,
         sh->mend[mended % kMends].stage = -1;
         mbar_arrive(&sh->mend_full[mended % kMends]);
     }
-    drain(sh->k_full, loaded_k, F::stages, 0u);
-    drain(sh->v_full, loaded_v, F::stages, to_mend);
+    drain(sh->k_full, loaded_k, F::k_stages, 0u);
+    drain(sh->v_full, loaded_v, F::v_stages, to_mend);
     drain(sh->q_full, queries, F::queries, 0u);
 }
 
@@ -338,42 +349,37 @@ __device__ void produce(const KernelArgs &k, Shared<E4M3> *sh, uint8_t *q_tiles,
 // part's last entry become zeros up to the 16-row step the product reads, and so
 // do entries marked NaN that some nodes do not see (0 * NaN would reach those;
 // the nodes that see them get the NaN back when the result is stored).
-template <bool IS_V>
-__device__ void expand_tiles(const KernelArgs &k, Shared<true> *sh, uint8_t *tiles_out, const uint8_t *raw) {
+__device__ void expand_tiles(const KernelArgs &k, Shared<true> *sh, const bool is_v, uint8_t *tiles_out, const uint8_t *raw) {
     using F = Form<true>;
-    constexpr int kRows = 4 * kExpandWarps, kSteps = kKeys / kRows;    // rows all warps take at a time
+    constexpr int kRows = 4 * kExpandWarps, kSteps = kKeys / kRows;    // rows the warps take at a time
     static_assert(kRows % 8 == 0 && kKeys % kRows == 0, "a thread's rows share their place in the swizzle");
-    const int lane = threadIdx.x & 31, tid = threadIdx.x - 32 * (kExpandWarp + (IS_V ? kExpandWarps : 0)), group = tid & 7, row0 = tid >> 3;
-    const uint8_t *scales = raw + size_t(2 * F::raw) * kRawBytes + (IS_V ? F::raw * kTile : 0);
-    raw += IS_V ? F::raw * kRawBytes : 0;
-    uint64_t *const raw_full = sh->raw_full[IS_V], *const raw_empty = sh->raw_empty[IS_V];
-    uint64_t *const full = IS_V ? sh->v_full : sh->k_full, *const empty = IS_V ? sh->v_empty : sh->k_empty;
+    const int lane = threadIdx.x & 31, tid = threadIdx.x & (32 * kExpandWarps - 1), group = tid & 7, row0 = tid >> 3;
+    const int stages = is_v ? F::v_stages : F::k_stages;
+    const uint8_t *scales = raw + size_t(2 * F::raw) * kRawBytes + (is_v ? F::raw * kTile : 0);
+    raw += is_v ? F::raw * kRawBytes : 0;
+    uint64_t *const raw_full = sh->raw_full[is_v], *const raw_empty = sh->raw_empty[is_v];
+    uint64_t *const full = is_v ? sh->v_full : sh->k_full, *const empty = is_v ? sh->v_empty : sh->k_empty;
     Ring<F::raw> from;
-    Ring<F::stages> to;
-    to.parity = 1u;     // of a fresh barrier, the phase before the first counts as over
+    unsigned done = 0;      // tiles so far
     for (unsigned n = 0;; ++n) {
         const int slot = n % kRing;
         if (!warp_wait(sh, &sh->item_full[slot], (n / kRing) & 1)) return;
         const int n_rows = sh->item[slot].n_rows, n_keys = sh->item[slot].n_keys, lim0 = sh->item[slot].lim0;
         if (n_rows == 0) return;
         const int tiles = (n_keys + kKeys - 1) / kKeys;
-        if (k.p.expanded && sh->item[slot].b < 0) {
-            // Copied as bf16: the ring's places pass by.  When the first own item is known, all of its
-            // stage's uses but the last are over (the last copy's producer had waited for that).
-            to.step(tiles);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
-            continue;
-        }
-        for (int t = 0; t < tiles; ++t) {
+        // An expanded prefix is copied as bf16: its tiles pass by.  When the first own item is known, all of its
+        // stages' uses but the last are over (the last copies' producer had waited for that).
+        const bool copied = k.p.expanded && sh->item[slot].b < 0;
+        for (int t = 0; t < tiles && !copied; ++t) {
             const int key = t * kKeys, valid = min(kKeys, n_keys - key);
-            const int fill = IS_V ? (valid + 15) & ~15 : valid, hidden = lim0 + 1 - key;
+            const int fill = is_v ? (valid + 15) & ~15 : valid, hidden = lim0 + 1 - key;
+            const unsigned round = (done + t) / stages, at = done + t - round * stages;
             if (!warp_wait(sh, &raw_full[from.at], from.parity)) return;
-            if (!warp_wait(sh, &empty[to.at], to.parity)) return;
+            if (round > 0 && !warp_wait(sh, &empty[at], (round - 1) & 1)) return;
             const uint8_t *src = raw + size_t(from.at) * kRawBytes + row0 * kHeadDim + 16 * group;
             const uint8_t *sc = scales + from.at * kTile + row0;
-            uint8_t *dst = tiles_out + size_t(to.at) * kKeyBytes + row0 * 128 + ((group ^ (row0 & 7)) << 4);
-            const bool whole = valid == kKeys && !(IS_V && hidden < kKeys);     // nothing to leave out
+            uint8_t *dst = tiles_out + size_t(at) * kKeyBytes + row0 * 128 + ((group ^ (row0 & 7)) << 4);
+            const bool whole = valid == kKeys && !(is_v && hidden < kKeys);     // nothing to leave out
             uint4 w[kSteps];
             uint32_t f[kSteps];
 #pragma unroll
@@ -386,7 +392,7 @@ __device__ void expand_tiles(const KernelArgs &k, Shared<true> *sh, uint8_t *til
                 const int row = row0 + i * kRows;
                 if (!whole) {
                     if (row >= fill) break;
-                    if (row >= valid || (IS_V && f[i] == uint32_t(kScaleNan) && row >= hidden)) {
+                    if (row >= valid || (is_v && f[i] == uint32_t(kScaleNan) && row >= hidden)) {
                         if (row < valid) *reinterpret_cast<volatile int *>(&sh->bad[slot]) = 1;
                         w[i] = make_uint4(0u, 0u, 0u, 0u);
                         f[i] = 0u;
@@ -404,12 +410,12 @@ __device__ void expand_tiles(const KernelArgs &k, Shared<true> *sh, uint8_t *til
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&full[to.at]);
+                mbar_arrive(&full[at]);
                 mbar_arrive(&raw_empty[from.at]);
             }
             from.step();
-            to.step();
         }
+        done += tiles;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
     }
@@ -493,8 +499,8 @@ template <bool E4M3>
 __global__ void __launch_bounds__(Form<E4M3>::threads, 1) attn_tree_kernel(const __grid_constant__ KernelArgs k) {
     using F = Form<E4M3>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint8_t *q_tiles = smem, *stages = smem + F::queries * kTileBytes, *raw = stages + size_t(2 * F::stages) * kKeyBytes;
-    uint8_t *const v_tiles = stages + size_t(F::stages) * kKeyBytes;
+    uint8_t *q_tiles = smem, *stages = smem + F::queries * kTileBytes, *raw = stages + size_t(F::k_stages + F::v_stages) * kKeyBytes;
+    uint8_t *const v_tiles = stages + size_t(F::k_stages) * kKeyBytes;
     Shared<E4M3> *sh = reinterpret_cast<Shared<E4M3> *>(raw + size_t(2 * F::raw) * (kRawBytes + kTile));
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
@@ -525,14 +531,16 @@ __global__ void __launch_bounds__(Form<E4M3>::threads, 1) attn_tree_kernel(const
             return store_results<E4M3>(k, sh, tmem, slot, tile, n_here, m, l, steps);
         });
     } else {
-        regs_lower<F::regs_other>();
         if (E4M3 && warp >= kExpandWarp) {
+            regs_lower<F::regs_expand>();
             if constexpr (E4M3) {
-                if (warp < kExpandWarp + kExpandWarps)
-                    expand_tiles<false>(k, sh, stages, raw);
-                else
-                    expand_tiles<true>(k, sh, v_tiles, raw);
+                const bool is_v = warp >= kExpandWarp + kExpandWarps;
+                expand_tiles(k, sh, is_v, is_v ? v_tiles : stages, raw);
             }
+        } else {
+            regs_lower<F::regs_other>();
+        }
+        if (E4M3 && warp >= kExpandWarp) {
         } else if (warp == kProducerWarp) {
             produce<E4M3>(k, sh, q_tiles, stages, raw);
         } else if (warp == kMendWarp) {
@@ -588,13 +596,13 @@ __global__ void __launch_bounds__(256) expand_prefix_kernel(KvBatch c, int len, 
 }
 
 // ------------------------------------------------------------------ near entries, and the sum
-// A CTA takes up to 32 vectors (whole nodes) of one KV head.  First the near entries, before the
+// A CTA takes up to VECS vectors (whole nodes) of one KV head.  First the near entries, before the
 // attention grid has ended: a warp a node, at most 16 keys in path order, one matrix product (bf16 operands, fp32
 // sums) for the scores of its heads and one for their outputs.  Then the far results are added up, the near ones last:
-// a lane per vector, a warp QUADS quads of columns.  It reads 520 bytes per vector and slot, and nothing else counts where
-// there are many.  With few vectors, the loads that follow one another count: CTAs of a quarter of the columns (which work
-// on the near entries four times) keep four times as many on their way.
-constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps, kJoinVecs = 32;
+// 256 threads, some quads of columns each.  It reads 520 bytes per vector and slot, and nothing else counts where
+// there are many.  With few vectors, the loads that follow one another do: SPLIT CTAs then take a part of the columns each (and
+// work on the near entries as often), and keep as many times more slots on their way.
+constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps;
 constexpr int kNearPitch = kHeadDim + 4;        // floats: lanes that read a quad of consecutive vectors meet no bank twice
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -625,16 +633,17 @@ __device__ __forceinline__ uint4 cache_chunk(const void *data, const uint8_t *sc
     return x;
 }
 
+template <int VECS>
 struct __align__(16) JoinShared {
-    float near[kJoinVecs][kNearPitch];      // near outputs; then, as bf16, the rows' outputs
-    float2 ml[kJoinVecs];
-    int depth[kJoinVecs];                   // of the nodes; -1: idle sequence, no tree or unused row
-    uint4 v[kJoinWarps][kMaxPath][16];      // a node's near values, chunk c of row t at c XOR (t % 8)
+    float near[VECS][kNearPitch];      // near outputs; then, as bf16, the rows' outputs
+    float2 ml[VECS];
+    int depth[VECS];                   // of the nodes; -1: idle sequence, no tree or unused row
+    uint4 v[VECS < kJoinWarps ? VECS : kJoinWarps][kMaxPath][16];      // a node's near values, chunk c of row t at c XOR (t % 8)
 };
 
 // One node's near entries; whole warp.  Rows of the products are the group's heads, a lane's are lane / 4 and that + 8.
-template <bool E4M3>
-__device__ void near_entries(const AttnTreeArgs &a, JoinShared *sh, int row, int j, int nth, uint4 (*s_v)[16]) {
+template <bool E4M3, int VECS>
+__device__ void near_entries(const AttnTreeArgs &a, JoinShared<VECS> *sh, int row, int j, int nth, uint4 (*s_v)[16]) {
     const int lane = threadIdx.x & 31, g = a.group, r = lane >> 2, c4 = lane & 3;
     const int b = idx_div(row, a.n), node = row - b * a.n;
     const long long pos = seq_position(a.pos, b, a.n, a.own.max_len, a.err, false);
@@ -749,14 +758,15 @@ __device__ void near_entries(const AttnTreeArgs &a, JoinShared *sh, int row, int
     __syncwarp();       // the next node's values may come
 }
 
-template <bool E4M3, int QUADS>
+template <bool E4M3, int VECS, int SPLIT>
 __global__ void __launch_bounds__(kJoinThreads, 2) attn_tree_join_kernel(AttnTreeArgs a, Plan p, const float *results,
                                                                          const float2 *ml, unsigned *next) {
+    constexpr int kQuads = VECS / 8 / SPLIT;        // a thread's: `quad` and the ones after it
     extern __shared__ __align__(1024) uint8_t smem[];
-    JoinShared *sh = reinterpret_cast<JoinShared *>(smem);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = a.group, j = blockIdx.y, n_kv = a.own.n_kv;
-    const int quad0 = blockIdx.z * (kJoinWarps * QUADS) + warp * QUADS;
-    const int nodes = kJoinVecs / g, row0 = blockIdx.x * nodes, here = min(nodes, p.rows - row0), n_vec = p.rows * g;
+    JoinShared<VECS> *sh = reinterpret_cast<JoinShared<VECS> *>(smem);
+    const int warp = threadIdx.x >> 5, g = a.group, j = blockIdx.y, n_kv = a.own.n_kv;
+    const int mine = threadIdx.x % VECS, quad = (blockIdx.z * (kJoinThreads / VECS) + threadIdx.x / VECS) * kQuads;
+    const int nodes = VECS / g, row0 = blockIdx.x * nodes, here = min(nodes, p.rows - row0), n_vec = p.rows * g;
     for (int i = warp; i < here; i += kJoinWarps) near_entries<E4M3>(a, sh, row0 + i, j, i, sh->v[warp]);
     __syncthreads();
     // The results come from the attention grid; all else from before it, which it had
@@ -764,49 +774,47 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_tree_join_kernel(AttnTre
     grid_dependency_wait();
     grid_launch_dependents();
     if (blockIdx.x == 0 && j == 0 && blockIdx.z == 0 && threadIdx.x == 0) *next = 0u;
-    const int nth = lane / g, depth = nth < here ? sh->depth[nth] : -1;
-    float4 sum[QUADS];
+    const int nth = mine / g, depth = nth < here ? sh->depth[nth] : -1;
+    float4 sum[kQuads];
     float l = 1.f;
 #pragma unroll
-    for (int i = 0; i < QUADS; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < kQuads; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (depth >= 0) {
         const long long far = a.pos[idx_div(row0 + nth, a.n)] + depth + 1 - kMaxPath;       // own entries that lie farther
         const int n = p.n_parts + (far > 0 ? int((far + kOwnPart - 1) / kOwnPart) : 0);
-        const int v = row0 * g + lane;
+        const int v = row0 * g + mine;
         const float2 *my_ml = ml + (size_t)j * n_vec + v;
-        const float4 *x = reinterpret_cast<const float4 *>(results) + ((size_t)j * 32 + quad0) * n_vec + v;
+        const float4 *x = reinterpret_cast<const float4 *>(results) + ((size_t)j * 32 + quad) * n_vec + v;
         const size_t step = (size_t)n_kv * n_vec;
         float m = -INFINITY;
         l = 0.f;
-        auto add = [&](const float2 &part, const float4 (&y)[QUADS]) {
+        auto add = [&](const float2 &part, const float4 (&y)[kQuads]) {
             const Factors f = factors(m, part.x);
             m = f.top;
             l = fold(f, l, part.y);
 #pragma unroll
-            for (int i = 0; i < QUADS; ++i) sum[i] = fold(f, sum[i], y[i]);
+            for (int i = 0; i < kQuads; ++i) sum[i] = fold(f, sum[i], y[i]);
         };
-        constexpr int kAhead = 16 / QUADS;
+        constexpr int kAhead = 16 / kQuads;
         float2 w[kAhead];
-        float4 y[kAhead][QUADS];
-        auto load = [&](int u) {
-            w[u] = *my_ml;
-#pragma unroll
-            for (int i = 0; i < QUADS; ++i) y[u][i] = __ldcs(x + (size_t)i * n_vec);
-            my_ml += step;
-            x += step * 32;
-        };
+        float4 y[kAhead][kQuads];
         for (int c = 0; c < n; c += kAhead) {
 #pragma unroll
             for (int u = 0; u < kAhead; ++u)
-                if (c + u < n) load(u);
+                if (c + u < n) {
+                    w[u] = *my_ml;
+#pragma unroll
+                    for (int i = 0; i < kQuads; ++i) y[u][i] = __ldcs(x + (size_t)i * n_vec);
+                    my_ml += step;
+                    x += step * 32;
+                }
 #pragma unroll
             for (int u = 0; u < kAhead; ++u)
                 if (c + u < n) add(w[u], y[u]);
         }
 #pragma unroll
-        for (int i = 0; i < QUADS; ++i)
-            y[0][i] = *reinterpret_cast<const float4 *>(&sh->near[lane][4 * (quad0 + i)]);
-        add(sh->ml[lane], y[0]);
+        for (int i = 0; i < kQuads; ++i) y[0][i] = *reinterpret_cast<const float4 *>(&sh->near[mine][4 * (quad + i)]);
+        add(sh->ml[mine], y[0]);
     }
     __syncthreads();    // the near outputs are read
     uint16_t *const rows = reinterpret_cast<uint16_t *>(&sh->near[0][0]);
@@ -816,11 +824,11 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_tree_join_kernel(AttnTre
         return *reinterpret_cast<const uint32_t *>(&r);
     };
 #pragma unroll
-    for (int i = 0; i < QUADS; ++i)
-        *reinterpret_cast<uint2 *>(rows + lane * kPitch + 4 * (quad0 + i)) =
+    for (int i = 0; i < kQuads; ++i)
+        *reinterpret_cast<uint2 *>(rows + mine * kPitch + 4 * (quad + i)) =
             make_uint2(pair(sum[i].x, sum[i].y), pair(sum[i].z, sum[i].w));
     __syncthreads();
-    constexpr int kChunks = kJoinWarps * QUADS / 2;     // 16-byte chunks of a vector
+    constexpr int kChunks = 16 / SPLIT;     // of 16 bytes
     for (int i = threadIdx.x; i < here * g * kChunks; i += kJoinThreads) {
         const int v = i / kChunks, c = i % kChunks + blockIdx.z * kChunks, at = v / g;
         *reinterpret_cast<uint4 *>(a.out + (size_t)(row0 + at) * a.ldo + (size_t)(j * g + v - at * g) * kHeadDim + 8 * c) =
@@ -861,9 +869,9 @@ static cudaError_t launch_form(const AttnTreeArgs &a, KernelArgs &k, cudaStream_
     if (dev < 0 || dev >= kMaxDevices || !opted_in[dev]) {
         e = cudaFuncSetAttribute(attn_tree_kernel<E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemBytes<E4M3>));
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(attn_tree_join_kernel<E4M3, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(JoinShared)));
+            e = cudaFuncSetAttribute(attn_tree_join_kernel<E4M3, 32, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(JoinShared<32>)));
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(attn_tree_join_kernel<E4M3, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(JoinShared)));
+            e = cudaFuncSetAttribute(attn_tree_join_kernel<E4M3, 32, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(JoinShared<32>)));
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < kMaxDevices) opted_in[dev] = true;
     }
@@ -873,10 +881,20 @@ static cudaError_t launch_form(const AttnTreeArgs &a, KernelArgs &k, cudaStream_
     e = launch_pdl(attn_tree_kernel<E4M3>, dim3(unsigned(jobs < sms ? jobs : sms)), dim3(Form<E4M3>::threads), kSmemBytes<E4M3>,
                    s, k);
     if (e != cudaSuccess) return e;
-    const int nodes = kJoinVecs / a.group, tiles = (k.p.rows + nodes - 1) / nodes;
-    const bool few = tiles * a.own.n_kv < kFewJoins;
-    return launch_pdl(few ? attn_tree_join_kernel<E4M3, 1> : attn_tree_join_kernel<E4M3, 4>, dim3(tiles, a.own.n_kv, few ? 4 : 1),
-                      dim3(kJoinThreads), sizeof(JoinShared), s, a, k.p, (const float *)k.values, (const float2 *)k.ml, k.next);
+    // Vectors of a CTA of the sum: no more than 16 nodes, two a warp (64 x 64 nodes of one head, 8 vectors: 23 us in all, 32: 27;
+    // 40 x 20 of three, 8: 30, 32: 23).  Columns split where there are fewer CTAs than kSplitCtas
+    // (3 x 41 nodes, 84 CTAs, over own 12007 entries: 32 us, 43 without; 5 x 24, 240 CTAs: 53, 44 without).
+    constexpr int kSplitCtas = 100;
+    auto join = [&](auto kernel, int vecs, int split, size_t smem) {
+        const int nodes = vecs / a.group;
+        return launch_pdl(kernel, dim3((k.p.rows + nodes - 1) / nodes, a.own.n_kv, split), dim3(kJoinThreads), smem, s, a, k.p,
+                          (const float *)k.values, (const float2 *)k.ml, k.next);
+    };
+    if (a.group == 1) return join(attn_tree_join_kernel<E4M3, 8, 1>, 8, 1, sizeof(JoinShared<8>));
+    const int nodes = 32 / a.group;
+    if ((k.p.rows + nodes - 1) / nodes * a.own.n_kv < kSplitCtas)
+        return join(attn_tree_join_kernel<E4M3, 32, 4>, 32, 4, sizeof(JoinShared<32>));
+    return join(attn_tree_join_kernel<E4M3, 32, 1>, 32, 1, sizeof(JoinShared<32>));
 }
 
 cudaError_t launch_attn_tree(const AttnTreeArgs &a, cudaStream_t s, const char **why) {
