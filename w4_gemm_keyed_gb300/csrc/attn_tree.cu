@@ -117,6 +117,9 @@ struct KernelArgs {
     float *values;          // [slots][128]
     float2 *ml;             // [slots]: (maximum score, weight sum)
     unsigned *next;         // items taken beyond the first of each CTA; zero between calls
+    int prefix_parts;       // that this kernel works on: all or none
+    bool own_parts;         // whether it works on them
+    bool overlaps;          // whether the preceding grid works on the other parts: nothing of its is read
 };
 
 template <bool E4M3>
@@ -156,7 +159,7 @@ __device__ int own_items(const KernelArgs &k, int b, bool report) {     // a hea
 __device__ Item item_of(const KernelArgs &k, const unsigned *before, unsigned i, int group_seqs) {
     Item it{};
     const unsigned n_kv = k.a.own.n_kv, pairs = k.p.pairs;
-    const unsigned n_prefix = k.p.n_parts * n_kv * pairs;
+    const unsigned n_prefix = k.prefix_parts * n_kv * pairs;
     if (i < n_prefix) {
         it.block = idx_div(i, pairs);
         const int c = idx_div(it.block, n_kv);
@@ -210,7 +213,7 @@ __device__ void produce(const KernelArgs &k, Shared<E4M3> *sh, uint8_t *q_tiles,
     int total = 0;
     for (int g0 = 0; g0 < n_groups; g0 += 32) {
         int n = 0;
-        for (int b = (g0 + lane) * group_seqs; b < min(n_seq, (g0 + lane + 1) * group_seqs); ++b)
+        for (int b = (g0 + lane) * group_seqs; k.own_parts && b < min(n_seq, (g0 + lane + 1) * group_seqs); ++b)
             n += own_items(k, b, blockIdx.x == 0);
         int sum = n;
         for (int o = 1; o < 32; o <<= 1) {
@@ -224,7 +227,7 @@ __device__ void produce(const KernelArgs &k, Shared<E4M3> *sh, uint8_t *q_tiles,
     __syncwarp();
 
     unsigned i = blockIdx.x;
-    unsigned loaded_k = 0, loaded_v = 0, raw_k = 0, raw_v = 0, queries = 0;     // tiles so far
+    unsigned loaded_k = 0, loaded_v = 0, queries = 0;   // tiles so far
     unsigned mended = 0;            // of them V tiles to mend
     unsigned to_mend = 0;           // bit st: the last tile of V stage st is one
     constexpr int kRaw = E4M3 ? F::raw : 1;
@@ -234,10 +237,6 @@ __device__ void produce(const KernelArgs &k, Shared<E4M3> *sh, uint8_t *q_tiles,
         const int st = n % stages_of;
         ok = ok && (n < unsigned(stages_of) || lane_wait(sh, &empty[st], (n / stages_of - 1) & 1));
         return st;
-    };
-    auto drain = [&](uint64_t *full, unsigned count, int stages_of, unsigned except) {
-        for (unsigned t = count > unsigned(stages_of) ? count - stages_of : 0; t < count; ++t)
-            if (!(except >> (t % stages_of) & 1u)) wait_drained(&full[t % stages_of], (t / stages_of) & 1);
     };
     for (unsigned n = 0;; ++n) {
         const int slot = n % kRing;
@@ -252,12 +251,6 @@ __device__ void produce(const KernelArgs &k, Shared<E4M3> *sh, uint8_t *q_tiles,
         }
         unsigned taken = 0;
         if (lane == 0) {
-            if (E4M3 && it.n_rows && it.b >= 0 && loaded_k > 0) {
-                // the last copies into bf16 stages have arrived before others fill these: no prefix part follows an own one
-                drain(sh->k_full, loaded_k, F::k_stages, 0u);
-                drain(sh->v_full, loaded_v, F::v_stages, 0u);
-                loaded_k = loaded_v = 0;
-            }
             sh->item[slot] = it;
             sh->bad[slot] = 0;
             mbar_arrive(&sh->item_full[slot]);
@@ -282,8 +275,8 @@ __device__ void produce(const KernelArgs &k, Shared<E4M3> *sh, uint8_t *q_tiles,
             // one tile of entries key0 + key ..
             auto load = [&](bool is_v, int key) {
                 const int row = it.key0 + key;
-                if (E4M3 && (own || !k.p.expanded)) {
-                    unsigned &loaded = is_v ? raw_v : raw_k;
+                if constexpr (E4M3) {
+                    unsigned &loaded = is_v ? loaded_v : loaded_k;
                     const int st = room(sh->raw_empty[is_v], loaded, kRaw), at = (is_v ? kRaw : 0) + st;
                     if (!ok) return;
                     ++loaded;
@@ -303,7 +296,7 @@ __device__ void produce(const KernelArgs &k, Shared<E4M3> *sh, uint8_t *q_tiles,
                     ++loaded;
                     uint64_t *bar = is_v ? &sh->v_full[st] : &sh->k_full[st];
                     uint8_t *dst = stages + size_t(is_v ? F::k_stages + st : st) * kKeyBytes;
-                    if (is_v && !E4M3) {
+                    if (is_v) {
                         to_mend &= ~(1u << st);
                         const int first = max(0, it.lim0 + 1 - key);
                         if (own && first < kKeys) {     // past the last entry that every node sees: handed over by the mender
@@ -317,8 +310,6 @@ __device__ void produce(const KernelArgs &k, Shared<E4M3> *sh, uint8_t *q_tiles,
                     mbar_arrive_expect_tx(bar, kKeyBytes);
                     tma_load_3d(dst, map, 0, row, outer, bar);
                     tma_load_3d(dst + kKeyHalf, map, 64, row, outer, bar);
-                    if (E4M3)       // the arrivals of the warps that expand other tiles
-                        for (int w = 1; w < kExpandWarps; ++w) mbar_arrive(bar);
                 }
             };
             for (int t = 0; t <= tiles && ok; ++t) {        // K(0), then K(t) and V(t - 1)
@@ -332,16 +323,20 @@ __device__ void produce(const KernelArgs &k, Shared<E4M3> *sh, uint8_t *q_tiles,
     }
     if (lane != 0) return;
     // no copy outlives the CTA
+    auto drain = [&](uint64_t *full, unsigned count, int stages_of, unsigned except) {
+        for (unsigned t = count > unsigned(stages_of) ? count - stages_of : 0; t < count; ++t)
+            if (!(except >> (t % stages_of) & 1u)) wait_drained(&full[t % stages_of], (t / stages_of) & 1);
+    };
     if constexpr (E4M3) {
-        drain(sh->raw_full[0], raw_k, kRaw, 0u);
-        drain(sh->raw_full[1], raw_v, kRaw, 0u);
+        drain(sh->raw_full[0], loaded_k, kRaw, 0u);
+        drain(sh->raw_full[1], loaded_v, kRaw, 0u);
     } else {
+        drain(sh->k_full, loaded_k, F::k_stages, 0u);
+        drain(sh->v_full, loaded_v, F::v_stages, to_mend);
         drain(sh->mend_full, mended, kMends, 0u);
         sh->mend[mended % kMends].stage = -1;
         mbar_arrive(&sh->mend_full[mended % kMends]);
     }
-    drain(sh->k_full, loaded_k, F::k_stages, 0u);
-    drain(sh->v_full, loaded_v, F::v_stages, to_mend);
     drain(sh->q_full, queries, F::queries, 0u);
 }
 
@@ -349,33 +344,30 @@ __device__ void produce(const KernelArgs &k, Shared<E4M3> *sh, uint8_t *q_tiles,
 // part's last entry become zeros up to the 16-row step the product reads, and so
 // do entries marked NaN that some nodes do not see (0 * NaN would reach those;
 // the nodes that see them get the NaN back when the result is stored).
-__device__ void expand_tiles(const KernelArgs &k, Shared<true> *sh, const bool is_v, uint8_t *tiles_out, const uint8_t *raw) {
+__device__ void expand_tiles(Shared<true> *sh, const bool is_v, uint8_t *tiles_out, const uint8_t *raw) {
     using F = Form<true>;
     constexpr int kRows = 4 * kExpandWarps, kSteps = kKeys / kRows;    // rows the warps take at a time
     static_assert(kRows % 8 == 0 && kKeys % kRows == 0, "a thread's rows share their place in the swizzle");
     const int lane = threadIdx.x & 31, tid = threadIdx.x & (32 * kExpandWarps - 1), group = tid & 7, row0 = tid >> 3;
-    const int stages = is_v ? F::v_stages : F::k_stages;
     const uint8_t *scales = raw + size_t(2 * F::raw) * kRawBytes + (is_v ? F::raw * kTile : 0);
     raw += is_v ? F::raw * kRawBytes : 0;
     uint64_t *const raw_full = sh->raw_full[is_v], *const raw_empty = sh->raw_empty[is_v];
     uint64_t *const full = is_v ? sh->v_full : sh->k_full, *const empty = is_v ? sh->v_empty : sh->k_empty;
     Ring<F::raw> from;
-    unsigned done = 0;      // tiles so far
+    const int stages = is_v ? F::v_stages : F::k_stages;
+    int at = 0;
+    uint32_t parity = 1u;   // of a fresh barrier, the phase before the first counts as over
     for (unsigned n = 0;; ++n) {
         const int slot = n % kRing;
         if (!warp_wait(sh, &sh->item_full[slot], (n / kRing) & 1)) return;
         const int n_rows = sh->item[slot].n_rows, n_keys = sh->item[slot].n_keys, lim0 = sh->item[slot].lim0;
         if (n_rows == 0) return;
         const int tiles = (n_keys + kKeys - 1) / kKeys;
-        // An expanded prefix is copied as bf16: its tiles pass by.  When the first own item is known, all of its
-        // stages' uses but the last are over (the last copies' producer had waited for that).
-        const bool copied = k.p.expanded && sh->item[slot].b < 0;
-        for (int t = 0; t < tiles && !copied; ++t) {
+        for (int t = 0; t < tiles; ++t) {
             const int key = t * kKeys, valid = min(kKeys, n_keys - key);
             const int fill = is_v ? (valid + 15) & ~15 : valid, hidden = lim0 + 1 - key;
-            const unsigned round = (done + t) / stages, at = done + t - round * stages;
             if (!warp_wait(sh, &raw_full[from.at], from.parity)) return;
-            if (round > 0 && !warp_wait(sh, &empty[at], (round - 1) & 1)) return;
+            if (!warp_wait(sh, &empty[at], parity)) return;
             const uint8_t *src = raw + size_t(from.at) * kRawBytes + row0 * kHeadDim + 16 * group;
             const uint8_t *sc = scales + from.at * kTile + row0;
             uint8_t *dst = tiles_out + size_t(at) * kKeyBytes + row0 * 128 + ((group ^ (row0 & 7)) << 4);
@@ -414,8 +406,11 @@ __device__ void expand_tiles(const KernelArgs &k, Shared<true> *sh, const bool i
                 mbar_arrive(&raw_empty[from.at]);
             }
             from.step();
+            if (++at == stages) {
+                at = 0;
+                parity ^= 1u;
+            }
         }
-        done += tiles;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
     }
@@ -512,13 +507,17 @@ __global__ void __launch_bounds__(Form<E4M3>::threads, 1) attn_tree_kernel(const
         fence_mbar_init();
     }
     if (warp == kScoreWarp) tc_alloc(&sh->tmem, kTmemCols);
-    if (warp == kProducerWarp && (threadIdx.x & 31) < 5 && (!E4M3 || (threadIdx.x & 31) == 4 || (k.p.expanded && (threadIdx.x & 31) < 2)))
-        prefetch_tensormap(&k.map[threadIdx.x & 31]);
+    if (warp == kProducerWarp && (threadIdx.x & 31) < 5) {
+        const int m = threadIdx.x & 31;
+        if (m == 4 || (!E4M3 && (m < 2 ? k.prefix_parts > 0 : k.own_parts))) prefetch_tensormap(&k.map[m]);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh->tmem;
-    grid_dependency_wait();     // queries, positions, parents and entries come from the preceding grids
+    // Queries, positions, parents and entries come from the preceding grids; the other parts' grid had waited
+    // for them when it let this one start.
+    if (!k.overlaps) grid_dependency_wait();
     grid_launch_dependents();
     if (warp < kSoftmaxWarps) {
         regs_raise<F::regs_softmax>();
@@ -535,7 +534,7 @@ __global__ void __launch_bounds__(Form<E4M3>::threads, 1) attn_tree_kernel(const
             regs_lower<F::regs_expand>();
             if constexpr (E4M3) {
                 const bool is_v = warp >= kExpandWarp + kExpandWarps;
-                expand_tiles(k, sh, is_v, is_v ? v_tiles : stages, raw);
+                expand_tiles(sh, is_v, is_v ? v_tiles : stages, raw);
             }
         } else {
             regs_lower<F::regs_other>();
@@ -558,6 +557,7 @@ __global__ void __launch_bounds__(Form<E4M3>::threads, 1) attn_tree_kernel(const
     tc_fence_after();
     if (threadIdx.x == 0 && sh->abort) set_error(k.a.err, kDevTimeout);
     if (warp == kScoreWarp) tc_dealloc(tmem, kTmemCols);
+    if (k.overlaps) grid_dependency_wait();     // what waits for this grid waits for that one too
 }
 
 // ------------------------------------------------------------------ an E4M3 prefix as bf16
@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_tree_join_kernel(AttnTre
     // waited for when it let this grid start.
     grid_dependency_wait();
     grid_launch_dependents();
-    if (blockIdx.x == 0 && j == 0 && blockIdx.z == 0 && threadIdx.x == 0) *next = 0u;
+    if (blockIdx.x == 0 && j == 0 && blockIdx.z == 0 && threadIdx.x == 0) next[0] = next[1] = 0u;
     const int nth = mine / g, depth = nth < here ? sh->depth[nth] : -1;
     float4 sum[kQuads];
     float l = 1.f;
@@ -860,27 +860,45 @@ size_t attn_tree_bytes(const KvBatch &own, int prefix_len, int group, int n) {
            expanded_bytes(p, prefix_len, own.n_kv);
 }
 
+namespace {
+
+// The attention kernel over the prefix's parts, own parts or both.
 template <bool E4M3>
-static cudaError_t launch_form(const AttnTreeArgs &a, KernelArgs &k, cudaStream_t s) {
+cudaError_t launch_parts(KernelArgs &k, bool prefix, bool own, bool overlaps, cudaStream_t s) {
     static std::atomic<bool> opted_in[kMaxDevices] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices || !opted_in[dev]) {
         e = cudaFuncSetAttribute(attn_tree_kernel<E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemBytes<E4M3>));
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(attn_tree_join_kernel<E4M3, 32, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(JoinShared<32>)));
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < kMaxDevices) opted_in[dev] = true;
+    }
+    const KvBatch &c = k.a.own;
+    k.prefix_parts = prefix ? k.p.n_parts : 0;
+    k.own_parts = own;
+    k.overlaps = overlaps;
+    const long long items = (long long)c.n_kv * ((long long)k.prefix_parts * k.p.pairs +
+                                                 (own ? (long long)c.n_seq * k.p.own_parts_max * k.p.own_pairs : 0));
+    const int sms = device_sm_count();
+    return launch_pdl(attn_tree_kernel<E4M3>, dim3(unsigned(items < sms ? items : sms)), dim3(Form<E4M3>::threads), kSmemBytes<E4M3>,
+                      s, k);
+}
+
+template <bool E4M3>
+cudaError_t launch_join(const KernelArgs &k, cudaStream_t s) {
+    static std::atomic<bool> opted_in[kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices || !opted_in[dev]) {
+        e = cudaFuncSetAttribute(attn_tree_join_kernel<E4M3, 32, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(JoinShared<32>)));
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(attn_tree_join_kernel<E4M3, 32, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(JoinShared<32>)));
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < kMaxDevices) opted_in[dev] = true;
     }
-    const long long jobs = (long long)a.own.n_kv * ((long long)k.p.n_parts * k.p.pairs +
-                                                    (long long)a.own.n_seq * k.p.own_parts_max * k.p.own_pairs);
-    const int sms = device_sm_count();
-    e = launch_pdl(attn_tree_kernel<E4M3>, dim3(unsigned(jobs < sms ? jobs : sms)), dim3(Form<E4M3>::threads), kSmemBytes<E4M3>,
-                   s, k);
-    if (e != cudaSuccess) return e;
+    const AttnTreeArgs &a = k.a;
     // Vectors of a CTA of the sum: no more than 16 nodes, two a warp (64 x 64 nodes of one head, 8 vectors: 23 us in all, 32: 27;
     // 40 x 20 of three, 8: 30, 32: 23).  Columns split where there are fewer CTAs than kSplitCtas
     // (3 x 41 nodes, 84 CTAs, over own 12007 entries: 32 us, 43 without; 5 x 24, 240 CTAs: 53, 44 without).
@@ -897,6 +915,8 @@ static cudaError_t launch_form(const AttnTreeArgs &a, KernelArgs &k, cudaStream_
     return join(attn_tree_join_kernel<E4M3, 32, 1>, 32, 1, sizeof(JoinShared<32>));
 }
 
+}  // namespace
+
 cudaError_t launch_attn_tree(const AttnTreeArgs &a, cudaStream_t s, const char **why) {
     KernelArgs k{};
     k.a = a;
@@ -909,30 +929,35 @@ cudaError_t launch_attn_tree(const AttnTreeArgs &a, cudaStream_t s, const char *
     k.values = reinterpret_cast<float *>(expanded + 2 * half);
     k.ml = reinterpret_cast<float2 *>(k.values + slots * kHeadDim);
     const bool e4m3 = a.own.format == kKvE4m3;
-    if (!encode_tiles(&k.map[4], a.q, {cuuint64_t(kHeadDim), cuuint64_t(a.own.n_kv) * a.group, cuuint64_t(k.p.rows)},
-                      {cuuint64_t(kHeadDim) * 2, cuuint64_t(a.ldq) * 2},
-                      {64, cuuint32_t(a.group), cuuint32_t(k.p.rows_tile)}, CU_TENSOR_MAP_SWIZZLE_128B, why))
-        return cudaErrorInvalidValue;
-    if (!e4m3) {
-        const KvBatch &pre = a.prefix_len > 0 ? a.prefix : a.own;
-        const int pre_rows = a.prefix_len > 0 ? a.prefix_len : a.own.max_len;
-        if (!encode_cache(&k.map[0], pre.k, pre_rows, pre.max_len, pre.n_kv, why) ||
-            !encode_cache(&k.map[1], pre.v, pre_rows, pre.max_len, pre.n_kv, why) ||
-            !encode_cache(&k.map[2], a.own.k, a.own.max_len, a.own.max_len, a.own.n_seq * a.own.n_kv, why) ||
-            !encode_cache(&k.map[3], a.own.v, a.own.max_len, a.own.max_len, a.own.n_seq * a.own.n_kv, why))
-            return cudaErrorInvalidValue;
+    bool ok = encode_tiles(&k.map[4], a.q, {cuuint64_t(kHeadDim), cuuint64_t(a.own.n_kv) * a.group, cuuint64_t(k.p.rows)},
+                           {cuuint64_t(kHeadDim) * 2, cuuint64_t(a.ldq) * 2},
+                           {64, cuuint32_t(a.group), cuuint32_t(k.p.rows_tile)}, CU_TENSOR_MAP_SWIZZLE_128B, why);
+    if (a.prefix_len > 0 && (!e4m3 || k.p.expanded)) {
+        const void *pk = e4m3 ? expanded : a.prefix.k, *pv = e4m3 ? expanded + half : a.prefix.v;
+        const int len = e4m3 ? expanded_len(a.prefix_len) : a.prefix.max_len;
+        ok = ok && encode_cache(&k.map[0], pk, a.prefix_len, len, a.own.n_kv, why) &&
+             encode_cache(&k.map[1], pv, a.prefix_len, len, a.own.n_kv, why);
     }
+    if (!e4m3)
+        ok = ok && encode_cache(&k.map[2], a.own.k, a.own.max_len, a.own.max_len, a.own.n_seq * a.own.n_kv, why) &&
+             encode_cache(&k.map[3], a.own.v, a.own.max_len, a.own.max_len, a.own.n_seq * a.own.n_kv, why);
+    if (!ok) return cudaErrorInvalidValue;
+    cudaError_t e;
     if (k.p.expanded) {
-        const int len = expanded_len(a.prefix_len);
-        if (!encode_cache(&k.map[0], expanded, a.prefix_len, len, a.own.n_kv, why) ||
-            !encode_cache(&k.map[1], expanded + half, a.prefix_len, len, a.own.n_kv, why))
-            return cudaErrorInvalidValue;
         const dim3 grid((a.prefix_len + kExpandEntries - 1) / kExpandEntries, a.own.n_kv, 2);
-        const cudaError_t e = launch_pdl(expand_prefix_kernel, grid, dim3(256), 0, s, a.prefix, a.prefix_len, len,
-                                         reinterpret_cast<uint4 *>(expanded), reinterpret_cast<uint4 *>(expanded + half));
-        if (e != cudaSuccess) return e;
+        e = launch_pdl(expand_prefix_kernel, grid, dim3(256), 0, s, a.prefix, a.prefix_len, expanded_len(a.prefix_len),
+                       reinterpret_cast<uint4 *>(expanded), reinterpret_cast<uint4 *>(expanded + half));
+        if (e == cudaSuccess) e = launch_parts<false>(k, true, false, false, s);
+        if (e == cudaSuccess) {
+            ++k.next;       // each grid has its counter
+            e = launch_parts<true>(k, false, true, true, s);
+            --k.next;
+        }
+    } else {
+        e = e4m3 ? launch_parts<true>(k, true, true, false, s) : launch_parts<false>(k, true, true, false, s);
     }
-    return e4m3 ? launch_form<true>(a, k, s) : launch_form<false>(a, k, s);
+    if (e != cudaSuccess) return e;
+    return e4m3 ? launch_join<true>(k, s) : launch_join<false>(k, s);
 }
 
 }  // namespace tfk
