@@ -641,34 +641,45 @@ struct __align__(16) JoinShared {
     uint4 v[VECS < kJoinWarps ? VECS : kJoinWarps][kMaxPath][16];      // a node's near values, chunk c of row t at c XOR (t % 8)
 };
 
-// One node's near entries; whole warp.  Rows of the products are the group's heads, a lane's are lane / 4 and that + 8.
-template <bool E4M3, int VECS>
-__device__ void near_entries(const AttnTreeArgs &a, JoinShared<VECS> *sh, int row, int j, int nth, uint4 (*s_v)[16]) {
-    const int lane = threadIdx.x & 31, g = a.group, r = lane >> 2, c4 = lane & 3;
-    const int b = idx_div(row, a.n), node = row - b * a.n;
-    const long long pos = seq_position(a.pos, b, a.n, a.own.max_len, a.err, false);
-    const int32_t *parents = a.parents + (size_t)b * a.n;
+// Where a node is in its tree.  Lane i holds nodes i and i + 32.
+struct Node {
+    int b, node, depth;     // depth -1: idle sequence, no tree or unused row
+    long long pos;
+    int above[2];           // parents (the root's: itself)
+};
+
+// Whole warp.
+__device__ __forceinline__ Node find_node(const AttnTreeArgs &a, int row, bool report) {
+    const int lane = threadIdx.x & 31;
+    Node t;
+    t.b = idx_div(row, a.n);
+    t.node = row - t.b * a.n;
+    t.pos = seq_position(a.pos, t.b, a.n, a.own.max_len, a.err, false);
+    const int32_t *parents = a.parents + (size_t)t.b * a.n;
     int d[2];
     const bool tree = tree_depths(parents, a.n, d);
-    if (!tree && pos >= 0 && node == 0 && j == 0 && lane == 0) set_error(a.err, kDevBadTree);
+    if (!tree && t.pos >= 0 && t.node == 0 && report && lane == 0) set_error(a.err, kDevBadTree);
+    const int lo = __shfl_sync(0xFFFFFFFFu, d[0], t.node & 31), hi = __shfl_sync(0xFFFFFFFFu, d[1], t.node & 31);
+    t.depth = tree && t.pos >= 0 ? (t.node < 32 ? lo : hi) : -1;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) t.above[h] = lane + 32 * h < a.n ? max(0, parents[lane + 32 * h]) : 0;
+    return t;
+}
+
+// One node's near entries; whole warp.  Rows of the products are the group's heads, a lane's are lane / 4 and that + 8.
+template <bool E4M3, int VECS>
+__device__ void near_entries(const AttnTreeArgs &a, JoinShared<VECS> *sh, const Node &t, int j, int nth, uint4 (*s_v)[16]) {
+    const int lane = threadIdx.x & 31, g = a.group, r = lane >> 2, c4 = lane & 3, b = t.b, row = t.b * a.n + t.node;
+    const long long pos = t.pos;
     auto of = [](const int (&v)[2], int i) {
         const int lo = __shfl_sync(0xFFFFFFFFu, v[0], i & 31), hi = __shfl_sync(0xFFFFFFFFu, v[1], i & 31);
         return i < 32 ? lo : hi;
     };
-    const int depth = of(d, node);
-    const bool none = !tree || pos < 0 || depth < 0;
-    if (lane == 0) sh->depth[nth] = none ? -1 : depth;
-    if (none) return;
     // lane t < near: the entry at own position first + t, of a node `up` steps above where it is one of the path
-    const int near = int(min((long long)kMaxPath, pos + depth + 1));
-    const long long first = pos + depth + 1 - near;
-    int up = max(0, near - 1 - lane), at = node;
-    int above[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int i = lane + 32 * h;
-        above[h] = i < a.n ? max(0, parents[i]) : 0;
-    }
+    const int near = int(min((long long)kMaxPath, pos + t.depth + 1));
+    const long long first = pos + t.depth + 1 - near;
+    int up = max(0, near - 1 - lane), at = t.node;
+    int above[2] = {t.above[0], t.above[1]};
 #pragma unroll
     for (int s = 0; s < 4; ++s) {       // above: 2^s steps
         const int higher = of(above, at);
@@ -707,9 +718,9 @@ __device__ void near_entries(const AttnTreeArgs &a, JoinShared<VECS> *sh, int ro
     }
 #pragma unroll
     for (int i = 0; i < kMaxPath / 2; ++i) {
-        const int t = 2 * i + (lane >> 4), c = lane & 15;
-        const size_t e = base + __shfl_sync(0xFFFFFFFFu, my_entry, t);
-        s_v[t][c ^ (t & 7)] = t < near ? cache_chunk<E4M3>(a.own.v, a.own.v_scale, e, c) : make_uint4(0u, 0u, 0u, 0u);
+        const int key = 2 * i + (lane >> 4), c = lane & 15;
+        const size_t e = base + __shfl_sync(0xFFFFFFFFu, my_entry, key);
+        s_v[key][c ^ (key & 7)] = key < near ? cache_chunk<E4M3>(a.own.v, a.own.v_scale, e, c) : make_uint4(0u, 0u, 0u, 0u);
     }
     __syncwarp();
     // weights: s[n][2h + i] is head r + 8h and key 8n + 2 c4 + i
@@ -740,12 +751,12 @@ __device__ void near_entries(const AttnTreeArgs &a, JoinShared<VECS> *sh, int ro
         if (c4 == 0 && r + 8 * h < g) sh->ml[nth * g + r + 8 * h] = make_float2(m, l);
     }
     // outputs, 16 columns at a time
-    const int t = lane & 15;
-    const uint32_t v_row = smem_u32(&s_v[t][0]);
+    const int key = lane & 15;
+    const uint32_t v_row = smem_u32(&s_v[key][0]);
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
         uint32_t v[4];      // keys 0-7 and 8-15 of columns 16n .., then of columns 16n + 8 ..
-        ldsm_x4_trans(v_row + 16 * ((2 * n + (lane >> 4)) ^ (t & 7)), v);
+        ldsm_x4_trans(v_row + 16 * ((2 * n + (lane >> 4)) ^ (key & 7)), v);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             float o[4] = {0.f, 0.f, 0.f, 0.f};
@@ -758,8 +769,8 @@ __device__ void near_entries(const AttnTreeArgs &a, JoinShared<VECS> *sh, int ro
     __syncwarp();       // the next node's values may come
 }
 
-template <bool E4M3, int VECS, int SPLIT>
-__global__ void __launch_bounds__(kJoinThreads, 2) attn_tree_join_kernel(AttnTreeArgs a, Plan p, const float *results,
+template <bool E4M3, int VECS, int SPLIT, int BLOCKS>
+__global__ void __launch_bounds__(kJoinThreads, BLOCKS) attn_tree_join_kernel(AttnTreeArgs a, Plan p, const float *results,
                                                                          const float2 *ml, unsigned *next) {
     constexpr int kQuads = VECS / 8 / SPLIT;        // a thread's: `quad` and the ones after it
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -767,8 +778,17 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_tree_join_kernel(AttnTre
     const int warp = threadIdx.x >> 5, g = a.group, j = blockIdx.y, n_kv = a.own.n_kv;
     const int mine = threadIdx.x % VECS, quad = (blockIdx.z * (kJoinThreads / VECS) + threadIdx.x / VECS) * kQuads;
     const int nodes = VECS / g, row0 = blockIdx.x * nodes, here = min(nodes, p.rows - row0), n_vec = p.rows * g;
-    for (int i = warp; i < here; i += kJoinWarps) near_entries<E4M3>(a, sh, row0 + i, j, i, sh->v[warp]);
+    Node t{};
+    for (int i = warp; i < here; i += kJoinWarps) {
+        t = find_node(a, row0 + i, j == 0 && blockIdx.z == 0);
+        if ((threadIdx.x & 31) == 0) sh->depth[i] = t.depth;
+    }
     __syncthreads();
+    // warps without a node go on meanwhile
+    for (int i = warp; i < here; i += kJoinWarps) {
+        if (warp + kJoinWarps < here) t = find_node(a, row0 + i, false);        // not the one just found
+        if (t.depth >= 0) near_entries<E4M3>(a, sh, t, j, i, sh->v[warp]);
+    }
     // The results come from the attention grid; all else from before it, which it had
     // waited for when it let this grid start.
     grid_dependency_wait();
@@ -779,6 +799,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_tree_join_kernel(AttnTre
     float l = 1.f;
 #pragma unroll
     for (int i = 0; i < kQuads; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float m = -INFINITY;
     if (depth >= 0) {
         const long long far = a.pos[idx_div(row0 + nth, a.n)] + depth + 1 - kMaxPath;       // own entries that lie farther
         const int n = p.n_parts + (far > 0 ? int((far + kOwnPart - 1) / kOwnPart) : 0);
@@ -786,7 +807,6 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_tree_join_kernel(AttnTre
         const float2 *my_ml = ml + (size_t)j * n_vec + v;
         const float4 *x = reinterpret_cast<const float4 *>(results) + ((size_t)j * 32 + quad) * n_vec + v;
         const size_t step = (size_t)n_kv * n_vec;
-        float m = -INFINITY;
         l = 0.f;
         auto add = [&](const float2 &part, const float4 (&y)[kQuads]) {
             const Factors f = factors(m, part.x);
@@ -795,7 +815,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_tree_join_kernel(AttnTre
 #pragma unroll
             for (int i = 0; i < kQuads; ++i) sum[i] = fold(f, sum[i], y[i]);
         };
-        constexpr int kAhead = 16 / kQuads;
+        constexpr int kAhead = (BLOCKS == 2 ? 16 : 8) / kQuads;     // slots on their way
         float2 w[kAhead];
         float4 y[kAhead][kQuads];
         for (int c = 0; c < n; c += kAhead) {
@@ -812,9 +832,14 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_tree_join_kernel(AttnTre
             for (int u = 0; u < kAhead; ++u)
                 if (c + u < n) add(w[u], y[u]);
         }
+    }
+    __syncthreads();    // the near entries' results are there
+    if (depth >= 0) {
+        const Factors f = factors(m, sh->ml[mine].x);
+        l = fold(f, l, sh->ml[mine].y);
 #pragma unroll
-        for (int i = 0; i < kQuads; ++i) y[0][i] = *reinterpret_cast<const float4 *>(&sh->near[mine][4 * (quad + i)]);
-        add(sh->ml[mine], y[0]);
+        for (int i = 0; i < kQuads; ++i)
+            sum[i] = fold(f, sum[i], *reinterpret_cast<const float4 *>(&sh->near[mine][4 * (quad + i)]));
     }
     __syncthreads();    // the near outputs are read
     uint16_t *const rows = reinterpret_cast<uint16_t *>(&sh->near[0][0]);
@@ -892,9 +917,9 @@ cudaError_t launch_join(const KernelArgs &k, cudaStream_t s) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices || !opted_in[dev]) {
-        e = cudaFuncSetAttribute(attn_tree_join_kernel<E4M3, 32, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(JoinShared<32>)));
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(attn_tree_join_kernel<E4M3, 32, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(JoinShared<32>)));
+        for (const auto kernel : {attn_tree_join_kernel<E4M3, 32, 4, 2>, attn_tree_join_kernel<E4M3, 32, 1, 2>, attn_tree_join_kernel<E4M3, 32, 1, 3>})
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(JoinShared<32>)));
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < kMaxDevices) opted_in[dev] = true;
     }
@@ -902,17 +927,18 @@ cudaError_t launch_join(const KernelArgs &k, cudaStream_t s) {
     // Vectors of a CTA of the sum: no more than 16 nodes, two a warp (64 x 64 nodes of one head, 8 vectors: 23 us in all, 32: 27;
     // 40 x 20 of three, 8: 30, 32: 23).  Columns split where there are fewer CTAs than kSplitCtas
     // (3 x 41 nodes, 84 CTAs, over own 12007 entries: 32 us, 43 without; 5 x 24, 240 CTAs: 53, 44 without).
-    constexpr int kSplitCtas = 100;
-    auto join = [&](auto kernel, int vecs, int split, size_t smem) {
-        const int nodes = vecs / a.group;
-        return launch_pdl(kernel, dim3((k.p.rows + nodes - 1) / nodes, a.own.n_kv, split), dim3(kJoinThreads), smem, s, a, k.p,
+    // Three CTAs an SM, with half the loads on their way, from kFullCtas on (24 x 64, 3072 CTAs: 1066 us, 1078 with
+    // two; 5 x 24: 45, 44 with two).
+    constexpr int kSplitCtas = 100, kFullCtas = 456;
+    const int vecs = a.group == 1 ? 8 : 32, nodes = vecs / a.group, ctas = (k.p.rows + nodes - 1) / nodes * a.own.n_kv;
+    auto join = [&](auto kernel, int split, size_t smem) {
+        return launch_pdl(kernel, dim3(ctas / a.own.n_kv, a.own.n_kv, split), dim3(kJoinThreads), smem, s, a, k.p,
                           (const float *)k.values, (const float2 *)k.ml, k.next);
     };
-    if (a.group == 1) return join(attn_tree_join_kernel<E4M3, 8, 1>, 8, 1, sizeof(JoinShared<8>));
-    const int nodes = 32 / a.group;
-    if ((k.p.rows + nodes - 1) / nodes * a.own.n_kv < kSplitCtas)
-        return join(attn_tree_join_kernel<E4M3, 32, 4>, 32, 4, sizeof(JoinShared<32>));
-    return join(attn_tree_join_kernel<E4M3, 32, 1>, 32, 1, sizeof(JoinShared<32>));
+    if (vecs == 8) return join(attn_tree_join_kernel<E4M3, 8, 1, 2>, 1, sizeof(JoinShared<8>));
+    if (ctas < kSplitCtas) return join(attn_tree_join_kernel<E4M3, 32, 4, 2>, 4, sizeof(JoinShared<32>));
+    if (ctas < kFullCtas) return join(attn_tree_join_kernel<E4M3, 32, 1, 2>, 1, sizeof(JoinShared<32>));
+    return join(attn_tree_join_kernel<E4M3, 32, 1, 3>, 1, sizeof(JoinShared<32>));
 }
 
 }  // namespace
