@@ -134,23 +134,26 @@ __device__ void mend_tiles(SHARED *sh, uint8_t *v_tiles) {
         uint8_t *v = v_tiles + size_t(m.stage) * kKeyBytes + (c >> 3) * kKeyHalf;
         auto at = [&](int row) { return reinterpret_cast<uint4 *>(v + row * 128 + (((c & 7) ^ (row & 7)) << 4)); };
         const int end = (m.valid + 15) & ~15;
-        bool bad = false;
+        // Nearly always there is nothing to mend, and the outputs wait for knowing it.
+        uint32_t found = 0u;
         for (int row0 = m.first + (lane >> 4); row0 < m.valid; row0 += 2 * kAtOnce) {
             uint4 x[kAtOnce];
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i)
-                x[i] = row0 + 2 * i < m.valid ? *at(row0 + 2 * i) : make_uint4(0u, 0u, 0u, 0u);
+                x[i] = *at(min(row0 + 2 * i, m.valid - 1));
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-                if (bf16x2_nonfinite(x[i].x) || bf16x2_nonfinite(x[i].y) || bf16x2_nonfinite(x[i].z) || bf16x2_nonfinite(x[i].w)) {
-                    *at(row0 + 2 * i) = make_uint4(bf16x2_finite(x[i].x), bf16x2_finite(x[i].y), bf16x2_finite(x[i].z),
-                                                   bf16x2_finite(x[i].w));
-                    bad = true;
-                }
+            for (int i = 0; i < kAtOnce; ++i)
+                found |= bf16x2_nonfinite_bits(x[i].x) | bf16x2_nonfinite_bits(x[i].y) | bf16x2_nonfinite_bits(x[i].z) |
+                         bf16x2_nonfinite_bits(x[i].w);
+        }
+        if (found & kNonfiniteBits) {
+            for (int row = m.first + (lane >> 4); row < m.valid; row += 2) {
+                const uint4 x = *at(row);
+                *at(row) = make_uint4(bf16x2_finite(x.x), bf16x2_finite(x.y), bf16x2_finite(x.z), bf16x2_finite(x.w));
             }
+            *reinterpret_cast<volatile int *>(&sh->bad[m.slot]) = 1;
         }
         for (int row = m.valid + (lane >> 4); row < end; row += 2) *at(row) = make_uint4(0u, 0u, 0u, 0u);
-        if (bad) *reinterpret_cast<volatile int *>(&sh->bad[m.slot]) = 1;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->v_full[m.stage]);

@@ -58,6 +58,10 @@ __device__ __forceinline__ void st_global_32(void *p, const uint32_t *v) {
 __device__ __forceinline__ bool bf16x2_nonfinite(uint32_t w) {
     return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
 }
+// The same as bits: the sum carries into kNonfiniteBits where a half's exponent is all ones, and the halves do not
+// meet.  The other bits are anything.
+constexpr uint32_t kNonfiniteBits = 0x80008000u;
+__device__ __forceinline__ uint32_t bf16x2_nonfinite_bits(uint32_t w) { return (w & 0x7F807F80u) + 0x00800080u; }
 __device__ __forceinline__ uint32_t bf16x2_finite(uint32_t w) {   // non-finite halves -> 0
     if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
     if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
