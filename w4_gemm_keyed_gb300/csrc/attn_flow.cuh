@@ -125,7 +125,7 @@ struct Ring {
 template <typename SHARED>
 __device__ void mend_tiles(SHARED *sh, uint8_t *v_tiles) {
     const int lane = threadIdx.x & 31, c = lane & 15;
-    constexpr int kAtOnce = 8;          // pairs of rows
+    constexpr int kAtOnce = 4;          // pairs of rows
     for (unsigned n = 0;; ++n) {
         const int slot = n % kMends;
         if (!warp_wait(sh, &sh->mend_full[slot], (n / kMends) & 1)) return;
@@ -136,6 +136,7 @@ __device__ void mend_tiles(SHARED *sh, uint8_t *v_tiles) {
         const int end = (m.valid + 15) & ~15;
         // Nearly always there is nothing to mend, and the outputs wait for knowing it.
         uint32_t found = 0u;
+#pragma unroll 1
         for (int row0 = m.first + (lane >> 4); row0 < m.valid; row0 += 2 * kAtOnce) {
             uint4 x[kAtOnce];
 #pragma unroll
@@ -147,12 +148,14 @@ __device__ void mend_tiles(SHARED *sh, uint8_t *v_tiles) {
                          bf16x2_nonfinite_bits(x[i].w);
         }
         if (found & kNonfiniteBits) {
+#pragma unroll 1
             for (int row = m.first + (lane >> 4); row < m.valid; row += 2) {
                 const uint4 x = *at(row);
                 *at(row) = make_uint4(bf16x2_finite(x.x), bf16x2_finite(x.y), bf16x2_finite(x.z), bf16x2_finite(x.w));
             }
             *reinterpret_cast<volatile int *>(&sh->bad[m.slot]) = 1;
         }
+#pragma unroll 1
         for (int row = m.valid + (lane >> 4); row < end; row += 2) *at(row) = make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
         __syncwarp();

@@ -269,17 +269,17 @@ __device__ void store_outputs(const KernelArgs &k, Shared *sh, uint32_t tmem) {
     const int g = k.a.group, my_row = v / g;
     const size_t place = (size_t)my_row * k.a.ldo + (size_t)(v - my_row * g) * kHeadDim;
     const bool sectors = ((reinterpret_cast<uintptr_t>(k.a.out) | size_t(k.a.ldo) * 2) & 31) == 0;
-    unsigned uses[2] = {0, 0};
+    unsigned uses0 = 0, uses1 = 0;
     for (unsigned n = 0;; ++n) {
         const int slot = n % kRing;
         if (!warp_wait(sh, &sh->item_full[slot], (n / kRing) & 1)) return;
         const Item it = sh->item[slot];
         if (it.n_rows == 0) return;
-#pragma unroll
+#pragma unroll 1
         for (int t = 0; t < 2; ++t) {
             const int n_here = min(k.rows_tile, it.n_rows - t * k.rows_tile);
             if (n_here <= 0) continue;
-            const unsigned use = uses[t]++;
+            const unsigned use = t ? uses1++ : uses0++;
             if (!warp_wait(sh, &sh->l_full[use & 1][t], (use >> 1) & 1) || !warp_wait(sh, &sh->o_last[t], use & 1)) return;
             if (32 * quarter < n_here * g) {
                 tc_fence_after();
@@ -287,7 +287,7 @@ __device__ void store_outputs(const KernelArgs &k, Shared *sh, uint32_t tmem) {
                 const float inv = __frcp_rn(sh->l[use & 1][t][v]);
                 const int row0 = it.seq0 + it.i0 + t * k.rows_tile;
                 uint16_t *const out = k.a.out + (size_t)row0 * k.a.ldo + (size_t)it.j * g * kHeadDim + place;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t o[32], w[16];
                     tc_ld32(t_o + 32 * c, o);
