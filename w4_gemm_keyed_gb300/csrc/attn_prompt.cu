@@ -27,7 +27,8 @@ using namespace flow;
 
 constexpr int kStages = 3;              // K tiles, and V tiles, in shared memory
 constexpr int kQueries = 3;             // query tiles in shared memory
-constexpr int kProducerWarp = 8, kScoreWarp = 9, kOutputWarp = 10, kMendWarp = 11;
+static_assert(kQueries == kStages, "one ring length");
+constexpr int kProducerWarp = 8, kScoreWarp = 9, kMendWarp = 11;
 constexpr int kStoreWarp = 12, kStoreWarps = 4;
 constexpr int kCtaThreads = 512;
 constexpr int kRegsSoftmax = 168, kRegsOther = 88;
@@ -48,65 +49,53 @@ struct KernelArgs {
     unsigned *next;     // items taken beyond the first of each CTA, and CTAs done; both zero between calls
 };
 
-struct __align__(16) Shared : SharedBase<Item, kStages, kStages, kQueries> {
-    // Of a tile's latest two items: the sums of the next item may follow before these are
-    // looked at, but not those of the one after.
-    uint64_t l_full[2][2];
-    float l[2][2][kTile];
-};
-constexpr size_t kSmemBytes = size_t(kQueries) * kTileBytes + size_t(2 * kStages) * kKeyBytes + sizeof(Shared);
-static_assert(kSmemBytes <= 227 * 1024, "shared memory");
-
 // ------------------------------------------------------------------ item order
 // Items in descending order of their place in their sequences (so of their cost):
 // level by level, at each level the sequences that reach it, heads fastest.  The set
 // of sequences that reach a level changes only where one of them ends, so a whole run of levels is
 // found with one pass over the sequences.  A warp's work, in step.
+struct Sequences {      // in shared memory
+    int start[kMaxSeqs + 1], levels[kMaxSeqs];      // first rows; items a head
+};
+
+struct __align__(16) Shared : SharedBase<Item, kStages, kStages, kQueries> {
+    // Of a tile's latest two items: the sums of the next item may follow before these are
+    // looked at, but not those of the one after.
+    uint64_t l_full[2][2];
+    float l[2][2][kTile];
+    Sequences sequences;
+};
+constexpr size_t kSmemBytes = size_t(kQueries) * kTileBytes + size_t(2 * kStages) * kKeyBytes + sizeof(Shared);
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
 struct Finder {
-    static constexpr int kHeld = 2;         // sequences a lane keeps in registers: the first 64 in all
     const KernelArgs &k;
-    int held[kHeld], start[kHeld], rows[kHeld];     // their items a head, first rows and lengths
+    Sequences &all;
     int next_level, high, count;
     unsigned first, end;
 
-    __device__ int levels(int n) const { return int(idx_div(unsigned(n) + k.rows_item - 1, k.rows_item)); }    // of n rows
-    // f(items a head, first row, length) of this lane's sequences, 32 in step, until f says true
-    template <typename F>
-    __device__ void each(F f) const {
-        const int lane = threadIdx.x & 31;
-#pragma unroll
-        for (int h = 0; h < kHeld; ++h)
-            if (f(held[h], start[h], rows[h])) return;
-        for (int s0 = 32 * kHeld; s0 < k.a.n_seq; s0 += 32) {
-            const int s = s0 + lane;
-            const int x = s < k.a.n_seq ? int(k.a.starts[s]) : 0, n = s < k.a.n_seq ? int(k.a.starts[s + 1]) - x : 0;
-            if (f(levels(n), x, n)) return;
-        }
-    }
     // Whole warp.  Starts that fall or lie outside the rows: no items.
-    __device__ explicit Finder(const KernelArgs &args) : k(args), held{}, start{}, rows{}, next_level(-1), high(0), count(0), first(0), end(0) {
+    __device__ Finder(const KernelArgs &args, Sequences &place) : k(args), all(place), next_level(-1), high(0), count(0), first(0), end(0) {
         const int lane = threadIdx.x & 31;
         bool bad = false;
+        int top = 0;
+#pragma unroll 1
         for (int s = lane; s < k.a.n_seq; s += 32) {
             const long long x = k.a.starts[s], y = k.a.starts[s + 1];
-            bad |= x < 0 || y < x || y > k.a.rows;
+            if (x < 0 || y < x || y > k.a.rows) {
+                bad = true;
+                continue;
+            }
+            all.start[s] = int(x);
+            if (s + 1 == k.a.n_seq) all.start[s + 1] = int(y);
+            all.levels[s] = int(idx_div(unsigned(y - x) + k.rows_item - 1, k.rows_item));
+            top = max(top, all.levels[s]);
         }
+        __syncwarp();
         if (__any_sync(0xFFFFFFFFu, bad)) {
             if (blockIdx.x == 0 && lane == 0) set_error(k.a.err, kDevBadPosition);
             return;
         }
-#pragma unroll
-        for (int h = 0; h < kHeld; ++h)
-            if (lane + 32 * h < k.a.n_seq) {
-                start[h] = int(k.a.starts[lane + 32 * h]);
-                rows[h] = int(k.a.starts[lane + 32 * h + 1]) - start[h];
-                held[h] = levels(rows[h]);
-            }
-        int top = 0;
-        each([&](int n, int, int) {
-            top = max(top, n);
-            return false;
-        });
         next_level = __reduce_max_sync(0xFFFFFFFFu, top) - 1;
     }
     // Whole warp; i never falls from call to call.
@@ -116,13 +105,14 @@ struct Finder {
         while (i >= end) {
             if (next_level < 0) return it;
             int more = 0, below = 0;
-            each([&](int n, int, int) {
+#pragma unroll 1
+            for (int s = lane; s < k.a.n_seq; s += 32) {
+                const int n = all.levels[s];
                 if (n > next_level)
                     ++more;
                 else
                     below = max(below, n);
-                return false;
-            });
+            }
             count = __reduce_add_sync(0xFFFFFFFFu, more);
             below = __reduce_max_sync(0xFFFFFFFFu, below);
             first = end;
@@ -135,21 +125,21 @@ struct Finder {
         int nth = int(idx_div(rest, k.a.n_kv));
         it.j = int(rest) - nth * k.a.n_kv;
         it.i0 = (high - int(down)) * k.rows_item;
-        each([&](int n, int x, int len) {       // the nth sequence that reaches the level
-            const unsigned reach = __ballot_sync(0xFFFFFFFFu, n > high);
+#pragma unroll 1
+        for (int s0 = 0;; s0 += 32) {       // the nth sequence that reaches the level
+            unsigned reach = __ballot_sync(0xFFFFFFFFu, s0 + lane < k.a.n_seq && all.levels[min(s0 + lane, kMaxSeqs - 1)] > high);
             const int here = __popc(reach);
-            if (nth < here) {
-                const bool me = n > high && __popc(reach & ((1u << lane) - 1u)) == nth;
-                const int from = __ffs(__ballot_sync(0xFFFFFFFFu, me)) - 1;
-                it.seq0 = __shfl_sync(0xFFFFFFFFu, x, from);
-                it.n_rows = min(k.rows_item, __shfl_sync(0xFFFFFFFFu, len, from) - it.i0);
-                it.n_keys = it.i0 + it.n_rows;
-                return true;
+            if (nth >= here) {
+                nth -= here;
+                continue;
             }
-            nth -= here;
-            return false;
-        });
-        return it;
+            const bool me = (reach >> lane & 1u) && __popc(reach & ((1u << lane) - 1u)) == nth;
+            const int s = s0 + __ffs(__ballot_sync(0xFFFFFFFFu, me)) - 1;
+            it.seq0 = all.start[s];
+            it.n_rows = min(k.rows_item, all.start[s + 1] - it.seq0 - it.i0);
+            it.n_keys = it.i0 + it.n_rows;
+            return it;
+        }
     }
 };
 
@@ -164,22 +154,22 @@ struct Finder {
 
 __device__ void produce(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint8_t *stages) {
     const int lane = threadIdx.x & 31, g = k.a.group;
-    Finder finder(k);
+    Finder finder(k, sh->sequences);
     unsigned i = blockIdx.x;
-    unsigned loaded_k = 0, loaded_v = 0, queries = 0;   // tiles so far
+    unsigned queries = 0, keys = 0, values = 0;     // tiles so far
     unsigned mended = 0;            // of them V tiles to mend
     unsigned to_mend = 0;           // bit st: the last tile of V stage st is one
     bool ok = true;
     // One thread.  The stage of a ring's next tile, once it is free.
-    auto room = [&](uint64_t *empty, unsigned n, int stages_of) {
-        const int st = n % stages_of;
-        ok = ok && (n < unsigned(stages_of) || lane_wait(sh, &empty[st], (n / stages_of - 1) & 1));
+    auto room = [&](uint64_t *empty, unsigned n) {
+        const int st = n % kStages;
+        ok = ok && (n < unsigned(kStages) || lane_idle_wait(sh, &empty[st], (n / kStages - 1) & 1));
         return st;
     };
     for (unsigned n = 0;; ++n) {
         const int slot = n % kRing;
         const Item it = finder.find(i);
-        if (n >= kRing && !warp_wait(sh, &sh->item_empty[slot], (n / kRing - 1) & 1)) break;
+        if (n >= kRing && !warp_idle_wait(sh, &sh->item_empty[slot], (n / kRing - 1) & 1)) break;
         unsigned taken = 0;
         if (lane == 0) {
             sh->item[slot] = it;
@@ -193,8 +183,9 @@ __device__ void produce(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint8
             // A tile of queries is whole rows of the KV head's query heads, one box of (64
             // elements, heads, rows) per half.  Rows of the box past the item's
             // fill vectors that nothing reads: rows of a product never mix.
+#pragma unroll 1
             for (int t = 0; t < 2 && t * k.rows_tile < it.n_rows; ++t) {
-                const int buf = room(sh->q_empty, queries, kQueries);
+                const int buf = room(sh->q_empty, queries);
                 if (!ok) break;
                 ++queries;
                 const int row = it.seq0 + it.i0 + t * k.rows_tile;
@@ -202,23 +193,14 @@ __device__ void produce(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint8
                 tma_load_3d(q_tiles + buf * kTileBytes, &k.q, 0, it.j * g, row, &sh->q_full[buf]);
                 tma_load_3d(q_tiles + buf * kTileBytes + kHalfBytes, &k.q, 64, it.j * g, row, &sh->q_full[buf]);
             }
-            auto load = [&](const CUtensorMap *map, uint8_t *dst, int key, uint64_t *bar) {
-                mbar_arrive_expect_tx(bar, kKeyBytes);
-                tma_load_3d(dst, map, 0, it.j, it.seq0 + key, bar);
-                tma_load_3d(dst + kKeyHalf, map, 64, it.j, it.seq0 + key, bar);
-            };
-            for (int t = 0; t <= tiles && ok; ++t) {        // K(0), then K(t) and V(t - 1)
-                if (t < tiles) {
-                    const int st = room(sh->k_empty, loaded_k, kStages);
-                    if (!ok) break;
-                    ++loaded_k;
-                    load(&k.k, stages + size_t(st) * kKeyBytes, t * kKeys, &sh->k_full[st]);
-                }
-                if (t > 0) {
-                    const int st = room(sh->v_empty, loaded_v, kStages), key = (t - 1) * kKeys;
-                    if (!ok) break;
-                    ++loaded_v;
-                    uint64_t *bar = &sh->v_full[st];
+#pragma unroll 1
+            for (int u = 0; u < 2 * tiles && ok; ++u) {
+                const bool is_v = order_is_v(u, tiles);
+                const int key = order_tile(u, tiles) * kKeys, st = room(is_v ? sh->v_empty : sh->k_empty, is_v ? values : keys);
+                if (!ok) break;
+                uint64_t *bar = is_v ? &sh->v_full[st] : &sh->k_full[st];
+                if (is_v) {
+                    ++values;
                     const int first = max(0, it.i0 + 1 - key);
                     to_mend &= ~(1u << st);
                     if (first < kKeys) {        // past the first row's last key: handed over by the mender
@@ -227,8 +209,14 @@ __device__ void produce(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint8
                         to_mend |= 1u << st;
                         bar = &sh->mend_full[m];
                     }
-                    load(&k.v, stages + size_t(kStages + st) * kKeyBytes, key, bar);
+                } else {
+                    ++keys;
                 }
+                const CUtensorMap *map = is_v ? &k.v : &k.k;
+                uint8_t *dst = stages + size_t(is_v ? kStages + st : st) * kKeyBytes;
+                mbar_arrive_expect_tx(bar, kKeyBytes);
+                tma_load_3d(dst, map, 0, it.j, it.seq0 + key, bar);
+                tma_load_3d(dst + kKeyHalf, map, 64, it.j, it.seq0 + key, bar);
             }
         }
         __syncwarp();
@@ -237,12 +225,13 @@ __device__ void produce(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint8
     }
     if (lane != 0) return;
     // no copy outlives the CTA
-    auto drain = [&](uint64_t *full, unsigned n, int stages_of, unsigned except) {
-        for (unsigned t = n > unsigned(stages_of) ? n - stages_of : 0; t < n; ++t)
+    auto drain = [&](uint64_t *full, unsigned n, unsigned stages_of, unsigned except) {
+#pragma unroll 1
+        for (unsigned t = n > stages_of ? n - stages_of : 0; t < n; ++t)
             if (!(except >> (t % stages_of) & 1u)) wait_drained(&full[t % stages_of], (t / stages_of) & 1);
     };
-    drain(sh->k_full, loaded_k, kStages, 0u);
-    drain(sh->v_full, loaded_v, kStages, to_mend);
+    drain(sh->k_full, keys, kStages, 0u);
+    drain(sh->v_full, values, kStages, to_mend);
     drain(sh->mend_full, mended, kMends, 0u);
     drain(sh->q_full, queries, kQueries, 0u);
     sh->mend[mended % kMends].stage = -1;
@@ -272,7 +261,7 @@ __device__ void store_outputs(const KernelArgs &k, Shared *sh, uint32_t tmem) {
     unsigned uses0 = 0, uses1 = 0;
     for (unsigned n = 0;; ++n) {
         const int slot = n % kRing;
-        if (!warp_wait(sh, &sh->item_full[slot], (n / kRing) & 1)) return;
+        if (!warp_idle_wait(sh, &sh->item_full[slot], (n / kRing) & 1)) return;
         const Item it = sh->item[slot];
         if (it.n_rows == 0) return;
 #pragma unroll 1
@@ -280,7 +269,7 @@ __device__ void store_outputs(const KernelArgs &k, Shared *sh, uint32_t tmem) {
             const int n_here = min(k.rows_tile, it.n_rows - t * k.rows_tile);
             if (n_here <= 0) continue;
             const unsigned use = t ? uses1++ : uses0++;
-            if (!warp_wait(sh, &sh->l_full[use & 1][t], (use >> 1) & 1) || !warp_wait(sh, &sh->o_last[t], use & 1)) return;
+            if (!warp_idle_wait(sh, &sh->l_full[use & 1][t], (use >> 1) & 1) || !warp_idle_wait(sh, &sh->o_last[t], use & 1)) return;
             if (32 * quarter < n_here * g) {
                 tc_fence_after();
                 const uint32_t t_o = tmem + kTmemO + t * kHeadDim + (uint32_t(32 * quarter) << 16);

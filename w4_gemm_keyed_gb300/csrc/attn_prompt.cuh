@@ -9,6 +9,8 @@
 
 namespace tfk {
 
+constexpr int kMaxSeqs = 1024;
+
 struct AttnPromptArgs {
     const uint16_t *q, *k, *v;  // bf16 [rows][ldq], [rows][ldk], [rows][ldv]
     int ldq, ldk, ldv;

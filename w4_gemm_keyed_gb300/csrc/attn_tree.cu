@@ -32,7 +32,7 @@ constexpr int kPrefixItems = 76;        // of a batch that is one pair of tiles,
 constexpr int kSms = 152;
 constexpr int kExpandPairs = 2;         // pairs of query tiles from which on an E4M3 prefix is expanded first
 constexpr int kGroups = 128;            // entries of the table of own items
-constexpr int kProducerWarp = 8, kScoreWarp = 9, kOutputWarp = 10, kMendWarp = 11;
+constexpr int kProducerWarp = 8, kScoreWarp = 9, kMendWarp = 11;
 constexpr int kExpandWarp = 12, kExpandWarps = 4;       // E4M3: for K tiles, and as many for V tiles
 constexpr int kRawBytes = kKeys * kHeadDim;
 static_assert(kOwnPart % kKeys == 0 && kMinPrefixPart % kKeys == 0, "whole key tiles");
@@ -459,7 +459,7 @@ __device__ bool store_results(const KernelArgs &k, Shared<E4M3> *sh, uint32_t tm
         const size_t block = it.block;
         const int at = (it.row0 + t * k.p.rows_tile) * g + v;
         float4 *const out = reinterpret_cast<float4 *>(k.values) + block * 32 * n_vec + at;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
             uint32_t o[32];
             tc_ld32(t_o + 32 * c, o);

@@ -1046,6 +1046,7 @@ tf_status tf_attention_prompt(const uint16_t *q, int32_t ldq, const uint16_t *k,
                               int32_t n_seq, uint16_t *out, int32_t ldo, void *ws, size_t ws_bytes, void *stream) {
     if (group < 1 || group > 16) return fail(TF_ERR_UNSUPPORTED, "group=%d outside [1, 16]", group);
     if (n_kv < 1 || n_kv > 128) return fail(TF_ERR_UNSUPPORTED, "n_kv=%d outside [1, 128]", n_kv);
+    static_assert(TF_MAX_SEQS == kMaxSeqs, "room for the starts");
     if (n_seq < 1 || n_seq > TF_MAX_SEQS) return fail(TF_ERR_UNSUPPORTED, "n_seq=%d outside [1, %d]", n_seq, TF_MAX_SEQS);
     if (rows < 0) return fail(TF_ERR_INVALID_ARG, "rows=%d must be >= 0", rows);
     const int n_q = n_kv * group;
