@@ -193,14 +193,24 @@ __device__ void produce(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint8
                 tma_load_3d(q_tiles + buf * kTileBytes, &k.q, 0, it.j * g, row, &sh->q_full[buf]);
                 tma_load_3d(q_tiles + buf * kTileBytes + kHalfBytes, &k.q, 64, it.j * g, row, &sh->q_full[buf]);
             }
+            auto load = [&](const CUtensorMap *map, uint8_t *dst, int key, uint64_t *bar) {
+                mbar_arrive_expect_tx(bar, kKeyBytes);
+                tma_load_3d(dst, map, 0, it.j, it.seq0 + key, bar);
+                tma_load_3d(dst + kKeyHalf, map, 64, it.j, it.seq0 + key, bar);
+            };
 #pragma unroll 1
-            for (int u = 0; u < 2 * tiles && ok; ++u) {
-                const bool is_v = order_is_v(u, tiles);
-                const int key = order_tile(u, tiles) * kKeys, st = room(is_v ? sh->v_empty : sh->k_empty, is_v ? values : keys);
-                if (!ok) break;
-                uint64_t *bar = is_v ? &sh->v_full[st] : &sh->k_full[st];
-                if (is_v) {
+            for (int t = 0; t <= tiles && ok; ++t) {        // K(0), then K(t) and V(t - 1)
+                if (t < tiles) {
+                    const int st = room(sh->k_empty, keys);
+                    if (!ok) break;
+                    ++keys;
+                    load(&k.k, stages + size_t(st) * kKeyBytes, t * kKeys, &sh->k_full[st]);
+                }
+                if (t > 0) {
+                    const int st = room(sh->v_empty, values), key = (t - 1) * kKeys;
+                    if (!ok) break;
                     ++values;
+                    uint64_t *bar = &sh->v_full[st];
                     const int first = max(0, it.i0 + 1 - key);
                     to_mend &= ~(1u << st);
                     if (first < kKeys) {        // past the first row's last key: handed over by the mender
@@ -209,14 +219,8 @@ __device__ void produce(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint8
                         to_mend |= 1u << st;
                         bar = &sh->mend_full[m];
                     }
-                } else {
-                    ++keys;
+                    load(&k.v, stages + size_t(kStages + st) * kKeyBytes, key, bar);
                 }
-                const CUtensorMap *map = is_v ? &k.v : &k.k;
-                uint8_t *dst = stages + size_t(is_v ? kStages + st : st) * kKeyBytes;
-                mbar_arrive_expect_tx(bar, kKeyBytes);
-                tma_load_3d(dst, map, 0, it.j, it.seq0 + key, bar);
-                tma_load_3d(dst + kKeyHalf, map, 64, it.j, it.seq0 + key, bar);
             }
         }
         __syncwarp();

@@ -235,13 +235,13 @@ __device__ void produce(const KernelArgs &k, Shared<E4M3> *sh, uint8_t *q_tiles,
     // One thread.  The stage of a ring's next tile, once it is free.
     auto room = [&](uint64_t *empty, unsigned n, int stages_of) {
         const int st = n % stages_of;
-        ok = ok && (n < unsigned(stages_of) || lane_wait(sh, &empty[st], (n / stages_of - 1) & 1));
+        ok = ok && (n < unsigned(stages_of) || lane_idle_wait(sh, &empty[st], (n / stages_of - 1) & 1));
         return st;
     };
     for (unsigned n = 0;; ++n) {
         const int slot = n % kRing;
         const Item it = item_of(k, sh->before, i, group_seqs);
-        if (n >= kRing && !warp_wait(sh, &sh->item_empty[slot], (n / kRing - 1) & 1)) break;
+        if (n >= kRing && !warp_idle_wait(sh, &sh->item_empty[slot], (n / kRing - 1) & 1)) break;
         if (it.n_rows && it.b >= 0) {
             int d[2];       // of no tree: anything small; what its rows get is not used
             tree_depths(k.a.parents + (size_t)it.b * k.a.n, k.a.n, d);
@@ -263,6 +263,7 @@ __device__ void produce(const KernelArgs &k, Shared<E4M3> *sh, uint8_t *q_tiles,
             // A tile of queries is whole rows of the KV head's query heads, one box of (64
             // elements, heads, rows) per half.  Rows of the box past the item's
             // fill vectors that nothing reads: rows of a product never mix.
+#pragma unroll 1
             for (int t = 0; t < 2 && t * k.p.rows_tile < it.n_rows; ++t) {
                 const int buf = room(sh->q_empty, queries, F::queries);
                 if (!ok) break;
@@ -312,6 +313,7 @@ __device__ void produce(const KernelArgs &k, Shared<E4M3> *sh, uint8_t *q_tiles,
                     tma_load_3d(dst + kKeyHalf, map, 64, row, outer, bar);
                 }
             };
+#pragma unroll 1
             for (int t = 0; t <= tiles && ok; ++t) {        // K(0), then K(t) and V(t - 1)
                 if (t < tiles) load(false, t * kKeys);
                 if (t > 0 && ok) load(true, (t - 1) * kKeys);
