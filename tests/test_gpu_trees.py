@@ -334,6 +334,49 @@ def test_a_workspace_that_batch_attention_used(tf):
     assert tf.workspace_status(ws) == tf.TF_DEV_OK
 
 
+@pytest.mark.parametrize("B,n,n_kv,g,P,fmt", [
+    (57, 64, 1, 8, 700, "bf16"),        # many CTAs of the sum; two tiles an item
+    (13, 64, 1, 8, 700, "e4m3"),        # fewer
+    (64, 64, 2, 1, 333, "bf16"),        # one query head
+    (20, 64, 2, 8, 5003, "e4m3"),       # the 8-bit prefix is expanded first
+    (64, 40, 1, 16, 9001, "e4m3"),
+    (9, 50, 8, 3, 1207, "bf16"),
+])
+def test_large_batches_give_each_sequence_its_own_bits(tf, B, n, n_kv, g, P, fmt):
+    """Whatever form the size of a batch asks for, a sequence's bits are those it has alone, and an 8-bit cache's
+    those of its values in 16 bits.  Twice, with other entries, on one workspace."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(B + P)
+    pos = [(37 * b) % 450 - (b % 5 == 4) * 10 ** 6 for b in range(B)]
+    pos = [p if p >= 0 else -1 for p in pos]
+    parents = trees(71, n, *[1 + (13 * b) % n for b in range(B)])
+    L = -(-(450 + n) // 256) * 256
+
+    def normal(rows, heads, std=1.0):
+        return (std * torch.randn((rows, heads * D), generator=gen, device="cuda")).to(torch.bfloat16)
+    cache, prefix = tf.KVBatch(B, n_kv, L, fmt), tf.KVBatch(1, n_kv, -(-P // 256) * 256, fmt)
+    ws = tf.workspace(cache.tree_attention_workspace_bytes(g, n, P))
+    for _ in range(2):
+        q, own, shared = normal(B * n, n_kv * g, 2.0), [normal(B * L, n_kv) for _ in range(2)], [normal(P, n_kv) for _ in range(2)]
+        cache.store(*own, dev_pos([0] * B))
+        prefix.store(*shared, dev_pos([0]))
+        out = cache.tree_attention(q, g, dev_pos(pos), dev_i32(parents), prefix=prefix, prefix_len=P, ws=ws)
+        assert tf.workspace_status(ws) == tf.TF_DEV_OK
+        if fmt == "e4m3":
+            wide, wide_prefix = tf.KVBatch(B, n_kv, L), tf.KVBatch(1, n_kv, prefix.max_len)
+            wide.store(*cache.load(dev_pos([0] * B), L), dev_pos([0] * B))
+            wide_prefix.store(*prefix.load(dev_pos([0]), P), dev_pos([0]))
+            assert torch.equal(out, wide.tree_attention(q, g, dev_pos(pos), dev_i32(parents), prefix=wide_prefix, prefix_len=P))
+        out = out.view(B, n, -1)
+        for b in (0, B // 2, B - 1):
+            one = tf.KVBatch(1, n_kv, L, fmt)
+            one.store(*(x.view(B, L, -1)[b].contiguous() for x in own), dev_pos([0]))
+            alone = one.tree_attention(q.view(B, n, -1)[b].contiguous(), g, dev_pos([pos[b]]), dev_i32([parents[b]]), prefix=prefix,
+                                       prefix_len=P)
+            assert torch.equal(alone, out[b])
+            assert bool(alone.any()) == (pos[b] >= 0)
+
+
 # ---------------------------------------------------------------- acceptance
 @pytest.mark.parametrize("B,n,vocab", [(1, 1, 3), (1, 8, 3), (3, 33, 2), (5, 64, 4), (130, 20, 2), (1024, 64, 3)])
 def test_accept(tf, B, n, vocab):

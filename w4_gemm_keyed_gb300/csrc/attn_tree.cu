@@ -27,10 +27,15 @@ namespace {
 using namespace flow;
 
 constexpr int kOwnPart = 320;           // own entries per part
-constexpr int kMinPrefixPart = 320;     // shared entries per part, at least
+constexpr int kMinPrefixPart = 240;     // shared entries per part, at least (8 nodes over 300 entries: 9.5 us, 10.5 with 320; 64 x 16 over
+                                        // 700, 32 heads: 60, 72 with 160)
 constexpr int kPrefixItems = 76;        // of a batch that is one pair of tiles, about
 constexpr int kSms = 152;
-constexpr int kExpandPairs = 2;         // pairs of query tiles from which on an E4M3 prefix is expanded first
+// An E4M3 prefix is expanded into the workspace first where that pays: it saves every pair of query tiles
+// 28 ns per 1,000 entries and head, costs 76 ns and the two further grids 10 us, so from (pairs - 3) x entries x heads = 340,000 on
+// (16 x 32 nodes, 16 pairs, over 16461 x 8: 262 us, 301 without; 16 x 8 nodes, 4 pairs, over 16000 x 8: 87, 82 without;
+// 32 x 16 nodes, 16 pairs, over 1000 x 8: 76, 70 without).
+constexpr long long kExpandWork = 340000;
 constexpr int kGroups = 128;            // entries of the table of own items
 constexpr int kProducerWarp = 8, kScoreWarp = 9, kMendWarp = 11;
 constexpr int kExpandWarp = 12, kExpandWarps = 4;       // E4M3: for K tiles, and as many for V tiles
@@ -96,7 +101,7 @@ Plan plan_of(const KvBatch &own, int prefix_len, int group, int n) {
     p.own_rows_item = rows_item((long long)p.own_parts_max * own.n_kv * own.n_seq, n);
     p.pairs = items(p.rows, p.rows_item);
     p.own_pairs = items(n, p.own_rows_item);
-    p.expanded = own.format == kKvE4m3 && prefix_len > 0 && items(p.rows, both) >= kExpandPairs;
+    p.expanded = own.format == kKvE4m3 && (long long)(items(p.rows, both) - 3) * prefix_len * own.n_kv >= kExpandWork;
     return p;
 }
 
