@@ -377,6 +377,43 @@ def test_large_batches_give_each_sequence_its_own_bits(tf, B, n, n_kv, g, P, fmt
             assert bool(alone.any()) == (pos[b] >= 0)
 
 
+def test_two_graphs_share_a_workspace(tf):
+    """One with its 8-bit prefix expanded first (four grids, two of them at once), one without."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+
+    def normal(rows, heads, std=1.0):
+        return (std * torch.randn((rows, heads * D), generator=gen, device="cuda")).to(torch.bfloat16)
+    calls = []
+    for B, n, n_kv, g, P in ((20, 64, 2, 8, 5003), (3, 10, 2, 4, 700)):
+        cache, prefix = tf.KVBatch(B, n_kv, 512, "e4m3"), tf.KVBatch(1, n_kv, -(-P // 256) * 256, "e4m3")
+        cache.store(normal(B * 512, n_kv), normal(B * 512, n_kv), dev_pos([0] * B))
+        prefix.store(normal(P, n_kv), normal(P, n_kv), dev_pos([0]))
+        q, pos = normal(B * n, n_kv * g, 2.0), dev_pos([(31 * b) % 440 for b in range(B)])
+        tree, out = dev_i32(trees(81, n, *[n - b % 4 for b in range(B)])), torch.zeros((B * n, n_kv * g * D), dtype=torch.bfloat16, device="cuda")
+        calls.append((cache, prefix, q, pos, tree, out, g, n, P))
+    ws = tf.workspace(max(c[0].tree_attention_workspace_bytes(c[6], c[7], c[8]) for c in calls))
+
+    def call(c, out, ws):
+        c[0].tree_attention(c[2], c[6], c[3], c[4], prefix=c[1], prefix_len=c[8], out=out, ws=ws)
+    graphs = []
+    for c in calls:
+        call(c, c[5], ws)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call(c, c[5], ws)
+    for i in (0, 1, 1, 0, 0, 1):
+        c = calls[i]
+        c[2].copy_(normal(c[2].shape[0], c[2].shape[1] // D, 2.0))
+        c[5].zero_()
+        graphs[i].replay()
+        want = torch.empty_like(c[5])
+        call(c, want, None)
+        assert torch.equal(c[5], want)
+    assert tf.workspace_status(ws) == tf.TF_DEV_OK
+
+
 # ---------------------------------------------------------------- acceptance
 @pytest.mark.parametrize("B,n,vocab", [(1, 1, 3), (1, 8, 3), (3, 33, 2), (5, 64, 4), (130, 20, 2), (1024, 64, 3)])
 def test_accept(tf, B, n, vocab):

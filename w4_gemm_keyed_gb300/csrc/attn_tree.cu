@@ -7,7 +7,7 @@
 //
 // A node's bits must not tell whether an ancestor is a node of this pass or was
 // committed before.  So the entries at its last kMaxPath own positions, every node of its path among
-// them, are "near": they are folded in path order and in fp32.  The others, all of them
+// them, are "near": they are one matrix product's keys, in path order.  The others, all of them
 // before the root, are "far" and lie on a fixed grid of parts:
 // kOwnPart own entries, or of the prefix a length that P and the number of KV heads
 // fix.  A far part is folded by the flow of attn_flow.cuh, each vector for itself, and its result stored (maximum m,
