@@ -13,6 +13,12 @@
 // fix.  A far part is folded by the flow of attn_flow.cuh, each vector for itself, and its result stored (maximum m,
 // weight sum l, unnormalised output o, fp32); a second kernel works on the near entries and adds up all parts in ascending
 // order, the near ones last.  So bits depend on a node's query, position, P and the entries that it sees.
+//
+// What bounds it (GB300, call after call on the same inputs): many nodes, the tensor cores and what
+// storing an item's results takes, 128 KB at 28 bytes a cycle (24 x 64 nodes x 64 heads over 32768 entries 1,077 us: parts 973 at
+// 1.50 PFLOP/s, the sum 96 at 5.1 TB/s); few, the steps one SM has in a row (5 x 24 nodes over 8192 43 us: two items of 12
+// steps, the sum 13; 3 x 41 nodes x 20 heads over own 12007 32 us) or launches (8 nodes over 300 entries 9.7 us).  E4M3 where nothing is
+// expanded first, the chain copy - expand - product - softmax of a step (16 nodes over 30000 50 us, 37 as a bf16 cache).
 #include <atomic>
 
 #include "attn_flow.cuh"
@@ -29,7 +35,9 @@ using namespace flow;
 constexpr int kOwnPart = 320;           // own entries per part
 constexpr int kMinPrefixPart = 240;     // shared entries per part, at least (8 nodes over 300 entries: 9.5 us, 10.5 with 320; 64 x 16 over
                                         // 700, 32 heads: 60, 72 with 160)
-constexpr int kPrefixItems = 76;        // of a batch that is one pair of tiles, about
+// Items of a batch that is one pair of tiles, about.  Twice as many: 4 x 8 nodes over 30000 entries 39 us (52), 24 x 64 over 32768
+// 1,241 (1,099), 5 x 24 over 8192 64 (53).
+constexpr int kPrefixItems = 76;
 constexpr int kSms = 152;
 // An E4M3 prefix is expanded into the workspace first where that pays: it saves every pair of query tiles
 // 28 ns per 1,000 entries and head, costs 76 ns and the two further grids 10 us, so from (pairs - 3) x entries x heads = 340,000 on
@@ -90,7 +98,8 @@ Plan plan_of(const KvBatch &own, int prefix_len, int group, int n) {
     p.n_parts = prefix_len > 0 ? (prefix_len - 1) / p.part + 1 : 0;
     p.own_parts_max = (own.max_len + kOwnPart - 1) / kOwnPart;
     // Two tiles share each K and V tile, and a step of both takes 1.7 times as long as of one alone: one tile an
-    // item where the SMs are then done sooner.  Own parts: at most as many as the caches hold.
+    // item where the SMs are then done sooner (4 x 8 nodes over 30000 entries, 72 items of two: 41 us, 52 as two; 8 x 8 over 16000,
+    // 144: 39 as two, 50 as one).  Own parts: at most as many as the caches hold.
     auto items = [](int rows, int rows_item) { return (rows + rows_item - 1) / rows_item; };
     const int both = 2 * p.rows_tile;
     auto rows_item = [&](long long parts, int rows) {

