@@ -55,15 +55,16 @@ static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     return fn;
 }
 
-bool encode_tiles(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
-                  const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle, const char **why) {
-    const cuuint32_t ones[3] = {1, 1, 1};
+template <int N>
+bool encode_tiles(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[N], const cuuint64_t (&strides)[N - 1],
+                  const cuuint32_t (&box)[N], CUtensorMapSwizzle swizzle, const char **why) {
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
     const auto fn = tensor_map_encoder();
     if (!fn) {
         *why = "cuTensorMapEncodeTiled is unavailable";
         return false;
     }
-    if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, ones,
+    if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, N, const_cast<void *>(base), dims, strides, box, ones,
            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
         *why = "cuTensorMapEncodeTiled rejected the layout";
@@ -71,6 +72,8 @@ bool encode_tiles(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[3],
     }
     return true;
 }
+template bool encode_tiles<4>(CUtensorMap *, const void *, const cuuint64_t (&)[4], const cuuint64_t (&)[3], const cuuint32_t (&)[4],
+                              CUtensorMapSwizzle, const char **);
 
 namespace {
 
@@ -999,14 +1002,14 @@ __global__ void __launch_bounds__(kJoinThreads, 6) attn_batch_join_kernel(AttnBa
 // is stored with its 16-byte chunks already permuted by position, as the
 // 128-byte swizzle wants them in shared memory, so the copy permutes nothing.
 bool encode_cache(CUtensorMap *m, const void *base, int rows, int max_len, int outer, const char **why) {
-    return encode_tiles(m, base, {cuuint64_t(kHeadDim), cuuint64_t(rows), cuuint64_t(outer)},
+    return encode_tiles<3>(m, base, {cuuint64_t(kHeadDim), cuuint64_t(rows), cuuint64_t(outer)},
                   {cuuint64_t(kHeadDim) * 2, cuuint64_t(max_len) * kHeadDim * 2}, {64, kTile, 1},
                   CU_TENSOR_MAP_SWIZZLE_NONE, why);
 }
 
 // Innermost first: a head's 128 elements, heads, rows.
 bool encode_queries(CUtensorMap *m, const AttnBatchArgs &a, const char **why) {
-    return encode_tiles(m, a.q, {cuuint64_t(kHeadDim), cuuint64_t(a.own.n_kv) * a.group, cuuint64_t(a.own.n_seq) * a.R},
+    return encode_tiles<3>(m, a.q, {cuuint64_t(kHeadDim), cuuint64_t(a.own.n_kv) * a.group, cuuint64_t(a.own.n_seq) * a.R},
                   {cuuint64_t(kHeadDim) * 2, cuuint64_t(a.ldq) * 2},
                   {64, cuuint32_t(a.group), cuuint32_t(kTile / a.group)}, CU_TENSOR_MAP_SWIZZLE_128B, why);
 }

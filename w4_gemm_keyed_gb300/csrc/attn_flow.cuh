@@ -119,6 +119,20 @@ __device__ __forceinline__ bool warp_idle_wait(SHARED *sh, uint64_t *bar, uint32
     return __all_sync(0xFFFFFFFFu, lane_idle_wait(sh, bar, parity));
 }
 
+// A tile of queries is whole rows of a KV head's query heads, a box of (64 elements, heads, rows, halves): both halves in one copy
+// where they are 128 vectors, whose halves then lie where the products expect them.  Rows of the box past the
+// item's fill vectors that nothing reads: rows of a product never mix.  One thread.
+__device__ __forceinline__ void load_queries(uint8_t *dst, const CUtensorMap *map, int head, int row, int vectors, uint64_t *bar) {
+    mbar_arrive_expect_tx(bar, 2 * uint32_t(vectors) * 128u);
+    tma_load_4d(dst, map, 0, head, row, 0, bar);
+    if (vectors < kTile) tma_load_4d(dst + kHalfBytes, map, 0, head, row, 1, bar);
+}
+inline bool encode_queries(CUtensorMap *m, const uint16_t *base, int heads, int rows, int ld, int group, int rows_tile, const char **why) {
+    return encode_tiles<4>(m, base, {64, cuuint64_t(heads), cuuint64_t(rows), 2}, {cuuint64_t(kHeadDim) * 2, cuuint64_t(ld) * 2, 128},
+                           {64, cuuint32_t(group), cuuint32_t(rows_tile), group * rows_tile == kTile ? 2u : 1u},
+                           CU_TENSOR_MAP_SWIZZLE_128B, why);
+}
+
 // A place in a ring of N barriers, and the parity of the phase that is awaited there.
 template <int N>
 struct Ring {

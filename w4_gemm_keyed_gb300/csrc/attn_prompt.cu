@@ -186,23 +186,17 @@ __device__ void produce(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint8
         if (it.n_rows == 0) break;
         if (lane == 0) {
             const int n_keys = it.n_keys, tiles = (n_keys + kKeys - 1) / kKeys;
-            // A tile of queries is whole rows of the KV head's query heads, one box of (64
-            // elements, heads, rows) per half.  Rows of the box past the item's
-            // fill vectors that nothing reads: rows of a product never mix.
 #pragma unroll 1
             for (int t = 0; t < 2 && t * k.rows_tile < it.n_rows; ++t) {
                 const int buf = room(sh->q_empty, queries);
                 if (!ok) break;
                 ++queries;
                 const int row = it.seq0 + it.i0 + t * k.rows_tile;
-                mbar_arrive_expect_tx(&sh->q_full[buf], 2 * uint32_t(k.rows_tile * g) * 128u);
-                tma_load_3d(q_tiles + buf * kTileBytes, &k.q, 0, it.j * g, row, &sh->q_full[buf]);
-                tma_load_3d(q_tiles + buf * kTileBytes + kHalfBytes, &k.q, 64, it.j * g, row, &sh->q_full[buf]);
+                load_queries(q_tiles + buf * kTileBytes, &k.q, it.j * g, row, k.rows_tile * g, &sh->q_full[buf]);
             }
             auto load = [&](const CUtensorMap *map, uint8_t *dst, int key, uint64_t *bar) {
                 mbar_arrive_expect_tx(bar, kKeyBytes);
-                tma_load_3d(dst, map, 0, it.j, it.seq0 + key, bar);
-                tma_load_3d(dst + kKeyHalf, map, 64, it.j, it.seq0 + key, bar);
+                tma_load_4d(dst, map, 0, it.seq0 + key, it.j, 0, bar);
             };
 #pragma unroll 1
             for (int t = 0; t <= tiles && ok; ++t) {        // K(0), then K(t) and V(t - 1)
@@ -383,12 +377,10 @@ __global__ void __launch_bounds__(kCtaThreads, 1) attn_prompt_kernel(const __gri
     if (warp == kScoreWarp) tc_dealloc(tmem, kTmemCols);
 }
 
-// Innermost first: a head's 128 elements, heads, rows.
-bool encode_rows(CUtensorMap *m, const uint16_t *base, int heads, int rows, int ld, int box_heads, int box_rows,
-                 const char **why) {
-    return encode_tiles(m, base, {cuuint64_t(kHeadDim), cuuint64_t(heads), cuuint64_t(rows)},
-                        {cuuint64_t(kHeadDim) * 2, cuuint64_t(ld) * 2}, {64, cuuint32_t(box_heads), cuuint32_t(box_rows)},
-                        CU_TENSOR_MAP_SWIZZLE_128B, why);
+// Innermost first: half a head's elements, rows, heads, halves: a tile's two halves in one copy.
+bool encode_keys(CUtensorMap *m, const uint16_t *base, int heads, int rows, int ld, const char **why) {
+    return encode_tiles<4>(m, base, {64, cuuint64_t(rows), cuuint64_t(heads), 2},
+                           {cuuint64_t(ld) * 2, cuuint64_t(kHeadDim) * 2, 128}, {64, kKeys, 1, 2}, CU_TENSOR_MAP_SWIZZLE_128B, why);
 }
 
 }  // namespace
@@ -416,9 +408,9 @@ cudaError_t launch_attn_prompt(const AttnPromptArgs &a, cudaStream_t s, const ch
     };
     // two tiles share each K and V tile, but one tile an item where two would leave SMs without any
     k.rows_item = items(2 * k.rows_tile) >= sms ? 2 * k.rows_tile : k.rows_tile;
-    if (!encode_rows(&k.q, a.q, a.n_kv * a.group, a.rows, a.ldq, a.group, k.rows_tile, why) ||
-        !encode_rows(&k.k, a.k, a.n_kv, a.rows, a.ldk, 1, kKeys, why) ||
-        !encode_rows(&k.v, a.v, a.n_kv, a.rows, a.ldv, 1, kKeys, why))
+    if (!encode_queries(&k.q, a.q, a.n_kv * a.group, a.rows, a.ldq, a.group, k.rows_tile, why) ||
+        !encode_keys(&k.k, a.k, a.n_kv, a.rows, a.ldk, why) ||
+        !encode_keys(&k.v, a.v, a.n_kv, a.rows, a.ldv, why))
         return cudaErrorInvalidValue;
     const long long most = items(k.rows_item);
     return launch_pdl(attn_prompt_kernel, dim3(unsigned(most < sms ? most : sms)), dim3(kCtaThreads), kSmemBytes, s, k);

@@ -70,7 +70,8 @@ __device__ __forceinline__ uint32_t bf16x2_finite(uint32_t w) {   // non-finite 
 
 // Tiled map of bf16 elements, innermost dimension first (its stride is 1; strides in
 // bytes); false and *why where there is none.
-bool encode_tiles(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
-                  const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle, const char **why);
+template <int N>
+bool encode_tiles(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[N], const cuuint64_t (&strides)[N - 1],
+                  const cuuint32_t (&box)[N], CUtensorMapSwizzle swizzle, const char **why);
 
 }  // namespace tfk

@@ -274,18 +274,13 @@ __device__ void produce(const KernelArgs &k, Shared<E4M3> *sh, uint8_t *q_tiles,
         if (lane == 0) {
             const bool own = it.b >= 0;
             const int tiles = (it.n_keys + kKeys - 1) / kKeys, outer = own ? it.b * k.a.own.n_kv + it.j : it.j;
-            // A tile of queries is whole rows of the KV head's query heads, one box of (64
-            // elements, heads, rows) per half.  Rows of the box past the item's
-            // fill vectors that nothing reads: rows of a product never mix.
 #pragma unroll 1
             for (int t = 0; t < 2 && t * k.p.rows_tile < it.n_rows; ++t) {
                 const int buf = room(sh->q_empty, queries, F::queries);
                 if (!ok) break;
                 ++queries;
                 const int row = it.row0 + t * k.p.rows_tile;
-                mbar_arrive_expect_tx(&sh->q_full[buf], 2 * uint32_t(k.p.rows_tile * g) * 128u);
-                tma_load_3d(q_tiles + buf * kTileBytes, &k.map[4], 0, it.j * g, row, &sh->q_full[buf]);
-                tma_load_3d(q_tiles + buf * kTileBytes + kHalfBytes, &k.map[4], 64, it.j * g, row, &sh->q_full[buf]);
+                load_queries(q_tiles + buf * kTileBytes, &k.map[4], it.j * g, row, k.p.rows_tile * g, &sh->q_full[buf]);
             }
             // one tile of entries key0 + key ..
             auto load = [&](bool is_v, int key) {
@@ -323,8 +318,7 @@ __device__ void produce(const KernelArgs &k, Shared<E4M3> *sh, uint8_t *q_tiles,
                     }
                     const CUtensorMap *map = &k.map[(own ? 2 : 0) + (is_v ? 1 : 0)];
                     mbar_arrive_expect_tx(bar, kKeyBytes);
-                    tma_load_3d(dst, map, 0, row, outer, bar);
-                    tma_load_3d(dst + kKeyHalf, map, 64, row, outer, bar);
+                    tma_load_4d(dst, map, 0, row, outer, 0, bar);
                 }
             };
 #pragma unroll 1
@@ -877,14 +871,14 @@ __global__ void __launch_bounds__(kJoinThreads, BLOCKS) attn_tree_join_kernel(At
     }
 }
 
-// Innermost first: an entry's 128 elements, entries, (sequence, head).  The cache
+// Innermost first: half an entry's elements, entries, (sequence, head), halves: a tile's two halves in one copy.  The cache
 // is stored with its 16-byte chunks already permuted by position, as the
 // 128-byte swizzle wants them in shared memory (parts and tiles start at multiples of 8), so the copy
 // permutes nothing.
 bool encode_cache(CUtensorMap *m, const void *base, int rows, int max_len, int outer, const char **why) {
-    return encode_tiles(m, base, {cuuint64_t(kHeadDim), cuuint64_t(rows), cuuint64_t(outer)},
-                        {cuuint64_t(kHeadDim) * 2, cuuint64_t(max_len) * kHeadDim * 2}, {64, kKeys, 1},
-                        CU_TENSOR_MAP_SWIZZLE_NONE, why);
+    return encode_tiles<4>(m, base, {64, cuuint64_t(rows), cuuint64_t(outer), 2},
+                           {cuuint64_t(kHeadDim) * 2, cuuint64_t(max_len) * kHeadDim * 2, 128}, {64, kKeys, 1, 2},
+                           CU_TENSOR_MAP_SWIZZLE_NONE, why);
 }
 
 }  // namespace
@@ -971,9 +965,7 @@ cudaError_t launch_attn_tree(const AttnTreeArgs &a, cudaStream_t s, const char *
     k.values = reinterpret_cast<float *>(expanded + 2 * half);
     k.ml = reinterpret_cast<float2 *>(k.values + slots * kHeadDim);
     const bool e4m3 = a.own.format == kKvE4m3;
-    bool ok = encode_tiles(&k.map[4], a.q, {cuuint64_t(kHeadDim), cuuint64_t(a.own.n_kv) * a.group, cuuint64_t(k.p.rows)},
-                           {cuuint64_t(kHeadDim) * 2, cuuint64_t(a.ldq) * 2},
-                           {64, cuuint32_t(a.group), cuuint32_t(k.p.rows_tile)}, CU_TENSOR_MAP_SWIZZLE_128B, why);
+    bool ok = encode_queries(&k.map[4], a.q, a.own.n_kv * a.group, k.p.rows, a.ldq, a.group, k.p.rows_tile, why);
     if (a.prefix_len > 0 && (!e4m3 || k.p.expanded)) {
         const void *pk = e4m3 ? expanded : a.prefix.k, *pv = e4m3 ? expanded + half : a.prefix.v;
         const int len = e4m3 ? expanded_len(a.prefix_len) : a.prefix.max_len;
