@@ -644,7 +644,7 @@ TF_API tf_status tf_attention_prompt(const uint16_t *q, int32_t ldq, const uint1
  * tf_attention_tree: as tf_attention_batch, with row i of sequence b attending over the prefix's
  *   entries, own entries 0 .. pos[b] - 1 and the entries of its path's nodes, itself
  *   included.  n rows per sequence (pos[b] + n <= max_len, n * group may exceed 128).
- *   Rows of idle sequences and unused rows are zeros.  A node's bits depend on its query,
+ *   Rows of idle sequences and unused rows are zeros; out does not overlap q.  A node's bits depend on its query,
  *   its position pos[b] + depth, prefix_len and the entries it sees, in path order: the same
  *   whether an entry is a node of this pass or was committed before.  ws:
  *   tf_attention_tree_workspace_bytes (0: unsupported arguments).

@@ -937,7 +937,7 @@ cudaError_t launch_join(const KernelArgs &k, cudaStream_t s) {
     // Vectors of a CTA of the sum: no more than 16 nodes, two a warp (64 x 64 nodes of one head, 8 vectors: 23 us in all, 32: 27;
     // 40 x 20 of three, 8: 30, 32: 23).  Columns split where there are fewer CTAs than kSplitCtas
     // (3 x 41 nodes, 84 CTAs, over own 12007 entries: 32 us, 43 without; 5 x 24, 240 CTAs: 53, 44 without).
-    // Three CTAs an SM, with half the loads on their way, from kFullCtas on (24 x 64, 3072 CTAs: 1066 us, 1078 with
+    // Three CTAs an SM, with half the loads on their way, from kFullCtas on (24 x 64 nodes of 8 heads: 1066 us, 1078 with
     // two; 5 x 24: 45, 44 with two).
     constexpr int kSplitCtas = 100, kFullCtas = 456;
     const int vecs = a.group == 1 ? 8 : 32, nodes = vecs / a.group, ctas = (k.p.rows + nodes - 1) / nodes * a.own.n_kv;

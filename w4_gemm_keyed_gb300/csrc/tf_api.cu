@@ -1,7 +1,7 @@
 // extern "C" entry points of libtf: argument validation, workspace layout and
 // launch sequencing.  Every step of the verify pass runs in this library's own
 // kernels (w4_gemm.cu, sampler.cu, glue.cu, attention.cu, kv_batch.cu,
-// attn_batch.cu, attn_prompt.cu, tree.cu); nothing here computes
+// attn_batch.cu, attn_prompt.cu, attn_tree.cu, tree.cu); nothing here computes
 // on the host.
 #include <cmath>
 #include <cstdarg>
