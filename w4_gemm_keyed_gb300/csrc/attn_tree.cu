@@ -17,7 +17,7 @@
 // What bounds it (GB300, call after call on the same inputs): many nodes, the tensor cores and what
 // storing an item's results takes, 128 KB at 28 bytes a cycle (24 x 64 nodes x 64 heads over 32768 entries 1,077 us: parts 973 at
 // 1.50 PFLOP/s, the sum 96 at 5.1 TB/s); few, the steps one SM has in a row (5 x 24 nodes over 8192 43 us: two items of 12
-// steps, the sum 13; 3 x 41 nodes x 20 heads over own 12007 32 us) or launches (8 nodes over 300 entries 9.7 us).  E4M3 where nothing is
+// steps, the sum 13; 3 x 41 nodes x 20 heads over own 12007 32 us) or launches (8 nodes over 300 entries 10.7 us).  E4M3 where nothing is
 // expanded first, the chain copy - expand - product - softmax of a step (16 nodes over 30000 50 us, 37 as a bf16 cache).
 #include <atomic>
 
@@ -33,8 +33,10 @@ namespace {
 using namespace flow;
 
 constexpr int kOwnPart = 320;           // own entries per part
-constexpr int kMinPrefixPart = 240;     // shared entries per part, at least (8 nodes over 300 entries: 9.5 us, 10.5 with 320; 64 x 16 over
-                                        // 700, 32 heads: 60, 72 with 160)
+// Shared entries per part, at least: an item's results take as long to store as two and a half steps.  With 240: 64 x 64 nodes over
+// 500 entries 307 us (238), 32 x 16 over 1000 61 (44), but 8 over 300 9.7 (10.7), 8 over 2000 10.8 (12.5); with 960 30 x 40 over 3000
+// 85 (97), 8 over 2000 15.4.
+constexpr int kMinPrefixPart = 560;
 // Items of a batch that is one pair of tiles, about.  Twice as many: 4 x 8 nodes over 30000 entries 39 us (52), 24 x 64 over 32768
 // 1,241 (1,099), 5 x 24 over 8192 64 (53).
 constexpr int kPrefixItems = 76;
