@@ -16,8 +16,8 @@
 //
 // What bounds it (GB300, call after call on the same inputs): many nodes, the tensor cores and what
 // storing an item's results takes, 128 KB at 28 bytes a cycle (24 x 64 nodes x 64 heads over 32768 entries 1,077 us: parts 973 at
-// 1.50 PFLOP/s, the sum 96 at 5.1 TB/s); few, the steps one SM has in a row (5 x 24 nodes over 8192 43 us: two items of 12
-// steps, the sum 13; 3 x 41 nodes x 20 heads over own 12007 32 us) or launches (8 nodes over 300 entries 10.7 us).  E4M3 where nothing is
+// 1.50 PFLOP/s, the sum 93 at 5.2 TB/s); few, the steps one SM has in a row (5 x 24 nodes over 8192 41 us: two items of 12
+// steps, the sum 11; 3 x 41 nodes x 20 heads over own 12007 31 us) or launches (8 nodes over 300 entries 10.7 us).  E4M3 where nothing is
 // expanded first, the chain copy - expand - product - softmax of a step (16 nodes over 30000 50 us, 37 as a bf16 cache).
 #include <atomic>
 
@@ -856,8 +856,9 @@ __global__ void __launch_bounds__(kJoinThreads, BLOCKS) attn_tree_join_kernel(At
     __syncthreads();    // the near outputs are read
     uint16_t *const rows = reinterpret_cast<uint16_t *>(&sh->near[0][0]);
     constexpr int kPitch = kHeadDim + 8;        // 16-bit elements
+    const float inv = __frcp_rn(l);     // a division for each output took a quarter of the kernel's instructions
     auto pair = [&](float e0, float e1) {
-        const __nv_bfloat162 r = __floats2bfloat162_rn(__fdiv_rn(e0, l), __fdiv_rn(e1, l));
+        const __nv_bfloat162 r = __floats2bfloat162_rn(e0 * inv, e1 * inv);
         return *reinterpret_cast<const uint32_t *>(&r);
     };
 #pragma unroll
@@ -867,7 +868,7 @@ __global__ void __launch_bounds__(kJoinThreads, BLOCKS) attn_tree_join_kernel(At
     __syncthreads();
     constexpr int kChunks = 16 / SPLIT;     // of 16 bytes
     for (int i = threadIdx.x; i < here * g * kChunks; i += kJoinThreads) {
-        const int v = i / kChunks, c = i % kChunks + blockIdx.z * kChunks, at = v / g;
+        const int v = i / kChunks, c = i % kChunks + blockIdx.z * kChunks, at = idx_div(v, g);
         *reinterpret_cast<uint4 *>(a.out + (size_t)(row0 + at) * a.ldo + (size_t)(j * g + v - at * g) * kHeadDim + 8 * c) =
             *reinterpret_cast<const uint4 *>(rows + v * kPitch + 8 * c);
     }
