@@ -868,7 +868,7 @@ __global__ void __launch_bounds__(kJoinThreads, BLOCKS) attn_tree_join_kernel(At
     __syncthreads();
     constexpr int kChunks = 16 / SPLIT;     // of 16 bytes
     for (int i = threadIdx.x; i < here * g * kChunks; i += kJoinThreads) {
-        const int v = i / kChunks, c = i % kChunks + blockIdx.z * kChunks, at = idx_div(v, g);
+        const int v = i / kChunks, c = i % kChunks + blockIdx.z * kChunks, at = v / g;
         *reinterpret_cast<uint4 *>(a.out + (size_t)(row0 + at) * a.ldo + (size_t)(j * g + v - at * g) * kHeadDim + 8 * c) =
             *reinterpret_cast<const uint4 *>(rows + v * kPitch + 8 * c);
     }
