@@ -82,7 +82,8 @@ __global__ void __launch_bounds__(32 * kKeepWarps) kv_keep_kernel(KvBatch c, con
                (node >= 0 && (lane == 0 ? node != 0 : node <= before));
     const int last = __shfl_sync(0xFFFFFFFFu, node, max(n, 1) - 1);
     bad = __any_sync(0xFFFFFFFFu, bad);
-    const bool out = p < -1 || (p >= 0 && p + last >= c.max_len);
+    // no sum with p: it may be any int64
+    const bool out = p < -1 || p > (long long)c.max_len - 1 - last;
     if (p != -1 && (bad || out) && unit == 0 && lane == 0) set_error(err, out ? kDevBadPosition : kDevBadTree);
     if (p < 0 || bad || out || n < 2) return;
     const int j = unit >> 1;
