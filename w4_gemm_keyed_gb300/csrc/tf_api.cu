@@ -1089,8 +1089,10 @@ tf_status tf_tree_accept(const int32_t *parents, const int32_t *tokens, const in
                          int32_t *committed, void *ws, size_t ws_bytes, void *stream) {
     if (n_seq < 1 || n_seq > TF_MAX_SEQS) return fail(TF_ERR_UNSUPPORTED, "n_seq=%d outside [1, %d]", n_seq, TF_MAX_SEQS);
     if (n < 1 || n > TF_MAX_NODES) return fail(TF_ERR_INVALID_ARG, "n=%d outside [1, %d]", n, TF_MAX_NODES);
-    if (!parents || !tokens || !sampled || !pos || !accepted || !bonus || !path || !committed || !aligned(pos, 8))
-        return fail(TF_ERR_INVALID_ARG, "null or misaligned pointer");
+    if (!pos || !aligned(pos, 8)) return fail(TF_ERR_INVALID_ARG, "null or misaligned pos");
+    for (const int32_t *p : {parents, tokens, sampled, (const int32_t *)accepted, (const int32_t *)bonus,
+                             (const int32_t *)path, (const int32_t *)committed})
+        if (!p || !aligned(p, 4)) return fail(TF_ERR_INVALID_ARG, "null or misaligned int32 array");
     tf_status st = check_ws(ws, ws_bytes, 256);
     if (st != TF_OK) return st;
     TreeAcceptArgs a{};
