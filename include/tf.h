@@ -609,7 +609,7 @@ TF_API tf_status tf_attention_batch(const tf_kv_batch *own, const tf_kv_batch *p
  *   h / group (group in 1..16, n_kv in 1..128); k, v: dev bf16 [rows][ldk], [rows][ldv],
  *   KV head j at columns j*128; out: dev bf16 [rows][ldo], rounded once.  Each ld a
  *   multiple of 8, each pointer 16-B aligned; the three inputs may be columns of one
- *   array (what tf_qk_norm_rope leaves); out overlaps none of them.  Rows before
+ *   array (what tf_qk_norm_rope leaves); out overlaps none of them (refused).  Rows before
  *   starts[0] and from starts[n_seq] on are not written, and may hold anything.  Starts that
  *   fall, or lie outside [0, rows], record TF_DEV_BAD_POSITION and nothing is
  *   written.  The softmax weights are rounded to bf16 for the product with v
@@ -644,7 +644,7 @@ TF_API tf_status tf_attention_prompt(const uint16_t *q, int32_t ldq, const uint1
  * tf_attention_tree: as tf_attention_batch, with row i of sequence b attending over the prefix's
  *   entries, own entries 0 .. pos[b] - 1 and the entries of its path's nodes, itself
  *   included.  n rows per sequence (pos[b] + n <= max_len, n * group may exceed 128).
- *   Rows of idle sequences and unused rows are zeros; out does not overlap q.  A node's bits depend on its query,
+ *   Rows of idle sequences and unused rows are zeros; out does not overlap q (refused).  A node's bits depend on its query,
  *   its position pos[b] + depth, prefix_len and the entries it sees, in path order: the same
  *   whether an entry is a node of this pass or was committed before.  ws:
  *   tf_attention_tree_workspace_bytes (0: unsupported arguments).

@@ -43,3 +43,39 @@ def test_the_other_calls_take_no_such_position_either(tf, pos):
     tree = dev_i32([[-1] + [0] * 7] * 2)
     out = cache.tree_attention(rows, 1, dev_pos([10, pos]), tree, ws=ws)
     assert tf.workspace_status(ws) == tf.TF_DEV_BAD_POSITION and not out[8:].any() and out[:8].all()
+
+
+# ---------------------------------------------------------------- outputs beside what is read
+def test_outputs_may_be_other_columns_or_rows_of_an_inputs_array(tf):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(3)
+    cols, n = 8 * 128, 9
+
+    def normal(rows, width):
+        return torch.randn((rows, width), generator=gen, device="cuda").to(torch.bfloat16)
+    x, starts = normal(n, 2 * cols + 512), torch.tensor([0, 4, n], device="cuda")
+    q, k, v = x[:, :cols], x[:, cols:cols + 256], x[:, cols + 256:cols + 512]
+    want = tf.prompt_attention(q, k, v, 2, 4, starts)
+    got = tf.prompt_attention(q, k, v, 2, 4, starts, out=x[:, cols + 512:])
+    assert torch.equal(got, want) and got.data_ptr() == x.data_ptr() + 2 * (cols + 512)
+    rows = normal(2 * n, cols)
+    rows[:n] = q
+    got = tf.prompt_attention(rows[:n], k, v, 2, 4, starts, out=rows[n:])
+    assert torch.equal(got, want)
+    cache, pos, tree = tf.KVBatch(1, 2, 256), dev_pos([3]), dev_i32([[-1] + [0] * (n - 1)])
+    cache.store(normal(20, 256), normal(20, 256), dev_pos([0]))
+    want = cache.tree_attention(q, 4, pos, tree)
+    assert torch.equal(cache.tree_attention(q, 4, pos, tree, out=x[:, cols + 512:]), want)
+    every = torch.stack([q, torch.zeros_like(q)], 1).view(2 * n, cols)      # every other row
+    assert torch.equal(cache.tree_attention(every[::2], 4, pos, tree, out=every[1::2]), want)
+
+
+def test_an_output_in_an_input_is_refused(tf):
+    x = torch.ones((9, 1536), dtype=torch.bfloat16, device="cuda")
+    starts, cache = torch.tensor([0, 9], device="cuda"), tf.KVBatch(1, 2, 256)
+    q, k, v = x[:, :1024], x[:, 1024:1280], x[:, 1280:]
+    for out in (q, x[:, 512:], x[:, 8:1032]):
+        with pytest.raises(tf.TFError, match="out overlaps"):
+            tf.prompt_attention(q, k, v, 2, 4, starts, out=out)
+        with pytest.raises(tf.TFError, match="out overlaps q"):
+            cache.tree_attention(q, 4, dev_pos([0]), dev_i32([[-1] + [0] * 8]), out=out)

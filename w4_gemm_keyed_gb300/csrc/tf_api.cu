@@ -890,6 +890,16 @@ tf_status check_attention(const tf_kv_batch *own, const tf_kv_batch *prefix, int
     return TF_OK;
 }
 
+// Whether two 16-bit arrays of `rows` rows share an element: row strides lda and ldb, of which the first a_cols and
+// b_cols are used.  Of arrays that lie within each other with two strides it is taken for granted.
+bool overlap(const uint16_t *a, int64_t lda, int64_t a_cols, const uint16_t *b, int64_t ldb, int64_t b_cols, int64_t rows) {
+    const int64_t d = (int64_t(reinterpret_cast<uintptr_t>(b)) - int64_t(reinterpret_cast<uintptr_t>(a))) / 2;
+    if (d >= (rows - 1) * lda + a_cols || -d >= (rows - 1) * ldb + b_cols) return false;
+    if (rows == 1 || lda != ldb) return true;
+    const int64_t r = (d % lda + lda) % lda;    // where b's rows begin in a's
+    return r < a_cols || lda - r < b_cols;
+}
+
 bool attn_tree_supported(const tf_kv_batch *own, int32_t group, int32_t n, int32_t prefix_len) {
     return group >= 1 && group <= 16 && n >= 1 && n <= TF_MAX_NODES && n <= own->max_len && prefix_len >= 0;
 }
@@ -1021,6 +1031,9 @@ tf_status tf_attention_tree(const tf_kv_batch *own, const tf_kv_batch *prefix, i
     if ((st = check_attention(own, prefix, prefix_len, group, q, ldq, pos, out, ldo)) != TF_OK) return st;
     if (!parents || !aligned(parents, 4)) return fail(TF_ERR_INVALID_ARG, "null or misaligned parents");
     if ((st = check_ws(ws, ws_bytes, tf_attention_tree_workspace_bytes(own, group, n, prefix_len))) != TF_OK) return st;
+    // the output's first rows are written while queries are still read
+    const int64_t cols = (int64_t)own->n_kv * group * kHeadDim;
+    if (overlap(q, ldq, cols, out, ldo, cols, (int64_t)own->n_seq * n)) return fail(TF_ERR_INVALID_ARG, "out overlaps q");
     AttnTreeArgs a{};
     a.own = kv_batch(*own);
     if (prefix_len > 0) a.prefix = kv_batch(*prefix);
@@ -1056,12 +1069,16 @@ tf_status tf_attention_prompt(const uint16_t *q, int32_t ldq, const uint16_t *k,
     tf_status st = check_ws(ws, ws_bytes, 256);
     if (st != TF_OK) return st;
     if (rows == 0) return ok();
-    const struct { const void *p; int ld, heads; const char *name; } arrays[] = {
+    const struct { const uint16_t *p; int ld, heads; const char *name; } arrays[] = {
         {q, ldq, n_q, "q"}, {k, ldk, n_kv, "k"}, {v, ldv, n_kv, "v"}, {out, ldo, n_q, "out"}};
     for (const auto &t : arrays)
         if (!t.p || !aligned(t.p, 16) || t.ld < t.heads * kHeadDim || t.ld % 8)
             return fail(TF_ERR_INVALID_ARG, "%s must be non-null and 16-B aligned with a row stride that is a multiple "
                         "of 8 and >= %d, got %d", t.name, t.heads * kHeadDim, t.ld);
+    // the output's first rows are written while the others are still read
+    for (const auto &t : arrays)
+        if (&t != &arrays[3] && overlap(t.p, t.ld, (int64_t)t.heads * kHeadDim, out, ldo, (int64_t)n_q * kHeadDim, rows))
+            return fail(TF_ERR_INVALID_ARG, "out overlaps %s", t.name);
     AttnPromptArgs a{};
     a.q = q;
     a.k = k;
