@@ -615,7 +615,9 @@ TF_API tf_status tf_attention_batch(const tf_kv_batch *own, const tf_kv_batch *p
  *   written.  The softmax weights are rounded to bf16 for the product with v
  *   (fp32 in their sum).  A row's bits depend on its query, its place in
  *   its sequence and rows 0 .. i of the sequence alone: not on other rows (infinities
- *   and NaN in them included), other sequences, or where the sequence lies.
+ *   and NaN in them included), other sequences, or where the sequence lies.  Where its scores
+ *   are finite and rows 0 .. i hold values of v that are not, in some column, its output there is their sum (an
+ *   infinity, or NaN), however small their weights are.
  *   rows = 0 does nothing.  ws: >= 256 B.
  */
 TF_API tf_status tf_attention_prompt(const uint16_t *q, int32_t ldq, const uint16_t *k, int32_t ldk,

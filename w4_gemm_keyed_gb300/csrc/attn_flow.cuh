@@ -150,7 +150,7 @@ struct Ring {
 // last become zeros (up to the 16-row step the product reads; they are another sequence's,
 // or nobody's), and non-finite elements of rows that only some vectors see become zero, since
 // 0 * inf would reach the others; the vectors that see them get them back when
-// the output is stored.
+// the output is stored (attn_tiles.cuh).
 template <typename SHARED>
 __device__ void mend_tiles(SHARED *sh, uint8_t *v_tiles) {
     const int lane = threadIdx.x & 31, c = lane & 15;

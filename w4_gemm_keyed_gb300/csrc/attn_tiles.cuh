@@ -68,6 +68,29 @@ __device__ __forceinline__ uint32_t bf16x2_finite(uint32_t w) {   // non-finite 
     return w;
 }
 
+// A weight e^(s - m) is above zero, however far it lies below what the sums hold, so an output whose column
+// of V holds values that are not finite, among the entries that its vector attends over, is their sum: an infinity, or
+// NaN.  A product gives that up to weights that are zero here (0 * inf is NaN), which depends on the rows
+// beside a vector where an entry's value was taken out of a tile and added later.  So the kernels that write
+// outputs look whether one is not finite where its weights' sum is (a product a pair of outputs with a zero), and then
+// look through the entries of its column.  That is a rare and slow path: no tile is looked over for it.
+__device__ __forceinline__ uint32_t probe_finite(uint32_t pair, uint32_t so_far) { return fma_bf16x2(pair, 0u, so_far); }
+// x += the non-finite of a chunk's eight values, or of a quad's four
+__device__ __forceinline__ void add_nonfinite(uint32_t w, float &x0, float &x1) {
+    if ((w & 0x7F80u) == 0x7F80u) x0 += __uint_as_float(w << 16);
+    if ((w & 0x7F800000u) == 0x7F800000u) x1 += __uint_as_float(w & 0xFFFF0000u);
+}
+__device__ __forceinline__ void add_nonfinite(const uint4 &w, float (&x)[8]) {
+    add_nonfinite(w.x, x[0], x[1]);
+    add_nonfinite(w.y, x[2], x[3]);
+    add_nonfinite(w.z, x[4], x[5]);
+    add_nonfinite(w.w, x[6], x[7]);
+}
+// The sum's non-zero elements take the outputs' place.
+__device__ __forceinline__ float4 put_nonfinite(const float4 &out, const float4 &x) {
+    return make_float4(x.x != 0.f ? x.x : out.x, x.y != 0.f ? x.y : out.y, x.z != 0.f ? x.z : out.z, x.w != 0.f ? x.w : out.w);
+}
+
 // Tiled map of bf16 elements, innermost dimension first (its stride is 1; strides in
 // bytes); false and *why where there is none.
 template <int N>
