@@ -648,7 +648,8 @@ TF_API tf_status tf_attention_prompt(const uint16_t *q, int32_t ldq, const uint1
  *   included.  n rows per sequence (pos[b] + n <= max_len, n * group may exceed 128).
  *   Rows of idle sequences and unused rows are zeros; out does not overlap q (refused).  A node's bits depend on its query,
  *   its position pos[b] + depth, prefix_len and the entries it sees, in path order: the same
- *   whether an entry is a node of this pass or was committed before.  ws:
+ *   whether an entry is a node of this pass or was committed before.  Values of V that are not
+ *   finite count as in tf_attention_prompt.  ws:
  *   tf_attention_tree_workspace_bytes (0: unsupported arguments).
  * tf_tree_accept: from the root, the walk goes to the lowest-numbered child whose
  *   token (tokens: dev int32 [n_seq][n], a node's drafted token; the root's is not

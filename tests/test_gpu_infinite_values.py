@@ -118,3 +118,81 @@ def test_a_long_prompt_of_nothing_but_infinities(tf):
     assert out[19000:, 0, :, 3].isnan().all()
     out[19000:, 0, :, 3] = INF
     assert (out == INF).all()
+
+
+# ---------------------------------------------------------------- trees and batches over caches
+class Cached:
+    """A sequence of `own` entries behind a prefix of P, V spoiled at rows of the whole."""
+
+    def __init__(self, tf, seed, kind, P, own, n_kv, g, spoiled, fmt="bf16"):
+        gen = generator(seed)
+        n = P + own
+        self.tf, self.P, self.n_kv, self.g, self.own, self.fmt = tf, P, n_kv, g, own, fmt
+        if kind == "normal":
+            self.q, self.k = normal(gen, n, n_kv * g, 16.0), normal(gen, n, n_kv)
+        else:
+            self.q, self.k = steep(gen, [LEVELS[kind](t) for t in range(n)], n_kv, g)
+        self.v = normal(gen, n, n_kv)
+        self.bad = spoil(self.v.clone(), spoiled)
+
+    def prefix(self, v):
+        if not self.P:
+            return {}
+        c = self.tf.KVBatch(1, self.n_kv, -(-self.P // 256) * 256, self.fmt)
+        c.store(self.k[:self.P], v[:self.P], dev64([0]))
+        return dict(prefix=c, prefix_len=self.P)
+
+    def cache(self, v, n_seq=1, rows=None):
+        at = self.P + (torch.arange(self.own, device="cuda") if rows is None else torch.tensor(rows, device="cuda"))
+        c = self.tf.KVBatch(n_seq, self.n_kv, 1024, self.fmt)
+        c.store(self.k[at].repeat(n_seq, 1), v[at].repeat(n_seq, 1), dev64([0] * n_seq))
+        return c
+
+
+CASES = [  # prefix, own entries before the pass, spoiled rows of prefix + own
+    (0, 12, SPOILED),                                               # near entries, of the pass and before it
+    (0, 60, SPOILED),                                               # far ones
+    (0, 334, [(320, 5, INF), (321, 7, -INF), (322, 7, INF), (325, 9, INF), (318, 4, NAN)]),     # mended for some nodes
+    (0, 700, [(3, 5, INF), (330, 5, INF), (690, 8, -INF), (699, 9, INF)]),
+    (40, 30, SPOILED + [(55, 30, INF), (60, 31, -INF)]),
+    (700, 400, SPOILED + [(600, 40, INF), (650, 41, INF), (1080, 41, -INF), (1095, 42, INF)]),
+]
+
+
+@pytest.mark.parametrize("g", [1, 3, 8])
+@pytest.mark.parametrize("kind", [*LEVELS, "normal"])
+@pytest.mark.parametrize("P,pos,spoiled", CASES)
+def test_tree_and_serial(tf, g, kind, P, pos, spoiled):
+    """A tree of two chains, and the same nodes one a pass: the same bits, the formula's."""
+    n, n_kv = 13, 2
+    c = Cached(tf, P + pos + g, kind, P, pos + n, n_kv, g, spoiled + [(P + pos + 4, 50, INF), (P + pos + 9, 51, -INF)])
+    parents = [-1, 0, 1, 2, 3, 4, 5, 2, 7, 8, 9, 10, 11]
+    q, fixed, was = c.q[P + pos:], c.prefix(c.bad), c.prefix(c.v)
+    ws = tf.workspace(c.cache(c.v).tree_attention_workspace_bytes(g, n, P))
+    clean = c.cache(c.v).tree_attention(q, g, dev64([pos]), dev32([parents]), **was)
+    out = c.cache(c.bad).tree_attention(q, g, dev64([pos]), dev32([parents]), ws=ws, **fixed)
+    assert tf.workspace_status(ws) == tf.TF_DEV_OK
+    two = c.cache(c.bad, 2).tree_attention(q.repeat(2, 1), g, dev64([pos, -1]), dev32([parents] * 2), **fixed)
+    assert torch.equal(bits(two[:n]), bits(out)) and not two[n:].any()
+    for leaf in (6, 12):
+        path = [leaf]
+        while path[0]:
+            path.insert(0, parents[path[0]])
+        serial = c.cache(c.bad, rows=[*range(pos), *(pos + i for i in path)])
+        for d, i in enumerate(path):
+            seen = c.bad[[*range(P + pos), *(P + pos + x for x in path[:d + 1])]]
+            check(out[i], clean[i], seen, g)
+            one = serial.tree_attention(q[i:i + 1], g, dev64([pos + d]), dev32([[-1]]), **fixed)
+            assert torch.equal(bits(one[0]), bits(out[i])), (leaf, d)
+
+
+@pytest.mark.parametrize("kind", [*LEVELS, "normal"])
+def test_8_bit_entries_are_nan_whatever_their_weight(tf, kind):
+    P, pos, n, n_kv, g = 700, 330, 13, 2, 8
+    c = Cached(tf, 9, kind, P, pos + n, n_kv, g, [(650, 5, INF), (1015, D + 9, INF)], "e4m3")
+    q, fixed, cache = c.q[P + pos:], c.prefix(c.bad), c.cache(c.bad)
+    parents = [-1, *range(n - 1)]
+    for out in (cache.tree_attention(q, g, dev64([pos]), dev32([parents]), **fixed), cache.attention(q, g, dev64([pos]), **fixed)):
+        assert out.isnan().all()
+    one = c.cache(c.bad).tree_attention(q[3:4], g, dev64([pos + 3]), dev32([[-1]]), **fixed)
+    assert one.isnan().all()

@@ -86,9 +86,35 @@ __device__ __forceinline__ void add_nonfinite(const uint4 &w, float (&x)[8]) {
     add_nonfinite(w.z, x[4], x[5]);
     add_nonfinite(w.w, x[6], x[7]);
 }
-// The sum's non-zero elements take the outputs' place.
-__device__ __forceinline__ float4 put_nonfinite(const float4 &out, const float4 &x) {
-    return make_float4(x.x != 0.f ? x.x : out.x, x.y != 0.f ? x.y : out.y, x.z != 0.f ? x.z : out.z, x.w != 0.f ? x.w : out.w);
+// The sum of the non-finite values among a quad of columns (4 quad ..) of entries first .. last of one head's bf16 cache.
+__device__ __noinline__ inline float4 cached_nonfinite(const uint16_t *v, int first, int last, int quad) {
+    constexpr int kAtOnce = 8;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int t0 = first; t0 <= last; t0 += kAtOnce) {
+        uint2 w[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {     // the last entry again changes nothing
+            const int t = min(t0 + i, last);
+            w[i] = *reinterpret_cast<const uint2 *>(v + (size_t)t * kHeadDim + 8 * ((quad >> 1) ^ (t & 7)) + 4 * (quad & 1));
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            add_nonfinite(w[i].x, x.x, x.y);
+            add_nonfinite(w[i].y, x.z, x.w);
+        }
+    }
+    return x;
+}
+__device__ __forceinline__ float4 add4(const float4 &x, const float4 &y) {
+    return make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+}
+// The sum's non-zero elements take the place of four outputs.
+__device__ __forceinline__ void put_nonfinite(uint16_t *out, const float4 &x) {
+    if (x.x != 0.f) out[0] = __bfloat16_as_ushort(__float2bfloat16_rn(x.x));
+    if (x.y != 0.f) out[1] = __bfloat16_as_ushort(__float2bfloat16_rn(x.y));
+    if (x.z != 0.f) out[2] = __bfloat16_as_ushort(__float2bfloat16_rn(x.z));
+    if (x.w != 0.f) out[3] = __bfloat16_as_ushort(__float2bfloat16_rn(x.w));
 }
 
 // Tiled map of bf16 elements, innermost dimension first (its stride is 1; strides in

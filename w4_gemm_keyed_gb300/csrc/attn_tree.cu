@@ -781,9 +781,30 @@ __device__ void near_entries(const AttnTreeArgs &a, JoinShared<VECS> *sh, const 
     __syncwarp();       // the next node's values may come
 }
 
+// The sums of the non-finite values that row `row` (a node's) attends over take the place of its outputs of `quads` quads of
+// columns; bf16 caches.
+__device__ __noinline__ void put_seen_nonfinite(const AttnTreeArgs &a, int j, int row, int quad, int quads, uint16_t *out) {
+    const int b = row / a.n;
+    const int32_t *parents = a.parents + (size_t)b * a.n;
+    const int pos = int(a.pos[b]);      // the node is one of a tree, so the position is a good one
+    const uint16_t *const own = static_cast<const uint16_t *>(a.own.v) + (size_t)(b * a.own.n_kv + j) * a.own.max_len * kHeadDim;
+#pragma unroll 1
+    for (int i = 0; i < quads; ++i) {
+        float4 x = cached_nonfinite(own, 0, pos - 1, quad + i);
+        if (a.prefix_len > 0)
+            x = add4(x, cached_nonfinite(static_cast<const uint16_t *>(a.prefix.v) + (size_t)j * a.prefix.max_len * kHeadDim, 0,
+                                         a.prefix_len - 1, quad + i));
+        int node = row - b * a.n;
+        for (; node > 0; node = parents[node])      // a parent's number is lower
+            x = add4(x, cached_nonfinite(own, pos + node, pos + node, quad + i));
+        put_nonfinite(out + 4 * i, add4(x, cached_nonfinite(own, pos, pos, quad + i)));
+    }
+}
+
 template <bool E4M3, int VECS, int SPLIT, int BLOCKS>
-__global__ void __launch_bounds__(kJoinThreads, BLOCKS) attn_tree_join_kernel(AttnTreeArgs a, Plan p, const float *results,
-                                                                         const float2 *ml, unsigned *next) {
+__global__ void __launch_bounds__(kJoinThreads, BLOCKS) attn_tree_join_kernel(const __grid_constant__ AttnTreeArgs a, Plan p,
+                                                                         const float *results, const float2 *ml,
+                                                                         unsigned *next) {
     constexpr int kQuads = VECS / 8 / SPLIT;        // a thread's: `quad` and the ones after it
     extern __shared__ __align__(1024) uint8_t smem[];
     JoinShared<VECS> *sh = reinterpret_cast<JoinShared<VECS> *>(smem);
@@ -861,10 +882,16 @@ __global__ void __launch_bounds__(kJoinThreads, BLOCKS) attn_tree_join_kernel(At
         const __nv_bfloat162 r = __floats2bfloat162_rn(e0 * inv, e1 * inv);
         return *reinterpret_cast<const uint32_t *>(&r);
     };
+    uint32_t probe = 0u;
 #pragma unroll
-    for (int i = 0; i < kQuads; ++i)
-        *reinterpret_cast<uint2 *>(rows + mine * kPitch + 4 * (quad + i)) =
-            make_uint2(pair(sum[i].x, sum[i].y), pair(sum[i].z, sum[i].w));
+    for (int i = 0; i < kQuads; ++i) {
+        const uint2 y = make_uint2(pair(sum[i].x, sum[i].y), pair(sum[i].z, sum[i].w));
+        *reinterpret_cast<uint2 *>(rows + mine * kPitch + 4 * (quad + i)) = y;
+        probe = probe_finite(y.y, probe_finite(y.x, probe));
+    }
+    // 8-bit values are finite or NaN, which any weight gives
+    if (!E4M3 && __builtin_expect(bf16x2_nonfinite(probe) && l > 0.f, 0))
+        put_seen_nonfinite(a, j, row0 + nth, quad, kQuads, rows + mine * kPitch + 4 * quad);
     __syncthreads();
     constexpr int kChunks = 16 / SPLIT;     // of 16 bytes
     for (int i = threadIdx.x; i < here * g * kChunks; i += kJoinThreads) {
