@@ -561,7 +561,9 @@ TF_API tf_status tf_attention_verify(const tf_kv_cache *c, int32_t group, const 
  *   The softmax weights are rounded to bf16 for the product with v (fp32 in
  *   their sum; tf_attention_verify keeps about 16 bits of them).  The prefix is
  *   read once for the whole batch.  Entries no row attends over may hold
- *   anything, infinities and NaN included.  n_seq in 1..1024.  ws:
+ *   anything, infinities and NaN included.  Where a row's scores are finite and its entries hold values of V
+ *   that are not, in some column, its output there is their sum (an infinity, or NaN), however small
+ *   their weights are.  n_seq in 1..1024.  ws:
  *   tf_attention_batch_workspace_bytes of scratch (0: unsupported arguments),
  *   which follows max_len, n_seq and prefix_len, whatever the positions are.
  */

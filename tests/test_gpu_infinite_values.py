@@ -186,6 +186,25 @@ def test_tree_and_serial(tf, g, kind, P, pos, spoiled):
             assert torch.equal(bits(one[0]), bits(out[i])), (leaf, d)
 
 
+@pytest.mark.parametrize("g", [1, 3, 8])
+@pytest.mark.parametrize("kind", [*LEVELS, "normal"])
+@pytest.mark.parametrize("P,pos,spoiled", CASES + [(0, 510, [(500, 5, INF), (505, 7, -INF), (508, 7, INF)])])
+def test_batch_rows_and_one(tf, g, kind, P, pos, spoiled):
+    """Several rows a pass, one, and another sequence beside them: the same bits, the formula's."""
+    R, n_kv = 13, 2
+    c = Cached(tf, P + pos + g, kind, P, pos + R, n_kv, g, spoiled + [(P + pos + 4, 50, INF), (P + pos + 9, 51, -INF)])
+    q, fixed, was = c.q[P + pos:], c.prefix(c.bad), c.prefix(c.v)
+    cache = c.cache(c.bad)
+    clean = c.cache(c.v).attention(q, g, dev64([pos]), **was)
+    out = cache.attention(q, g, dev64([pos]), **fixed)
+    two = c.cache(c.bad, 2).attention(q.repeat(2, 1), g, dev64([-1, pos]), **fixed)
+    assert torch.equal(bits(two[R:]), bits(out)) and not two[:R].any()
+    for r in range(R):
+        check(out[r], clean[r], c.bad[:P + pos + r + 1], g)
+        one = cache.attention(q[r:r + 1], g, dev64([pos + r]), **fixed)
+        assert torch.equal(bits(one[0]), bits(out[r])), r
+
+
 @pytest.mark.parametrize("kind", [*LEVELS, "normal"])
 def test_8_bit_entries_are_nan_whatever_their_weight(tf, kind):
     P, pos, n, n_kv, g = 700, 330, 13, 2, 8

@@ -881,8 +881,23 @@ __global__ void __launch_bounds__(Form<E4M3>::threads, 1) attn_batch_kernel(cons
 // these); where there are few, the chain of three loads does.
 constexpr int kJoinRuns = 4, kJoinUnroll = 4, kJoinThreads = 32 * kJoinRuns;
 
-__global__ void __launch_bounds__(kJoinThreads, 6) attn_batch_join_kernel(AttnBatchArgs a, Plan p, const float *opart,
-                                                                          const float2 *ml, unsigned *next) {
+// The sums of the non-finite values that vector v of KV head j attends over take the place of its outputs of two quads of
+// columns; bf16 caches.
+__device__ __noinline__ void put_seen_nonfinite(const AttnBatchArgs &a, int j, int v, int quad, uint16_t *out) {
+    const int row = v / a.group, b = row / a.R, last = int(a.pos[b]) + row - b * a.R;   // a sequence that is not idle
+    const uint16_t *const own = static_cast<const uint16_t *>(a.own.v) + (size_t)(b * a.own.n_kv + j) * a.own.max_len * kHeadDim;
+    const uint16_t *const prefix = static_cast<const uint16_t *>(a.prefix.v) + (size_t)j * a.prefix.max_len * kHeadDim;
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+        float4 x = cached_nonfinite(own, 0, last, quad + i);
+        if (a.prefix_len > 0) x = add4(x, cached_nonfinite(prefix, 0, a.prefix_len - 1, quad + i));
+        put_nonfinite(out + 4 * i, x);
+    }
+}
+
+__global__ void __launch_bounds__(kJoinThreads, 6) attn_batch_join_kernel(const __grid_constant__ AttnBatchArgs a, Plan p,
+                                                                          const float *opart, const float2 *ml,
+                                                                          unsigned *next) {
     __shared__ float s_top[kJoinRuns][32], s_l[kJoinRuns][32];
     __shared__ float4 s_o[kJoinRuns][2][32];
     const int lane = threadIdx.x & 31, run = threadIdx.x >> 5, quad = 2 * blockIdx.z;
@@ -995,7 +1010,11 @@ __global__ void __launch_bounds__(kJoinThreads, 6) attn_batch_join_kernel(AttnBa
         y = make_uint4(pair(o[0].x, o[0].y), pair(o[0].z, o[0].w), pair(o[1].x, o[1].y), pair(o[1].z, o[1].w));
     }
     const int row = idx_div(v, a.group);
-    *reinterpret_cast<uint4 *>(a.out + (size_t)row * a.ldo + (size_t)(j * a.group + v - row * a.group) * kHeadDim + 4 * quad) = y;
+    uint16_t *const out = a.out + (size_t)row * a.ldo + (size_t)(j * a.group + v - row * a.group) * kHeadDim + 4 * quad;
+    *reinterpret_cast<uint4 *>(out) = y;
+    // 8-bit values are finite or NaN, which any weight gives
+    const uint32_t probe = probe_finite(y.x, probe_finite(y.y, probe_finite(y.z, probe_finite(y.w, 0u))));
+    if (__builtin_expect(bf16x2_nonfinite(probe) && l > 0.f && a.own.format != kKvE4m3, 0)) put_seen_nonfinite(a, j, v, quad, out);
 }
 
 // Innermost first: an entry's 128 elements, entries, (sequence, head).  The cache
