@@ -79,3 +79,34 @@ def test_an_output_in_an_input_is_refused(tf):
             tf.prompt_attention(q, k, v, 2, 4, starts, out=out)
         with pytest.raises(tf.TFError, match="out overlaps q"):
             cache.tree_attention(q, 4, dev_pos([0]), dev_i32([[-1] + [0] * 8]), out=out)
+
+
+# ---------------------------------------------------------------- a call's own workspace
+@pytest.mark.parametrize("op", ["tree", "batch"])
+def test_a_calls_own_workspace_may_hold_anything(tf, op):
+    """Above 32 MB it is not cleared as a whole: the same bits as on a cleared one, and no device error."""
+    B, n, n_kv, g, P = 24, 8, 8, 8, 700
+    cache, prefix = tf.KVBatch(B, n_kv, 8192), tf.KVBatch(1, n_kv, 768)
+    size = cache.tree_attention_workspace_bytes(g, n, P) if op == "tree" else cache.attention_workspace_bytes(g, n, P)
+    assert size > 32 << 20
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    for c in (cache, prefix):
+        rows = [torch.randn((c.n_seq * 700, n_kv * 128), generator=gen, device="cuda").to(torch.bfloat16) for _ in range(2)]
+        c.store(*rows, dev_pos([0] * c.n_seq))
+    q = torch.randn((B * n, n_kv * g * 128), generator=gen, device="cuda").to(torch.bfloat16)
+    pos, parents = dev_pos([28 * b for b in range(B)]), dev_i32([[-1, *range(n - 1)]] * B)
+
+    def call(**kw):
+        if op == "tree":
+            return cache.tree_attention(q, g, pos, parents, prefix=prefix, prefix_len=P, **kw)
+        return cache.attention(q, g, pos, prefix=prefix, prefix_len=P, **kw)
+    want, side = call(ws=tf.workspace(size)), torch.cuda.Stream()
+    for stream in (None, side):
+        with torch.cuda.stream(stream):
+            dirty = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        del dirty       # the allocator hands its memory to the call
+        got = call(stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)

@@ -195,6 +195,20 @@ def workspace(nbytes: int, device="cuda", stream=None) -> torch.Tensor:
         return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
+_CLEARED_WHOLE = 32 << 20    # bytes that are as quickly cleared as allocated: 11 us, 14 with 256 of them; 64 MB 18, 560 MB 145
+
+
+def _parts_workspace(nbytes: int, device, stream=None) -> torch.Tensor:
+    """The workspace of one attention call over parts: such a call writes every result before it
+    reads it, and only the status block, with its item counters, has to be zero."""
+    if nbytes <= _CLEARED_WHOLE:
+        return workspace(nbytes, device, stream)
+    with torch.cuda.stream(stream):     # None: the current one
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ws[:256].zero_()
+    return ws
+
+
 def _empty(shape, dtype, device, stream=None) -> torch.Tensor:
     """A call's own output: memory of the stream that the call runs on, so that nothing
     still queued elsewhere uses it, marked as used on the caller's stream too."""
@@ -758,7 +772,7 @@ class KVBatch:
         else:
             ldo = _bits16(out, "out", n, cols, dev)
         if ws is None:
-            ws = workspace(self.attention_workspace_bytes(group, R, prefix_len), dev, stream)
+            ws = _parts_workspace(self.attention_workspace_bytes(group, R, prefix_len), dev, stream)
         st = load().tf_attention_batch(self._c, prefix._c if prefix is not None else None, prefix_len, group,
                                        q.data_ptr(), ldq, R, at, out.data_ptr(), ldo, _ptr(ws), _bytes(ws, dev),
                                        _stream(stream))
@@ -791,7 +805,7 @@ class KVBatch:
         else:
             ldo = _bits16(out, "out", rows, cols, dev)
         if ws is None:
-            ws = workspace(self.tree_attention_workspace_bytes(group, n, prefix_len), dev, stream)
+            ws = _parts_workspace(self.tree_attention_workspace_bytes(group, n, prefix_len), dev, stream)
         st = load().tf_attention_tree(self._c, prefix._c if prefix is not None else None, prefix_len, group,
                                       q.data_ptr(), ldq, n, at, tree, out.data_ptr(), ldo, _ptr(ws), _bytes(ws, dev),
                                       _stream(stream))
