@@ -110,3 +110,59 @@ def test_a_calls_own_workspace_may_hold_anything(tf, op):
         got = call(stream=stream)
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+# ---------------------------------------------------------------- many sequences, many heads
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("B,n,P,longest", [(129, 5, 0, 1500), (300, 2, 300, 1000), (1024, 3, 0, 700), (1000, 4, 600, 330)])
+def test_more_sequences_than_the_table_of_own_parts(tf, B, n, P, longest, fmt):
+    """Above 128 sequences an entry of that table is several of them; idle ones leave whole entries without parts.
+    The bits are those of calls of 64."""
+    n_kv, g = 1, 4
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(B)
+
+    def normal(rows, heads):
+        return torch.randn((rows, heads * 128), generator=gen, device="cuda").to(torch.bfloat16)
+    at = [(7919 * b) % longest for b in range(B)]
+    for first, count in ((0, 20), (B // 3, 40), (B - 17, 17)):      # runs of idle sequences, at both ends too
+        at[first:first + count] = [-1] * count
+    at[B // 2], at[B // 2 + 1], at[B // 2 + 2] = 0, 16, 17          # no far entry, and the first ones
+    L = -(-(longest + n) // 256) * 256
+    cache, prefix = tf.KVBatch(B, n_kv, L, fmt), tf.KVBatch(1, n_kv, 768, fmt)
+    cache.store(normal(B * L, n_kv), normal(B * L, n_kv), dev_pos([0] * B))
+    prefix.store(normal(768, n_kv), normal(768, n_kv), dev_pos([0]))
+    q = normal(B * n, n_kv * g)
+    parents = [[-1] + [(5 * b + i) % i if (b + i) % 9 else i - 1 for i in range(1, n)] for b in range(B)]
+    ws = tf.workspace(cache.tree_attention_workspace_bytes(g, n, P))
+    for _ in range(2):
+        out = cache.tree_attention(q, g, dev_pos(at), dev_i32(parents), prefix=prefix, prefix_len=P, ws=ws).view(B, n, -1)
+        assert tf.workspace_status(ws) == tf.TF_DEV_OK
+    for first in range(0, B, 64):
+        m = min(64, B - first)
+        some = tf.KVBatch(m, n_kv, L, fmt)
+        for name in ("k", "v", "k_scale", "v_scale"):
+            if getattr(some, name) is not None:
+                getattr(some, name).copy_(getattr(cache, name)[first:first + m])
+        part = some.tree_attention(q[first * n:(first + m) * n], g, dev_pos(at[first:first + m]), dev_i32(parents[first:first + m]),
+                                   prefix=prefix, prefix_len=P).view(m, n, -1)
+        assert torch.equal(part, out[first:first + m]), first
+    used = torch.tensor(at, device="cuda") >= 0
+    assert out[used].view(int(used.sum()), -1).any(1).all() and not out[~used].any()
+
+
+@pytest.mark.parametrize("n_kv,g,P", [(76, 1, 1300), (77, 2, 1300), (128, 1, 561), (128, 1, 1201)])
+def test_heads_whose_prefix_is_one_part(tf, n_kv, g, P):
+    """Above 76 KV heads a prefix is not split; at 76 it is."""
+    from test_gpu_trees import Case
+    c = Case(tf, n_kv + P, [[-1, 0, 0, 2], [-1, 0, 1, -1]], n_kv, g, P, [330, 3], "bf16")
+    ws = tf.workspace(c.cache.tree_attention_workspace_bytes(g, 4, P))
+    out = c.run(ws=ws)
+    assert tf.workspace_status(ws) == tf.TF_DEV_OK
+    c.check(out)
+    assert torch.equal(out, c.run(ws=ws))
+
+
+def test_8_bit_heads_whose_prefix_is_one_part(tf):
+    from test_gpu_trees import test_large_batches_give_each_sequence_its_own_bits as same_as_16_bits
+    same_as_16_bits(tf, 3, 4, 77, 1, 1300, "e4m3")
