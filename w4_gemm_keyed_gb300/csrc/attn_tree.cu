@@ -40,7 +40,6 @@ constexpr int kMinPrefixPart = 560;
 // Items of a batch that is one pair of tiles, about.  Twice as many: 4 x 8 nodes over 30000 entries 39 us (52), 24 x 64 over 32768
 // 1,241 (1,099), 5 x 24 over 8192 64 (53).
 constexpr int kPrefixItems = 76;
-constexpr int kSms = 152;
 // An E4M3 prefix is expanded into the workspace first where that pays: it saves every pair of query tiles
 // 28 ns per 1,000 entries and head, costs 76 ns and the two further grids 10 us, so from (pairs - 3) x entries x heads = 340,000 on
 // (16 x 32 nodes, 16 pairs, over 16461 x 8: 262 us, 301 without; 16 x 8 nodes, 4 pairs, over 16000 x 8: 87, 82 without;
@@ -92,7 +91,8 @@ __host__ __device__ inline int prefix_part(int prefix_len, int n_kv) {
     return int(part < kMinPrefixPart ? kMinPrefixPart : (part > 0x7FFFFFFF ? 0x7FFFFFFF / kKeys * kKeys : part));
 }
 
-Plan plan_of(const KvBatch &own, int prefix_len, int group, int n) {
+// sms: SMs that items of one and of two tiles are weighed for; no size in the workspace follows it.
+Plan plan_of(const KvBatch &own, int prefix_len, int group, int n, int sms) {
     Plan p;
     p.rows = own.n_seq * n;
     p.rows_tile = kTile / group;
@@ -105,7 +105,7 @@ Plan plan_of(const KvBatch &own, int prefix_len, int group, int n) {
     auto items = [](int rows, int rows_item) { return (rows + rows_item - 1) / rows_item; };
     const int both = 2 * p.rows_tile;
     auto rows_item = [&](long long parts, int rows) {
-        auto rounds = [&](int of) { return (parts * items(rows, of) + kSms - 1) / kSms; };
+        auto rounds = [&](int of) { return (parts * items(rows, of) + sms - 1) / sms; };
         return 17 * rounds(both) <= 10 * rounds(p.rows_tile) ? both : p.rows_tile;
     };
     p.rows_item = rows_item((long long)p.n_parts * own.n_kv, p.rows);
@@ -920,7 +920,7 @@ bool encode_cache(CUtensorMap *m, const void *base, int rows, int max_len, int o
 constexpr size_t kCounterAt = 128, kResultsAt = 256 + kCounterBytes;
 
 size_t attn_tree_bytes(const KvBatch &own, int prefix_len, int group, int n) {
-    const Plan p = plan_of(own, prefix_len, group, n);
+    const Plan p = plan_of(own, prefix_len, group, n, 1);
     return kResultsAt + size_t(slots_of(p, own.n_kv, group)) * (kHeadDim * sizeof(float) + sizeof(float2)) +
            expanded_bytes(p, prefix_len, own.n_kv);
 }
@@ -986,7 +986,8 @@ cudaError_t launch_join(const KernelArgs &k, cudaStream_t s) {
 cudaError_t launch_attn_tree(const AttnTreeArgs &a, cudaStream_t s, const char **why) {
     KernelArgs k{};
     k.a = a;
-    k.p = plan_of(a.own, a.prefix_len, a.group, a.n);
+    const int sms = device_sm_count();
+    k.p = plan_of(a.own, a.prefix_len, a.group, a.n, sms > 0 ? sms : 1);
     char *base = static_cast<char *>(a.ws);
     k.next = reinterpret_cast<unsigned *>(base + kCounterAt);
     const size_t slots = size_t(slots_of(k.p, a.own.n_kv, a.group));
