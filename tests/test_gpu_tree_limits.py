@@ -166,3 +166,107 @@ def test_heads_whose_prefix_is_one_part(tf, n_kv, g, P):
 def test_8_bit_heads_whose_prefix_is_one_part(tf):
     from test_gpu_trees import test_large_batches_give_each_sequence_its_own_bits as same_as_16_bits
     same_as_16_bits(tf, 3, 4, 77, 1, 1300, "e4m3")
+
+
+# ---------------------------------------------------------------- calls side by side, passes in a graph, far offsets
+def normal_rows(gen, rows, heads):
+    return torch.randn((rows, heads * 128), generator=gen, device="cuda").to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_a_prompt_and_trees_at_the_same_time(tf, fmt):
+    """On two streams, each with workspaces of its own: the bits of calls by themselves."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(8)
+    x, starts = normal_rows(gen, 3000, 32 + 16), torch.tensor([0, 5, 1400, 3000], device="cuda")
+    q, k, v = x[:, :4096], x[:, 4096:5120], x[:, 5120:]
+    B, n, P = 12, 32, 5003
+    cache, prefix = tf.KVBatch(B, 4, 512, fmt), tf.KVBatch(1, 4, 5120, fmt)
+    cache.store(normal_rows(gen, B * 512, 4), normal_rows(gen, B * 512, 4), dev_pos([0] * B))
+    prefix.store(normal_rows(gen, 5120, 4), normal_rows(gen, 5120, 4), dev_pos([0]))
+    tq, pos, tree = normal_rows(gen, B * n, 32), dev_pos([37 * b for b in range(B)]), dev_i32([[-1] + [i // 2 for i in range(n - 1)]] * B)
+    size = cache.tree_attention_workspace_bytes(8, n, P)
+
+    def prompt(out, ws, stream=None):
+        tf.prompt_attention(q, k, v, 8, 4, starts, out=out, ws=ws, stream=stream)
+
+    def trees(out, ws, stream=None):
+        cache.tree_attention(tq, 8, pos, tree, prefix=prefix, prefix_len=P, out=out, ws=ws, stream=stream)
+    wide = torch.empty((3000, 4096), dtype=torch.bfloat16, device="cuda")
+    want, two = [wide, torch.empty_like(tq)], [tf.workspace(256), tf.workspace(size)]
+    prompt(want[0], two[0])
+    trees(want[1], two[1])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        got = [torch.zeros_like(t) for t in want]
+        torch.cuda.synchronize()
+        for _ in range(5):
+            prompt(got[0], two[0], streams[0])
+            trees(got[1], two[1], streams[1])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(tf.workspace_status(ws) == tf.TF_DEV_OK for ws in two)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_a_captured_pass_over_trees(tf, fmt):
+    """Store, attention, acceptance and the kept entries in one graph, replayed for other trees and positions: what the calls
+    do one by one."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(9)
+    B, n, n_kv, g, P = 3, 20, 2, 4, 700
+    pair = [tf.KVBatch(B, n_kv, 512, fmt) for _ in range(2)]
+    prefix = tf.KVBatch(1, n_kv, 768, fmt)
+    prefix.store(normal_rows(gen, 768, n_kv), normal_rows(gen, 768, n_kv), dev_pos([0]))
+    start = normal_rows(gen, B * 400, n_kv)
+    for c in pair:
+        c.store(start, start, dev_pos([0] * B))
+    x = normal_rows(gen, B * n, n_kv * (g + 2))
+    pos, ints = dev_pos([0] * B), dev_i32([[[-1] + [0] * (n - 1)] * B, [[0] * n] * B, [[0] * n] * B])
+    ws = tf.workspace(pair[0].tree_attention_workspace_bytes(g, n, P))
+    ko, vo = n_kv * g * 128, n_kv * (g + 1) * 128
+
+    def step(cache, ws=None):
+        cache.store(x[:, ko:vo], x[:, vo:], pos, ws=ws)
+        o = cache.tree_attention(x[:, :ko], g, pos, ints[0], prefix=prefix, prefix_len=P, ws=ws)
+        took = tf.tree_accept(ints[0], ints[1], ints[2], pos, ws=ws)
+        cache.keep(pos, took[2], ws=ws)
+        return [o, *took]
+    step(pair[0], ws)
+    step(pair[1])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step(pair[0], ws)
+    for i, at in enumerate(([400, 380, -1], [405, -1, 3], [410, 399, 200])):
+        x.copy_(normal_rows(gen, B * n, n_kv * (g + 2)))
+        pos.copy_(dev_pos(at))
+        ints.copy_(dev_i32([[[-1] + [(7 * b + i + r) % r for r in range(1, n)] for b in range(B)],
+                            [[(3 * r + b) % 2 for r in range(n)] for b in range(B)],
+                            [[(r + b + i) % 2 for r in range(n)] for b in range(B)]]))
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(held, step(pair[1])))
+        assert torch.equal(pair[0].k, pair[1].k) and torch.equal(pair[0].v, pair[1].v)
+    assert tf.workspace_status(ws) == tf.TF_DEV_OK
+
+
+def test_a_prompt_past_32_bits_of_elements(tf):
+    """Offsets into the rows pass 2^32 bytes and 2^31 elements."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(10)
+    n, each, n_kv, g = 1024, 300, 8, 8
+    x = torch.empty((n * each, (n_kv * g + 2 * n_kv) * 128), dtype=torch.bfloat16, device="cuda")
+    part = normal_rows(gen, 4 * each, n_kv * (g + 2))
+    for s in range(0, n, 4):
+        x[s * each:(s + 4) * each] = part
+    x[-each:] = normal_rows(gen, each, n_kv * (g + 2))
+    assert n * each * n_kv * g * 128 > 2 ** 31
+
+    def call(rows, starts, ws=None):
+        q, k, v = rows[:, :n_kv * g * 128], rows[:, n_kv * g * 128:n_kv * (g + 1) * 128], rows[:, n_kv * (g + 1) * 128:]
+        return tf.prompt_attention(q, k, v, n_kv, g, torch.tensor(starts, device="cuda"), ws=ws)
+    ws = tf.workspace(256)
+    out = call(x, [each * s for s in range(n + 1)], ws)
+    assert tf.workspace_status(ws) == tf.TF_DEV_OK
+    for s in (0, 1, n // 2, n - 2, n - 1):
+        assert torch.equal(out[s * each:(s + 1) * each], call(x[s * each:(s + 1) * each].contiguous(), [0, each]))
