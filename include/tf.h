@@ -633,7 +633,11 @@ TF_API tf_status tf_attention_prompt(const uint16_t *q, int32_t ldq, const uint1
  * A pass may verify a tree of drafts instead of a chain: several continuations
  * of one token, of which at most one survives.  The guarantee is the chain's
  * (README, the two guarantees): a node's bits are those of decoding its path one
- * token a pass, so the tree changes the speed and never a token.
+ * token a pass with the same call (n = 1), so the tree changes the speed and never a
+ * token.  tf_attention_batch and tf_attention_verify add up the same entries in other
+ * groups and round otherwise, and so does tf_attention_prompt: two runs whose tokens have to
+ * agree read their prompts by the same call and decode by the same call, passes of one
+ * token included.
  *
  * A tree has n rows, n in 1..TF_MAX_NODES, per sequence; node i of sequence b is row
  * b * n + i.  parents: dev int32 [n_seq][n]: parents[b][0] = -1 (node 0, the

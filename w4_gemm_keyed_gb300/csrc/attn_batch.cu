@@ -581,7 +581,7 @@ __device__ void multiply(const KernelArgs &k, Shared *sh, uint8_t *q_tiles, uint
 }
 
 // Rows that see an own entry with non-finite values get them back: mend_values
-// took them out of the product.  x: one element of the output, d its index.
+// took them out of the product.  The join then finds such an output (put_seen_nonfinite).  x: one element of the output, d its index.
 template <bool E4M3>
 __device__ __forceinline__ float with_nonfinite(const KernelArgs &k, const Item &it, int first, int last, int d, float x) {
     for (int t = first; t <= last; ++t) {

@@ -15,7 +15,7 @@
 // order, the near ones last.  So bits depend on a node's query, position, P and the entries that it sees.
 //
 // What bounds it (GB300, call after call on the same inputs): many nodes, the tensor cores and what
-// storing an item's results takes, 128 KB at 28 bytes a cycle (24 x 64 nodes x 64 heads over 32768 entries 1,077 us: parts 973 at
+// storing an item's results takes, 128 KB at 28 bytes a cycle (24 x 64 nodes x 64 heads over 32768 entries 1,075 us: parts 973 at
 // 1.50 PFLOP/s, the sum 93 at 5.2 TB/s); few, the steps one SM has in a row (5 x 24 nodes over 8192 41 us: two items of 12
 // steps, the sum 11; 3 x 41 nodes x 20 heads over own 12007 31 us) or launches (8 nodes over 300 entries 10.7 us).  E4M3 where nothing is
 // expanded first, the chain copy - expand - product - softmax of a step (16 nodes over 30000 50 us, 37 as a bf16 cache).
@@ -34,16 +34,17 @@ using namespace flow;
 
 constexpr int kOwnPart = 320;           // own entries per part
 // Shared entries per part, at least: an item's results take as long to store as two and a half steps.  With 240: 64 x 64 nodes over
-// 500 entries 307 us (238), 32 x 16 over 1000 61 (44), but 8 over 300 9.7 (10.7), 8 over 2000 10.8 (12.5); with 960 30 x 40 over 3000
-// 85 (97), 8 over 2000 15.4.
+// 500 entries 297 us (225), 32 x 16 over 1000 60 (43), but 8 over 300 9.9 (11.1), 8 over 2000 10.9 (12.7); with 960 30 x 40 over 3000
+// 83 (95), 8 over 2000 15.6, 64 x 64 of one head over 1000 23.8 (22.0).
 constexpr int kMinPrefixPart = 560;
-// Items of a batch that is one pair of tiles, about.  Twice as many: 4 x 8 nodes over 30000 entries 39 us (52), 24 x 64 over 32768
-// 1,241 (1,099), 5 x 24 over 8192 64 (53).
+// Items of a batch that is one pair of tiles, about.  Twice as many: 1 x 16 nodes over 65536 entries 57 us (69), over 30000 8-bit ones
+// 37 (51), 4 x 8 over 30000 41 (44), but 24 x 64 over 32768 1,228 (1,074), 16 x 32 over 16461 8-bit ones 297 (257), 8 x 8 over 16000
+// 43 (37), 5 x 24 over 8192 48 (41).
 constexpr int kPrefixItems = 76;
 // An E4M3 prefix is expanded into the workspace first where that pays: it saves every pair of query tiles
 // 28 ns per 1,000 entries and head, costs 76 ns and the two further grids 10 us, so from (pairs - 3) x entries x heads = 340,000 on
-// (16 x 32 nodes, 16 pairs, over 16461 x 8: 262 us, 301 without; 16 x 8 nodes, 4 pairs, over 16000 x 8: 87, 82 without;
-// 32 x 16 nodes, 16 pairs, over 1000 x 8: 76, 70 without).
+// (16 x 32 nodes, 16 pairs, over 16461 x 8: 257 us, 297 without; 16 x 8 nodes, 4 pairs, over 16000 x 8: 85, 80 without;
+// 32 x 16 nodes, 16 pairs, over 1000 x 8: 55, 51 without).
 constexpr long long kExpandWork = 340000;
 constexpr int kGroups = 128;            // entries of the table of own items
 constexpr int kProducerWarp = 8, kScoreWarp = 9, kMendWarp = 11;
@@ -100,8 +101,8 @@ Plan plan_of(const KvBatch &own, int prefix_len, int group, int n, int sms) {
     p.n_parts = prefix_len > 0 ? (prefix_len - 1) / p.part + 1 : 0;
     p.own_parts_max = (own.max_len + kOwnPart - 1) / kOwnPart;
     // Two tiles share each K and V tile, and a step of both takes 1.7 times as long as of one alone: one tile an
-    // item where the SMs are then done sooner (4 x 8 nodes over 30000 entries, 72 items of two: 41 us, 52 as two; 8 x 8 over 16000,
-    // 144: 39 as two, 50 as one).  Own parts: at most as many as the caches hold.
+    // item where the SMs are then done sooner (4 x 8 nodes over 30000 entries, 72 items of two: 40-44 us, 54 as two; 8 x 8 over 16000,
+    // 144: 37 as two, 47 as one).  Own parts: at most as many as the caches hold.
     auto items = [](int rows, int rows_item) { return (rows + rows_item - 1) / rows_item; };
     const int both = 2 * p.rows_tile;
     auto rows_item = [&](long long parts, int rows) {
@@ -429,7 +430,7 @@ __device__ void expand_tiles(Shared<true> *sh, const bool is_v, uint8_t *tiles_o
 }
 
 // Nodes that see an own entry with non-finite values get them back: they had been left out of the
-// product.  out: a stored result, its quads `step` apart; first .. last: the item's entries in question.
+// product.  The kernel that adds up the parts then finds such an output (put_seen_nonfinite).  out: a stored result, its quads `step` apart; first .. last: the item's entries in question.
 template <bool E4M3>
 __device__ __noinline__ void add_nonfinite(const AttnTreeArgs &a, int b, int j, int key0, int first, int last, float4 *out,
                                            size_t step) {
@@ -964,11 +965,12 @@ cudaError_t launch_join(const KernelArgs &k, cudaStream_t s) {
         if (dev >= 0 && dev < kMaxDevices) opted_in[dev] = true;
     }
     const AttnTreeArgs &a = k.a;
-    // Vectors of a CTA of the sum: no more than 16 nodes, two a warp (64 x 64 nodes of one head, 8 vectors: 23 us in all, 32: 27;
-    // 40 x 20 of three, 8: 30, 32: 23).  Columns split where there are fewer CTAs than kSplitCtas
-    // (3 x 41 nodes, 84 CTAs, over own 12007 entries: 32 us, 43 without; 5 x 24, 240 CTAs: 53, 44 without).
-    // Three CTAs an SM, with half the loads on their way, from kFullCtas on (24 x 64 nodes of 8 heads: 1066 us, 1078 with
-    // two; 5 x 24: 45, 44 with two).
+    // Vectors of a CTA of the sum: no more than 16 nodes, two a warp (64 x 64 nodes of one head, 8 vectors: 22 us in all, 32: 26;
+    // 40 x 20 of three, 8: 28, 32: 21).  Columns split where there are fewer CTAs than kSplitCtas
+    // (3 x 41 nodes, 84 CTAs, over own 12007 entries: 31 us, 41 without; 5 x 24, 240 CTAs: 52, 41 without; few parts gain
+    // nothing: 8 nodes over 300 entries 11.1, 10.1 without).
+    // Three CTAs an SM, with half the loads on their way, from kFullCtas on (24 x 64 nodes of 8 heads: 1,074 us, 1,086 with
+    // two; 64 x 64 over 500 entries 225, 254 with two; 5 x 24: 43, 41 with two).
     constexpr int kSplitCtas = 100, kFullCtas = 456;
     const int vecs = a.group == 1 ? 8 : 32, nodes = vecs / a.group, ctas = (k.p.rows + nodes - 1) / nodes * a.own.n_kv;
     auto join = [&](auto kernel, int split, size_t smem) {

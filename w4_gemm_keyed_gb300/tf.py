@@ -790,7 +790,9 @@ class KVBatch:
         """bf16 [n_seq*n][n_kv*group*128]: node i of sequence b's tree (parents int32 [n_seq][n],
         -1 for the root, node 0, and for unused rows; entry pos[b] + i stored) attending over entries
         0..prefix_len-1 of `prefix`, own entries 0..pos[b]-1 and its path's; rows of
-        idle sequences and unused rows are zeros."""
+        idle sequences and unused rows are zeros.  A node's bits are those of its path decoded one
+        token a pass by this call, not by `attention`, which adds up in another order: a run
+        uses one of them throughout.  `out` does not overlap `q`."""
         if group < 1:
             raise TFError(TF_ERR_UNSUPPORTED, f"group={group} outside [1, 16]")
         cols, dev = self.n_kv * group * HEAD_DIM, self.device
@@ -867,7 +869,9 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, n_kv: in
     """bf16 [rows][n_kv*group*128]: causal attention of whole prompts.  Sequence s holds rows
     starts[s] .. starts[s+1]-1 (int64 [n_seq + 1], on the device) of q [rows][n_kv*group*128]
     and of k and v [rows][n_kv*128] (bf16 / int16 bits, any row stride that is a multiple of 8:
-    columns of one projection, say); rows outside every sequence are not written."""
+    columns of one projection, say); rows outside every sequence are not written.  `out` overlaps
+    none of the inputs.  A prompt read in passes of `KVBatch.attention` rounds otherwise: runs whose
+    tokens have to agree read their prompts the same way."""
     if group < 1 or n_kv < 1:
         raise TFError(TF_ERR_UNSUPPORTED, f"n_kv={n_kv}, group={group} must be >= 1")
     dev, cols = q.device, n_kv * group * HEAD_DIM
