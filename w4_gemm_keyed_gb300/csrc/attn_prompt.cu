@@ -15,10 +15,10 @@
 // The flow through a CTA: attn_flow.cuh.
 //
 // What bounds it (GB300, call after call on the same inputs): long prompts, the tensor cores
-// and the power limit (32768 rows x 32 heads 5,220 us, 1.68 PFLOP/s; the softmax and its hand-overs make a step of two tiles and 80
+// and the power limit (32768 rows x 32 heads 5,250 us, 1.68 PFLOP/s; the softmax and its hand-overs make a step of two tiles and 80
 // keys 1,640 cycles where its products take 1,440); pages, the change from item to item, 2,000 to 3,000 cycles (2047 rows x 64
-// heads 56 us, five of up to 4099 rows x 20 heads 228); many short ones, one thread's finding and copying of an item, 5,000 to 8,000
-// cycles, next to 40 us of HBM time (48 of up to 301 rows x 64 heads 63 us); one token, the launch (5.4 us).
+// heads 56 us, five of up to 4099 rows x 20 heads 230); many short ones, one thread's finding and copying of an item, 5,000 to 8,000
+// cycles, next to 40 us of HBM time (48 of up to 301 rows x 64 heads 63 us); one token, the launch (5.6 us).
 #include <atomic>
 
 #include "attn_prompt.cuh"
@@ -277,8 +277,9 @@ __device__ __noinline__ void put_seen_nonfinite(const AttnPromptArgs &a, int j, 
 }
 
 // Outputs over their weight sums, as bf16: a thread per vector, 32 bytes (a whole
-// sector) at a time.  Looking whether one of them is not finite takes 0.2 us of a call's 5.6 and at most 1 % of a long
-// one; a test of each word's bits took as long.
+// sector) at a time.  Looking whether one of them is not finite takes 0.2 us of a call's 5.6, and 0 to 1 % of
+// longer ones (12000 rows x 16 heads 1.5 %); a test of each word's bits took as long.  With every value of v infinite, 32768 rows x 32
+// heads take 33 ms (5.2).
 __device__ void store_outputs(const KernelArgs &k, Shared *sh, uint32_t tmem) {
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) - kStoreWarp, v = 32 * quarter + lane;
     const int g = k.a.group, my_row = v / g;
@@ -328,13 +329,17 @@ __device__ void store_outputs(const KernelArgs &k, Shared *sh, uint32_t tmem) {
                     }
                 }
                 tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->o_free[t]);
+                // the next products need not wait for what follows; `l` has been read, and the slot is kept
                 const bool mine = my_row < n_here;
                 if (__any_sync(0xFFFFFFFFu, mine && l > 0.f && (bf16x2_nonfinite(probe) ||
                                                                *reinterpret_cast<volatile int *>(&sh->bad[slot]) != 0)))
                     put_seen_nonfinite(k.a, it.j, it.seq0, row0 + 32 * quarter / g, row0 + my_row, mine && l > 0.f, out);
+            } else if (lane == 0) {
+                mbar_arrive(&sh->o_free[t]);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->o_free[t]);
         }
         if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
     }
