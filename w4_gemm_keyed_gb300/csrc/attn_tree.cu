@@ -430,7 +430,8 @@ __device__ void expand_tiles(Shared<true> *sh, const bool is_v, uint8_t *tiles_o
 }
 
 // Nodes that see an own entry with non-finite values get them back: they had been left out of the
-// product.  The kernel that adds up the parts then finds such an output (put_seen_nonfinite).  out: a stored result, its quads `step` apart; first .. last: the item's entries in question.
+// product.  The kernel that adds up the parts then finds such an output (put_seen_nonfinite).  out: a
+// stored result, its quads `step` apart; first .. last: the item's entries in question.
 template <bool E4M3>
 __device__ __noinline__ void add_nonfinite(const AttnTreeArgs &a, int b, int j, int key0, int first, int last, float4 *out,
                                            size_t step) {
