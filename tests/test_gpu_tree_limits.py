@@ -270,3 +270,14 @@ def test_a_prompt_past_32_bits_of_elements(tf):
     assert tf.workspace_status(ws) == tf.TF_DEV_OK
     for s in (0, 1, n // 2, n - 2, n - 1):
         assert torch.equal(out[s * each:(s + 1) * each], call(x[s * each:(s + 1) * each].contiguous(), [0, each]))
+
+
+@pytest.mark.parametrize("pos", FAR)
+def test_the_calls_of_one_cache_take_no_position_past_its_entries(tf, pos):
+    cache, ws = tf.KVCache(2, 256), tf.workspace(256)
+    rows = torch.ones((8, 256), dtype=torch.bfloat16, device="cuda")
+    cache.append(rows, rows, dev_pos([pos]), ws=ws)
+    assert tf.workspace_status(ws) == tf.TF_DEV_BAD_POSITION and not cache.k.any() and not cache.v.any()
+    out, ws = torch.full((8, 256), 7.0, device="cuda"), tf.workspace(cache.workspace_bytes(1, 8))
+    cache.attention(rows, 1, dev_pos([pos]), out=out, ws=ws)
+    assert tf.workspace_status(ws) == tf.TF_DEV_BAD_POSITION and (out == 7).all()

@@ -47,7 +47,7 @@ __device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t &hi, uin
 }
 
 __device__ __forceinline__ bool bad_position(long long pos0, int R, int max_len) {
-    return pos0 < 0 || pos0 + R > max_len;
+    return pos0 < 0 || pos0 > (long long)max_len - R;    // no sum with pos0: it may be any int64
 }
 
 // Persistent CTAs over items (KV head j, partition c), j-major; each CTA takes
